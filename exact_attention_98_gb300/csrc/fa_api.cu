@@ -11,6 +11,7 @@
 #include "fa_device.cuh"
 #include "fa_bwd_dq.h"
 #include "fa_kernels.h"
+#include "fa_paged.cuh"
 
 namespace fa {
 
@@ -636,6 +637,192 @@ int fa_bwd_deterministic(const void* q, const void* k, const void* v, const void
                          size_t workspace_bytes, void* stream) {
   return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, H, N, d, scale, causal, workspace,
                   workspace_bytes, stream, true);
+}
+
+size_t fa_paged_block_bytes(int format, int page_size, int d) {
+  if (format != FA_CACHE_BF16 && format != FA_CACHE_FP4) return 0;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return 0;
+  if (d != 64 && d != 128) return 0;
+  return 2 * paged_half_bytes(format == FA_CACHE_FP4, page_size, d);
+}
+
+namespace {
+
+// A row tensor of `heads` heads: its pointer and strides.
+bool row_strides_ok(const void* p, long long row, long long head, int d) {
+  return p && aligned16(p) && row >= 0 && head >= 0 && row % 8 == 0 && head % 8 == 0 &&
+         (head >= d || head == 0);
+}
+
+// Checks a cache descriptor and the ragged batch's tables.  Returns FA_OK or
+// the error; *empty: nothing to do.
+int check_cache(const fa_paged_cache* c, const int* cu_new, int rows, PagedView* view, bool* empty) {
+  *empty = false;
+  if (!c || c->B < 0 || c->Hkv < 0 || rows < 0 || c->num_pages < 0 || c->max_pages < 0)
+    return FA_ERR_INVALID_ARG;
+  if (fa_paged_block_bytes(c->format, c->page_size, c->d) == 0) return FA_ERR_UNSUPPORTED;
+  if (c->B == 0 || c->Hkv == 0 || rows == 0) {
+    *empty = true;
+    return FA_OK;
+  }
+  if (c->num_pages == 0 || c->max_pages == 0) return FA_ERR_INVALID_ARG;
+  if (!c->pages || !c->page_table || !c->seq_lens || !cu_new) return FA_ERR_INVALID_ARG;
+  if (!aligned16(c->pages) || !aligned4(c->page_table) || !aligned4(c->seq_lens) ||
+      !aligned4(cu_new) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
+    return FA_ERR_INVALID_ARG;
+  if (c->format != FA_CACHE_FP4 && (c->k_scale || c->v_scale)) return FA_ERR_INVALID_ARG;
+  // block indices (times 2, K and V) and positions are ints in the kernels
+  if (2LL * c->num_pages * c->Hkv > 0x7fffffffLL ||
+      static_cast<long long>(c->max_pages) * c->page_size > 0x7fffff00LL)
+    return FA_ERR_UNSUPPORTED;
+  view->pages = static_cast<uint8_t*>(c->pages);
+  view->page_table = c->page_table;
+  view->seq_lens = c->seq_lens;
+  view->k_scale = c->k_scale;
+  view->v_scale = c->v_scale;
+  view->B = c->B;
+  view->Hkv = c->Hkv;
+  view->num_pages = c->num_pages;
+  view->page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  view->max_pages = c->max_pages;
+  return FA_OK;
+}
+
+}  // namespace
+
+int fa_paged_append(const fa_paged_cache* cache, const void* k, long long k_row, long long k_head,
+                    const void* v, long long v_row, long long v_head, const int* cu_new, int rows,
+                    const void* q, long long q_row, long long q_head, void* q_out, int H,
+                    const float* rope, int rope_len, int rot, int interleaved, void* stream) {
+  PagedAppendParams p = {};
+  bool empty = false;
+  const int rc = check_cache(cache, cu_new, rows, &p.c, &empty);
+  if (rc != FA_OK) return rc;
+  const int d = cache->d;
+  if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
+  if (rot < 0 || rot > d || rot % 16 != 0 || rope_len < 0) return FA_ERR_INVALID_ARG;
+  if (q && H < 1) return FA_ERR_INVALID_ARG;
+  if (empty) return FA_OK;
+  if (!row_strides_ok(k, k_row, k_head, d) || !row_strides_ok(v, v_row, v_head, d))
+    return FA_ERR_INVALID_ARG;
+  if (q && (!row_strides_ok(q, q_row, q_head, d) || !q_out || !aligned16(q_out)))
+    return FA_ERR_INVALID_ARG;
+  if (rot > 0 && (!rope || !aligned16(rope))) return FA_ERR_INVALID_ARG;
+  if ((q ? H : 0) + 2LL * cache->Hkv > 0x7fffffffLL - 64) return FA_ERR_UNSUPPORTED;
+  p.cu = cu_new;
+  p.rows = rows;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_row = k_row;
+  p.k_head = k_head;
+  p.v_row = v_row;
+  p.v_head = v_head;
+  p.q_row = q_row;
+  p.q_head = q_head;
+  p.H = q ? H : 0;
+  p.rope = rope;
+  p.rope_len = rope_len;
+  p.rot = rot;
+  p.interleaved = interleaved;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return launch_paged_append(p, d, cache->format == FA_CACHE_FP4, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void* k, void* v,
+                  void* stream) {
+  PagedReadParams p = {};
+  bool empty = false;
+  const int rc = check_cache(cache, cu_new, rows, &p.c, &empty);
+  if (rc != FA_OK || empty) return rc;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+  p.cu = cu_new;
+  p.rows = rows;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return launch_paged_read(p, cache->d, cache->format == FA_CACHE_FP4,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// Partial rows of every CTA (two slots of 16 rows each: O, maxima and sums)
+// and the segments' continuations.
+size_t fa_fwd_paged_workspace_bytes(int d) {
+  if (d != 64 && d != 128) return 0;
+  const size_t ctas = static_cast<size_t>(fwd_paged_ctas());
+  return round_up(ctas * 2 * 16 * d * sizeof(float)) + round_up(ctas * 2 * 2 * 16 * sizeof(float)) +
+         round_up(ctas * sizeof(int4));
+}
+
+int fa_fwd_paged(const fa_paged_cache* cache, const void* q, long long q_row, long long q_head,
+                 void* o, float* lse, const int* cu_new, int rows, int max_new, int H, float scale,
+                 int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
+  FwdPagedParams p = {};
+  bool empty = false;
+  const int rc = check_cache(cache, cu_new, rows, &p.c, &empty);
+  if (rc != FA_OK) return rc;
+  if (!(isfinite(scale) && scale > 0.0f)) return FA_ERR_INVALID_ARG;
+  if (H < 0 || window < 0 || sinks < 0 || max_new < 0) return FA_ERR_INVALID_ARG;
+  if (empty || H == 0) return FA_OK;
+  if (H % cache->Hkv != 0 || max_new < 1) return FA_ERR_INVALID_ARG;
+  const int d = cache->d;
+  const bool fp4 = cache->format == FA_CACHE_FP4;
+  if (!row_strides_ok(q, q_row, q_head, d) || !o || !lse || !aligned16(o) || !aligned4(lse))
+    return FA_ERR_INVALID_ARG;
+  const int group = H / cache->Hkv;
+  if (static_cast<long long>(max_new) * group > 0x7fffff00LL) return FA_ERR_UNSUPPORTED;
+  const long long blocks = (static_cast<long long>(max_new) * group + 15) / 16;
+  if (blocks * cache->Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa_fwd_paged_workspace_bytes(d);
+  if (!workspace || workspace_bytes < need ||
+      (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0)
+    return FA_ERR_WORKSPACE;
+  if (need == 0) return FA_ERR_CUDA;
+  const size_t ctas = static_cast<size_t>(fwd_paged_ctas());
+  char* w = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(w);
+  w += round_up(ctas * 2 * 16 * d * sizeof(float));
+  p.part_ml = reinterpret_cast<float*>(w);
+  w += round_up(ctas * 2 * 2 * 16 * sizeof(float));
+  p.info = reinterpret_cast<int4*>(w);
+  if (!fp4) {
+    const int box = cache->page_size < 64 ? cache->page_size : 64;
+    if (!encode_tile_map(&p.tm, cache->pages, cache->page_size, cache->num_pages * cache->Hkv * 2, d,
+                         static_cast<unsigned int>(box)))
+      return FA_ERR_CUDA;
+  }
+  p.cu = cu_new;
+  p.rows = rows;
+  p.max_new = max_new;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_row = q_row;
+  p.q_head = q_head;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.H = H;
+  p.group = group;
+  p.window = window == 0 ? 0x7fffffff : window;
+  p.sinks = sinks;
+  p.scale = scale * 1.4426950408889634f;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 63) / 64 + 1;
+  // an upper bound of the units of work, as far as it matters (the grid)
+  const long long cap = 1LL << 20;
+  long long units = blocks < cap ? blocks * cache->Hkv : cap;
+  units = units < cap ? units * tiles : cap;
+  units = units < cap ? units * cache->B : cap;
+  return launch_fwd_paged(p, d, fp4, units, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 int fa_last_device_status(void* stream) {

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -206,5 +207,79 @@ cudaError_t launch_bwd_dkdv(const BwdParams& p, int d, cudaStream_t stream);
 // kernels leave out of dS).
 cudaError_t launch_bwd_post(const float* dq_acc, void* dq, long long elems, float mul,
                             cudaStream_t stream);
+
+// The paged key/value cache as the kernels see it (fa_paged_cache in fa.h).
+struct PagedView {
+  uint8_t* pages;        // [num_pages, Hkv] blocks (see fa_paged.cuh)
+  const int* page_table;  // [B, max_pages]
+  const int* seq_lens;    // [B]
+  const float* k_scale;   // [Hkv], or null: 1
+  const float* v_scale;
+  int B;
+  int Hkv;
+  int num_pages;
+  int page_shift;  // log2(page_size)
+  int max_pages;
+};
+
+struct PagedAppendParams {
+  PagedView c;
+  const int* cu;  // [B + 1]: rows of sequence b are cu[b] .. cu[b+1]-1
+  int rows;
+  int tokens;  // rows a block of threads takes (set by the launcher)
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* q;  // null: no Q to rotate
+  __nv_bfloat16* q_out;    // [rows, H, d]
+  long long k_row, k_head, v_row, v_head, q_row, q_head;  // strides in elements
+  int H;
+  const float* rope;  // [rope_len, rot]: rot/2 cosines, then rot/2 sines
+  int rope_len;
+  int rot;  // 0: no rotation
+  int interleaved;
+  unsigned int* status;
+};
+
+struct PagedReadParams {
+  PagedView c;
+  const int* cu;
+  int rows;
+  int tokens;
+  __nv_bfloat16* k;  // [rows, Hkv, d]
+  __nv_bfloat16* v;
+  unsigned int* status;
+};
+
+cudaError_t launch_paged_append(PagedAppendParams p, int d, bool fp4, cudaStream_t stream);
+cudaError_t launch_paged_read(PagedReadParams p, int d, bool fp4, cudaStream_t stream);
+
+struct FwdPagedParams {
+  CUtensorMap tm;  // bf16 cache: (d, page_size, num_pages * Hkv * 2), box {64, min(page_size, 64), 1}
+  PagedView c;
+  const int* cu;
+  int rows;
+  int max_new;  // rows of a sequence at most
+  const __nv_bfloat16* q;
+  long long q_row, q_head;
+  __nv_bfloat16* o;  // [rows, H, d]
+  float* lse;        // [rows, H]
+  int H;
+  int group;   // H / Hkv
+  int window;  // INT_MAX: none
+  int sinks;
+  float scale;  // times log2(e): scores enter exp2 in these units
+  // workspace: two partial slots per CTA of 16 rows each, and where CTA c's last segment goes on
+  float* part_o;   // [2 * ctas, 16, d], not normalised
+  float* part_ml;  // [2 * ctas, 2, 16]: row maxima in log2 units, row sums
+  int4* info;      // [ctas]: {parts, sequence, key head * blocks of rows + block, 0}
+  unsigned int* status;
+};
+
+// CTAs of the paged forward on the current device (0 on an error): its
+// workspace has two partial slots for each.
+int fwd_paged_ctas();
+// One launch of the forward and one of the merge of its split segments.
+cudaError_t launch_fwd_paged(const FwdPagedParams& p, int d, bool fp4, long long max_units,
+                             cudaStream_t stream);
 
 }  // namespace fa

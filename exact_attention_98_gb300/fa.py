@@ -11,6 +11,7 @@ this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,6 +36,19 @@ class FAError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
         super().__init__(f"{where} failed: {status_string(code)} ({code})")
+
+
+FA_CACHE_BF16 = 0
+FA_CACHE_FP4 = 1
+
+
+class PagedCache(ctypes.Structure):
+    """fa_paged_cache of include/fa.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int), ("B", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 def _load() -> ctypes.CDLL:
@@ -89,6 +103,19 @@ def _load() -> ctypes.CDLL:
     lib.fa_timing_enable.restype = i
     lib.fa_timing_last_ms.argtypes = [i, ctypes.POINTER(ctypes.c_float)]
     lib.fa_timing_last_ms.restype = i
+    ll = ctypes.c_longlong
+    cache = ctypes.POINTER(PagedCache)
+    lib.fa_paged_block_bytes.argtypes = [i, i, i]
+    lib.fa_paged_block_bytes.restype = sz
+    lib.fa_paged_append.argtypes = [cache, vp, ll, ll, vp, ll, ll, vp, i, vp, ll, ll, vp, i, vp, i, i,
+                                    i, vp]
+    lib.fa_paged_append.restype = i
+    lib.fa_paged_read.argtypes = [cache, vp, i, vp, vp, vp]
+    lib.fa_paged_read.restype = i
+    lib.fa_fwd_paged_workspace_bytes.argtypes = [i]
+    lib.fa_fwd_paged_workspace_bytes.restype = sz
+    lib.fa_fwd_paged.argtypes = [cache, vp, ll, ll, vp, vp, vp, i, i, i, f, i, i, vp, sz, vp]
+    lib.fa_fwd_paged.restype = i
     lib.fa_launch_count.argtypes = []
     lib.fa_launch_count.restype = ctypes.c_ulonglong
     return lib
@@ -290,6 +317,93 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, scale: float, causal: bool
                               _stream(stream)), "fa_bwd_noalloc")
 
 
+def fa_paged_block_bytes(format: int, page_size: int, d: int) -> int:
+    return int(lib.fa_paged_block_bytes(int(format), int(page_size), int(d)))
+
+
+def _check_ints(t, name, shape, device):
+    _check_tensor(t, name, torch.int32, shape, device)
+
+
+def _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale):
+    """The cache's descriptor from its tensors (see paged_append); the
+    tensors have to outlive the call that takes it."""
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda:
+        raise ValueError("pages must be a CUDA tensor")
+    dev = pages.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"pages is on {dev}; the library launches on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    if not pages.is_contiguous():
+        raise ValueError("pages must be contiguous")
+    if pages.dtype == torch.bfloat16:
+        if pages.dim() != 5 or pages.shape[2] != 2 or pages.shape[4] != d:
+            raise ValueError(f"bf16 pages are [num_pages, Hkv, 2, page_size, {d}], got "
+                             f"{tuple(pages.shape)}")
+        fmt, page_size = FA_CACHE_BF16, int(pages.shape[3])
+    elif pages.dtype == torch.uint8:
+        row = d // 2 + d // 16
+        if pages.dim() != 4 or pages.shape[2] != 2 or pages.shape[3] % row != 0:
+            raise ValueError(f"4-bit pages are uint8 [num_pages, Hkv, 2, page_size * {row}], got "
+                             f"{tuple(pages.shape)}")
+        fmt, page_size = FA_CACHE_FP4, int(pages.shape[3]) // row
+    else:
+        raise ValueError(f"pages must be torch.bfloat16 or torch.uint8 (4 bits), got {pages.dtype}")
+    num_pages, Hkv = int(pages.shape[0]), int(pages.shape[1])
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = (int(x) for x in page_table.shape)
+    _check_ints(page_table, "page_table", (B, max_pages), dev)
+    _check_ints(seq_lens, "seq_lens", (B,), dev)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            _check_tensor(t, name, torch.float32, (Hkv,), dev)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return PagedCache(ptr(pages), ptr(page_table), ptr(seq_lens), ptr(k_scale), ptr(v_scale), fmt, B,
+                      Hkv, d, num_pages, page_size, max_pages)
+
+
+def _rows(t, name, heads, d, device, rows=None):
+    """(rows, row stride, head stride) of a bf16 [rows, heads, d] tensor whose
+    rows of d values are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) or (
+            rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"[{'rows' if rows is None else rows}, {'H' if heads is None else heads}, {d}]")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}'s rows of {d} values must be contiguous")
+    return int(t.shape[0]), t.stride(0), t.stride(1)
+
+
+def fa_paged_append(cache: PagedCache, k, k_row, k_head, v, v_row, v_head, cu_new, rows, q, q_row,
+                    q_head, q_out, H, rope, rope_len, rot, interleaved, stream=None) -> None:
+    _check(lib.fa_paged_append(ctypes.byref(cache), _ptr(k), k_row, k_head, _ptr(v), v_row, v_head,
+                               _ptr(cu_new), rows, _ptr(q), q_row, q_head, _ptr(q_out), H, _ptr(rope),
+                               rope_len, rot, int(bool(interleaved)), _stream(stream)),
+           "fa_paged_append")
+
+
+def fa_paged_read(cache: PagedCache, cu_new, rows, k, v, stream=None) -> None:
+    _check(lib.fa_paged_read(ctypes.byref(cache), _ptr(cu_new), rows, _ptr(k), _ptr(v),
+                             _stream(stream)), "fa_paged_read")
+
+
+def fa_fwd_paged_workspace_bytes(d: int) -> int:
+    return int(lib.fa_fwd_paged_workspace_bytes(int(d)))
+
+
+def fa_fwd_paged(cache: PagedCache, q, q_row, q_head, o, lse, cu_new, rows, max_new, H, scale, window,
+                 sinks, workspace, stream=None) -> None:
+    ws_ptr, ws_bytes = _workspace(workspace, q.device)
+    _check(lib.fa_fwd_paged(ctypes.byref(cache), _ptr(q), q_row, q_head, _ptr(o), _ptr(lse),
+                            _ptr(cu_new), rows, max_new, H, float(scale), window, sinks, ws_ptr,
+                            ws_bytes, _stream(stream)), "fa_fwd_paged")
+
+
 def fa_last_device_status(stream=None) -> int:
     return int(lib.fa_last_device_status(_stream(stream)))
 
@@ -391,3 +505,107 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     run = fa_bwd_deterministic if deterministic else fa_bwd_2cta if two_cta else fa_bwd
     run(q, k, v, o, lse, dout, dq, dk, dv, scale, causal, workspace, stream)
     return dq, dk, dv
+
+
+# --- the paged key/value cache -----------------------------------------------------
+
+
+def _allocating_on(stream):
+    """Allocations inside belong to the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def paged_pages(num_pages: int, heads: int, page_size: int, d: int, format: str = "bf16", device="cuda"):
+    """A cache's pages, zeroed: bf16 [num_pages, heads, 2, page_size, d], or for
+    format "fp4" uint8 [num_pages, heads, 2, page_size * (d/2 + d/16)]."""
+    if format not in ("bf16", "fp4"):
+        raise ValueError(f"format must be 'bf16' or 'fp4', got {format!r}")
+    if fa_paged_block_bytes(FA_CACHE_FP4 if format == "fp4" else FA_CACHE_BF16, page_size, d) == 0:
+        raise ValueError("a cache has page_size 16, 32, 64 or 128 and d 64 or 128")
+    if format == "fp4":
+        return torch.zeros((num_pages, heads, 2, page_size * (d // 2 + d // 16)), dtype=torch.uint8,
+                           device=device)
+    return torch.zeros((num_pages, heads, 2, page_size, d), dtype=torch.bfloat16, device=device)
+
+
+def rope_table(length: int, rot: int, base: float = 10000.0, device="cuda"):
+    """fp32 [length, rot]: cos, then sin of position * base^(-2 i / rot), the
+    angles taken in 64 bits."""
+    rate = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    angle = torch.arange(length, dtype=torch.float64)[:, None] * rate
+    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+
+
+def paged_append(k, v, pages, page_table, seq_lens, cu_new, q=None, rope=None, interleaved: bool = False,
+                 k_scale=None, v_scale=None, stream=None):
+    """Appends K and V rows [rows, Hkv, d] (any row and head strides that are
+    multiples of 8) to the cache `pages` (see paged_pages), K rotated by its
+    position with the table `rope` [length, rot] (see rope_table; None: no
+    rotation).  The rows cu_new[b] .. cu_new[b+1]-1 are sequence b's last ones,
+    seq_lens [B] counts them, page_table is [B, max_pages] (all int32).
+    k_scale, v_scale: a 4-bit cache's factors [Hkv] (None: 1).  With q [rows,
+    H, d] returns it rotated, [rows, H, d] contiguous; padding rows of the
+    result are not written."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("expected k [rows, Hkv, d]")
+    d = int(k.shape[2])
+    cache = _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale)
+    dev = pages.device
+    rows, k_row, k_head = _rows(k, "k", cache.Hkv, d, dev)
+    _, v_row, v_head = _rows(v, "v", cache.Hkv, d, dev, rows)
+    _check_ints(cu_new, "cu_new", (cache.B + 1,), dev)
+    H = q_row = q_head = rope_len = rot = 0
+    q_out = None
+    if q is not None:
+        _, q_row, q_head = _rows(q, "q", None, d, dev, rows)
+        H = int(q.shape[1])
+        with _allocating_on(stream):
+            q_out = torch.empty((rows, H, d), dtype=torch.bfloat16, device=dev)
+        if H == 0:
+            q = None
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            raise ValueError("rope must be [length, rot]")
+        rope_len, rot = (int(x) for x in rope.shape)
+        _check_tensor(rope, "rope", torch.float32, (rope_len, rot), dev)
+    fa_paged_append(cache, k, k_row, k_head, v, v_row, v_head, cu_new, rows, q, q_row, q_head,
+                    None if q is None else q_out, H, rope, rope_len, rot, interleaved, stream)
+    return q_out
+
+
+def paged_read(pages, page_table, seq_lens, cu_new, rows: int, d: int, k_scale=None, v_scale=None,
+               stream=None):
+    """The last rows of each sequence (cu_new as in paged_append) out of the
+    cache: (k, v), each bf16 [rows, Hkv, d]; padding rows are not written."""
+    cache = _paged_cache(pages, page_table, seq_lens, int(d), k_scale, v_scale)
+    _check_ints(cu_new, "cu_new", (cache.B + 1,), pages.device)
+    with _allocating_on(stream):
+        k, v = (torch.empty((int(rows), cache.Hkv, int(d)), dtype=torch.bfloat16, device=pages.device)
+                for _ in range(2))
+    fa_paged_read(cache, cu_new, int(rows), k, v, stream)
+    return k, v
+
+
+def paged_forward(q, pages, page_table, seq_lens, cu_new, max_new: int = 1, window: int = 0,
+                  sinks: int = 0, scale: float | None = None, k_scale=None, v_scale=None, workspace=None,
+                  stream=None):
+    """Attention of each sequence's last rows over its cached positions: q
+    [rows, H, d] (H a multiple of the cache's heads; strides as paged_append)
+    -> (o [rows, H, d], lse [rows, H]).  max_new: rows of a sequence at most;
+    window: positions that a row sees, itself included (0: all before it);
+    sinks: first positions that it sees besides."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("expected q [rows, H, d]")
+    H, d = int(q.shape[1]), int(q.shape[2])
+    cache = _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale)
+    dev = pages.device
+    rows, q_row, q_head = _rows(q, "q", H, d, dev)
+    _check_ints(cu_new, "cu_new", (cache.B + 1,), dev)
+    with _allocating_on(stream):
+        o = torch.empty((rows, H, d), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(fa_fwd_paged_workspace_bytes(d), 1), dtype=torch.uint8, device=dev)
+    fa_fwd_paged(cache, q, q_row, q_head, o, lse, cu_new, rows, int(max_new), H,
+                 default_scale(d) if scale is None else scale, int(window), int(sinks), workspace, stream)
+    return o, lse

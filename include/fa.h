@@ -279,14 +279,129 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
                    float scale, int causal, void* stream);
 
 /*
+ * A paged key/value cache.  The cache is an array of num_pages * Hkv blocks;
+ * block (page, head) holds page_size consecutive positions of one key head of
+ * one sequence: their K rows, then their V rows.
+ *   FA_CACHE_BF16: rows of d bf16 values.
+ *   FA_CACHE_FP4 : the K rows' codes (d/2 bytes a row, e2m1, the even element
+ *                  in the low four bits), the K rows' scales (d/16 bytes a
+ *                  row, e4m3, one per 16 consecutive elements), then V's codes
+ *                  and scales.  An element stands for code * scale * g, with
+ *                  g the head's factor (k_scale, v_scale).
+ * Position p of sequence b is in page page_table[b * max_pages + p / page_size],
+ * row p % page_size.  New rows come as a ragged batch: the rows cu_new[b] ..
+ * cu_new[b+1]-1 of the row tensors belong to sequence b and are its last ones,
+ * at the positions seq_lens[b] - (cu_new[b+1] - cu_new[b]) .. seq_lens[b]-1,
+ * so seq_lens counts the new rows.  Rows from cu_new[B] on are padding.
+ *
+ * page_table, seq_lens, cu_new, k_scale and v_scale are read on the device
+ * (a captured graph serves whatever they hold at each replay) and so cannot be
+ * checked by the call.  The kernels check them: a sequence longer than its
+ * pages (or than the rotation's table), a page outside the cache, rows that
+ * do not fit cu_new are skipped, and FA_ERR_INVALID_ARG is recorded in the
+ * device status word.  Pages that one call writes must belong to one position
+ * of one sequence each; pages that are only read may be shared.
+ */
+typedef enum {
+  FA_CACHE_BF16 = 0,
+  FA_CACHE_FP4 = 1
+} fa_cache_format;
+
+typedef struct {
+  void* pages;            /* num_pages * Hkv blocks of fa_paged_block_bytes, 16-byte aligned */
+  const int* page_table;  /* [B, max_pages] */
+  const int* seq_lens;    /* [B] */
+  const float* k_scale;   /* FA_CACHE_FP4: [Hkv], finite and > 0, or NULL = 1; else NULL */
+  const float* v_scale;   /* the same for V */
+  int format;             /* fa_cache_format */
+  int B;                  /* sequences */
+  int Hkv;                /* key/value heads */
+  int d;                  /* 64 or 128 */
+  int num_pages;
+  int page_size;          /* 16, 32, 64 or 128 */
+  int max_pages;          /* pages of a sequence at most */
+} fa_paged_cache;
+
+/* Bytes of one block: a page's K and V rows of one head.  0 for a format,
+ * page size or head dim that the cache does not have. */
+size_t fa_paged_block_bytes(int format, int page_size, int d);
+
+/*
+ * Appends new K and V rows to the cache, rotated by their positions on the
+ * way, and rotates Q rows with them.
+ *   k, v   : in,  bf16, element (row, head, i) at row * x_row + head * x_head + i
+ *            with Hkv heads (strides in elements, multiples of 8: rows as a
+ *            fused projection leaves them need no copy)
+ *   cu_new : in,  int [B + 1]
+ *   rows   : rows of the tensors (cu_new[B] at least)
+ *   q      : in,  as k with H heads, or NULL: no Q
+ *   q_out  : out, bf16 [rows, H, d]; padding rows are left as they were
+ *   rope   : in,  fp32 [rope_len, rot]: row p holds cos of the rot/2 angles of
+ *            position p, then their sines; NULL with rot = 0: no rotation
+ *   rot    : elements of a row that are rotated, a multiple of 16 up to d.
+ *            x'_a = x_a cos - x_b sin, x'_b = x_b cos + x_a sin with (a, b) =
+ *            (i, i + rot/2), or, interleaved = 1, (2i, 2i + 1); in fp32, each
+ *            product and sum rounded
+ * K and Q are rotated, V is not.  bf16 caches take the results rounded once.
+ * 4-bit caches take, with y = x / g in fp32 and per 16 elements, the scale
+ * s = e4m3(max |y| / 6) (at most 448) and the codes e2m1(y / s), to nearest,
+ * ties to even; a scale that rounds to 0 stores zeros, a block with an
+ * infinity or a NaN reads back as NaN.
+ */
+int fa_paged_append(const fa_paged_cache* cache, const void* k, long long k_row, long long k_head,
+                    const void* v, long long v_row, long long v_head, const int* cu_new, int rows,
+                    const void* q, long long q_row, long long q_head, void* q_out, int H,
+                    const float* rope, int rope_len, int rot, int interleaved, void* stream);
+
+/*
+ * Reads the last rows of each sequence out of the cache as bf16 (the rotated
+ * rows that fa_paged_append wrote, 4-bit values rounded once).
+ *   cu_new, rows : as fa_paged_append
+ *   k, v         : out, bf16 [rows, Hkv, d]; a row without a usable place is
+ *                  zeros, padding rows are left as they were
+ */
+int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void* k, void* v,
+                  void* stream);
+
+/*
+ * Attention of each sequence's last rows over its cached positions, its own
+ * included (append first).  The row at position p sees the positions j <= p
+ * with p - j < window, and the positions j < sinks (j <= p):
+ *   O = softmax(scale q K^T) V over these, LSE as fa_fwd.
+ * A row that sees nothing (a sequence of length 0) gets O = 0, LSE = -inf.
+ *   q        : in,  bf16 with H heads, strides as fa_paged_append; query head
+ *              h reads key head h / (H / Hkv)
+ *   o        : out, bf16 [rows, H, d]; lse: out, fp32 [rows, H]; padding rows
+ *              are left as they were
+ *   max_new  : rows of a sequence at most (1 for a decode step); rows beyond
+ *              it are not computed and FA_ERR_INVALID_ARG is recorded
+ *   H        : query heads, a multiple of Hkv
+ *   window   : positions that a row sees, itself included; 0 = all before it
+ *   sinks    : first positions that every row sees besides
+ *   workspace: fa_fwd_paged_workspace_bytes() bytes on the current device,
+ *              256-byte aligned, contents on entry irrelevant
+ * What positions outside every row's sight hold (the rest of a page, too) does
+ * not matter, infinities and NaN included; one that some row of the same call
+ * sees must be finite where another does not see it.
+ * The work does not depend on how lengths are spread over sequences; cached
+ * rows are read once for every 16 (row, query head of the group) pairs, so
+ * long chunks of new rows are served, but prompts better by fa_fwd_window.
+ */
+size_t fa_fwd_paged_workspace_bytes(int d);
+int fa_fwd_paged(const fa_paged_cache* cache, const void* q, long long q_row, long long q_head,
+                 void* o, float* lse, const int* cu_new, int rows, int max_new, int H, float scale,
+                 int window, int sinks, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word:
  * FA_OK, or FA_ERR_TIMEOUT when a kernel gave up on a bounded wait since the
- * last call, or FA_ERR_CUDA when the synchronisation itself failed.
+ * last call, or FA_ERR_INVALID_ARG when a kernel of the paged cache met tables
+ * that it could not follow, or FA_ERR_CUDA when the synchronisation itself failed.
  */
 int fa_last_device_status(void* stream);
 
 /* Extra detail about the last device status: the code of the wait site that
- * timed out (0 if none).  Valid after fa_last_device_status(). */
+ * timed out or of the check that failed (0 if none).  Valid after fa_last_device_status(). */
 int fa_last_device_site(void);
 
 /* Human-readable name of a fa_status value (static string). */
@@ -332,7 +447,9 @@ int fa_timing_last_ms(int kernel, float* ms);
  * then the merge); fa_bwd three;
  * fa_bwd_deterministic three; fa_fwd_fp8 three (two preparation kernels and
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
- * fa_fwd_2cta one; fa_bwd_2cta three.
+ * fa_fwd_2cta one; fa_bwd_2cta three; fa_paged_append and fa_paged_read one;
+ * fa_fwd_paged two (the forward, then the join of segments that several CTAs
+ * shared).
  */
 unsigned long long fa_launch_count(void);
 
