@@ -191,6 +191,7 @@ int sm_count() {
   return counts[dev];
 }
 
+constexpr int kMaxSinks = 128;  // first tokens of a sliding window: one key tile
 constexpr size_t kWsAlign = 256;
 size_t round_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
@@ -637,6 +638,183 @@ int fa_bwd_deterministic(const void* q, const void* k, const void* v, const void
                          size_t workspace_bytes, void* stream) {
   return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, H, N, d, scale, causal, workspace,
                   workspace_bytes, stream, true);
+}
+
+namespace {
+
+// Shape checks of the sliding-window calls.
+int check_window(int B, int H, int Hkv, int N, int d, float scale, int window, int sinks, bool* empty) {
+  if (Hkv < 0) return FA_ERR_INVALID_ARG;
+  const int rc = check_shape(B, H, N, d, scale, empty);
+  if (rc != FA_OK) return rc;
+  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (sinks > kMaxSinks) return FA_ERR_UNSUPPORTED;
+  if (*empty) return FA_OK;
+  if (Hkv == 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  // key positions plus a window, and the tiles of a group's heads, are ints
+  if (N > (1 << 30) || static_cast<long long>(H / Hkv) * ((N + kBlockM - 1) / kBlockM) > 0x7fffffffLL)
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// How fa_window.cu cuts the queries of a key head: about four CTAs per SM of a
+// 152-SM device in all, a part of 64 rows at least, 256 parts at most (the
+// join reads them all).  Nothing when no query's window leaves a first token.
+struct SinkParts {
+  int slots = 0, slot_rows = 0, sink_rows = 0;
+  size_t bytes = 0;
+};
+SinkParts sink_parts(int B, int Hkv, int N, int d, int window, int sinks) {
+  SinkParts s;
+  if (sinks == 0 || N <= window) return s;
+  const long long heads = static_cast<long long>(B) * Hkv;
+  long long slots = (608 + heads - 1) / heads;
+  if (slots > 256) slots = 256;
+  const int per = static_cast<int>((N + slots - 1) / slots);
+  s.slot_rows = (per + 63) / 64 * 64;
+  s.slots = (N + s.slot_rows - 1) / s.slot_rows;
+  s.sink_rows = (sinks + 15) / 16 * 16;
+  s.bytes = round_up(static_cast<size_t>(s.slots + 1) * heads * 2 * s.sink_rows * d * sizeof(float));
+  return s;
+}
+
+}  // namespace
+
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
+                  int N, int d, float scale, int window, int sinks, void* stream) {
+  bool empty = false;
+  const int rc = check_window(B, H, Hkv, N, d, scale, window, sinks, &empty);
+  if (rc != FA_OK || empty) return rc;
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse))
+    return FA_ERR_INVALID_ARG;
+  FwdParams p = {};
+  const int BH = B * H, group = H / Hkv;
+  if (!encode_tile_map(&p.tm_q, q, N, BH, d) || !encode_tile_map(&p.tm_k, k, N, B * Hkv, d) ||
+      !encode_tile_map(&p.tm_v, v, N, B * Hkv, d) || !encode_tile_map(&p.tm_o, o, N, BH, d))
+    return FA_ERR_CUDA;
+  p.o = o;
+  p.lse = lse;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  p.N = N;
+  p.BH = BH;
+  p.causal = 1;
+  p.c = scale * 1.4426950408889634f;
+  p.ln2 = 0.6931471805599453f;
+  p.num_splits = 1;
+  p.window = window < N ? window : N;
+  p.sinks = sinks < N ? sinks : N;
+  p.win_tiles = group % 2 == 0 ? 1 : 2;
+  p.n_qblk = (N + p.win_tiles * kBlockM - 1) / (p.win_tiles * kBlockM);
+  const int units = p.win_tiles == 1 ? BH / 2 : BH;
+  if (static_cast<long long>(p.n_qblk) * units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  p.n_items = p.n_qblk * units;
+  p.split_from = p.n_items;
+  p.div_bh = FastDiv(static_cast<uint32_t>(units));
+  p.div_qblk = FastDiv(static_cast<uint32_t>(p.n_qblk));
+  p.div_group = FastDiv(static_cast<uint32_t>(group));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = timing_record(0, true, s);
+  if (err == cudaSuccess) err = launch_fwd(p, d, s);
+  if (err == cudaSuccess) err = timing_record(0, false, s);
+  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks) {
+  bool empty = false;
+  if (check_window(B, H, Hkv, N, d, 1.0f, window, sinks, &empty) != FA_OK || empty) return 0;
+  return fa_bwd_workspace_bytes(B, H, N, d) + sink_parts(B, Hkv, N, d, window, sinks).bytes;
+}
+
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                  const void* dout, void* dq, void* dk, void* dv, int B, int H, int Hkv, int N, int d,
+                  float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
+  bool empty = false;
+  const int rc = check_window(B, H, Hkv, N, d, scale, window, sinks, &empty);
+  if (rc != FA_OK || empty) return rc;
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
+      !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_bwd_window_workspace_bytes(B, H, Hkv, N, d, window, sinks);
+  if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0) return FA_ERR_WORKSPACE;
+
+  const int BH = B * H, BHkv = B * Hkv;
+  const long long rows = static_cast<long long>(BH) * N;
+  const SinkParts sp = sink_parts(B, Hkv, N, d, window, sinks);
+  char* w = static_cast<char*>(workspace);
+  float* dsum = reinterpret_cast<float*>(w);
+  float* dq_acc = reinterpret_cast<float*>(w + round_up(static_cast<size_t>(rows) * sizeof(float)));
+  float* sink_part = reinterpret_cast<float*>(w + fa_bwd_workspace_bytes(B, H, N, d));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  BwdParams p = {};
+  if (!encode_tile_map(&p.tm_q, q, N, BH, d) || !encode_tile_map(&p.tm_k, k, N, BHkv, d) ||
+      !encode_tile_map(&p.tm_v, v, N, BHkv, d) || !encode_tile_map(&p.tm_do, dout, N, BH, d) ||
+      !encode_tile_map(&p.tm_dk, dk, N, BHkv, d) || !encode_tile_map(&p.tm_dv, dv, N, BHkv, d) ||
+      !encode_dq_map(&p.tm_dq, dq_acc, N, BH, d))
+    return FA_ERR_CUDA;
+  p.lse = lse;
+  p.dsum = dsum;
+  p.dq_acc = dq_acc;
+  p.dk = dk;
+  p.dv = dv;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  p.N = N;
+  p.BH = BHkv;
+  p.n_kblk = (N + kBlockN - 1) / kBlockN;
+  p.causal = 1;
+  p.c = scale * 1.4426950408889634f;
+  p.scale = scale;
+  p.inv_scale = 1.0f / scale;
+  p.log2e = 1.4426950408889634f;
+  p.window = window < N ? window : N;
+  p.group = H / Hkv;
+  p.sinks = sinks < N ? sinks : N;
+  p.sink_rows = sp.sink_rows;
+  p.sink_main = nullptr;
+  if (static_cast<long long>(p.n_kblk) * BHkv > 0x7fffffffLL ||
+      static_cast<long long>(BHkv) * (2 * kMaxSinks) > 0x7fffffffLL)
+    return FA_ERR_UNSUPPORTED;
+
+  WindowParams wp = {};
+  if (sp.slots > 0) {
+    wp.q = static_cast<const __nv_bfloat16*>(q);
+    wp.k = static_cast<const __nv_bfloat16*>(k);
+    wp.v = static_cast<const __nv_bfloat16*>(v);
+    wp.o = static_cast<const __nv_bfloat16*>(o);
+    wp.dout = static_cast<const __nv_bfloat16*>(dout);
+    wp.lse = lse;
+    wp.dsum = dsum;
+    wp.dq_acc = dq_acc;
+    wp.sink_part = sink_part;
+    wp.dk = static_cast<__nv_bfloat16*>(dk);
+    wp.dv = static_cast<__nv_bfloat16*>(dv);
+    wp.N = N;
+    wp.BHkv = BHkv;
+    wp.group = p.group;
+    wp.window = p.window;
+    wp.sinks = p.sinks;
+    wp.sink_rows = sp.sink_rows;
+    wp.slots = sp.slots;
+    wp.slot_rows = sp.slot_rows;
+    wp.c = p.c;
+    wp.log2e = p.log2e;
+    wp.scale = scale;
+    p.sink_main = sink_part + static_cast<size_t>(sp.slots) * BHkv * 2 * sp.sink_rows * d;
+    if (launch_window_pre(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
+  } else if (launch_bwd_pre(o, dout, dsum, dq_acc, rows, d, s) != cudaSuccess) {
+    return FA_ERR_CUDA;
+  }
+  if (timing_record(1, true, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_bwd_window(p, d, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (timing_record(1, false, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (sp.slots > 0 && launch_window_join(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_bwd_post(dq_acc, dq, rows * d, scale, s) != cudaSuccess) return FA_ERR_CUDA;
+  return FA_OK;
 }
 
 size_t fa_paged_block_bytes(int format, int page_size, int d) {

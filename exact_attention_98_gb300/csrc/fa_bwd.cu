@@ -205,9 +205,30 @@ enum : unsigned int {
   kSiteDSTmem = 0x20C,
 };
 
-// The kernel body; fa_bwd_kernel<D> (all five products) and
-// fa_bwd_dkdv_kernel<D> (dK and dV only) below are its two entry points.
-template <int D, bool kNoDQ>
+// The query tiles of a CTA in the order its roles walk them: tiles i_first.. of
+// the one head; window: of each query head of the group in turn, the tiles
+// i_first..i_last whose windows reach the key tile.
+template <bool kWindow>
+struct QueryWalk {
+  int i, bh;
+  int i_first, i_last;
+  __device__ __forceinline__ QueryWalk(int i_first_, int i_last_, int bh0)
+      : i(i_first_), bh(bh0), i_first(i_first_), i_last(i_last_) {}
+  __device__ __forceinline__ void next() {
+    ++i;
+    if constexpr (kWindow)
+      if (i > i_last) {
+        i = i_first;
+        ++bh;
+      }
+  }
+};
+
+// The kernel body; fa_bwd_kernel<D> (all five products), fa_bwd_dkdv_kernel<D>
+// (dK and dV only) and fa_bwd_window_kernel<D> below are its entry points.
+// kWindow: a row sees the `window` keys up to itself, and the query heads of a
+// group share a key head, whose dK and dV accumulate over them.
+template <int D, bool kNoDQ, bool kWindow = false>
 __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   using C = BwdCfg<D, kNoDQ>;
   extern __shared__ uint8_t smem_raw[];
@@ -225,13 +246,18 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   // Work item: key tile kt of head bh, head-major, so that the key tiles of
   // one head run in the same wave and add into the same dQ rows while those
   // are in L2; within a head the heaviest tile (causal: kt = 0) goes first.
+  // Window: bh is the key head, bq0 its group's first query head.
   const int blk = blockIdx.x;
   const int bh = blk / p.n_kblk;
   const int kt = blk % p.n_kblk;
   const int k0 = kt * kBlockN;
   const int n_qtiles = (p.N + kBlockM - 1) / kBlockM;
-  const int i_first = p.causal ? kt : 0;
-  const int n_iter = n_qtiles - i_first;
+  const int i_first = kWindow || p.causal ? kt : 0;
+  // (window <= N <= 2^30, so the sum is an int)
+  const int i_last = kWindow ? min(n_qtiles - 1, (k0 + kBlockN - 2 + p.window) / kBlockM) : n_qtiles - 1;
+  const int n_iter = (kWindow ? p.group : 1) * (i_last - i_first + 1);
+  const int bq0 = kWindow ? bh * p.group : bh;
+  using Walk = QueryWalk<kWindow>;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -283,21 +309,22 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         }
       }
       int issued = 0;
-      for (int it = 0; it < n_iter; ++it) {
+      Walk walk(i_first, i_last, bq0);
+      for (int it = 0; it < n_iter; ++it, walk.next()) {
         const int s = it % C::kStages;
         const int use = it / C::kStages;
         if (use > 0) {
           bool ok = mbar_wait(bar(C::kBarStEmpty + s), (use - 1) & 1, ctl, kSiteStEmpty);
           if (!__all_sync(0xffffffffu, ok)) break;
         }
-        const int q0 = (i_first + it) * kBlockM;
+        const int q0 = walk.i * kBlockM;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(C::kBarStFull + s), 2 * C::kTileBytes);
           for (int h = 0; h < D / 64; ++h) {
             tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_q,
-                        bar(C::kBarStFull + s), h * 64, q0, bh);
+                        bar(C::kBarStFull + s), h * 64, q0, walk.bh);
             tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_do,
-                        bar(C::kBarStFull + s), h * 64, q0, bh);
+                        bar(C::kBarStFull + s), h * 64, q0, walk.bh);
           }
         }
         if constexpr (C::kRowLse) {
@@ -309,7 +336,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           for (int r4 = 0; r4 < 4; ++r4) {
             const int r = r4 * 32 + lane;
             const int q = q0 + r;
-            const size_t gi = static_cast<size_t>(bh) * p.N + q;
+            const size_t gi = static_cast<size_t>(walk.bh) * p.N + q;
             row_l[r] = (q < p.N) ? -p.lse[gi] * p.log2e : -INFINITY;
             row_d[r] = (q < p.N) ? -p.dsum[gi] : 0.0f;
           }
@@ -323,7 +350,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         for (int r4 = 0; r4 < 4; ++r4) {
           const int r = r4 * 32 + lane;
           const int q = q0 + r;
-          const size_t gi = static_cast<size_t>(bh) * p.N + q;
+          const size_t gi = static_cast<size_t>(walk.bh) * p.N + q;
           const float vl = (q < p.N) ? -p.lse[gi] * p.inv_scale : -1.0e4f;
           const float vd = (q < p.N) ? -p.dsum[gi] : 0.0f;
           const int off = (r >> 3) * C::kBiasSbo + (r & 7) * 16;  // K half 0, entries 0 and 1
@@ -472,14 +499,15 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       // floats of one query row per reduction
       const int dcol = quarter * 32 + lane;
       const uint32_t t_dqt = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + C::kColDP;
-      for (int it = 0; it < n_iter; ++it) {
+      Walk walk(i_first, i_last, bq0);
+      for (int it = 0; it < n_iter; ++it, walk.next()) {
         bool ok = mbar_wait(bar(C::kBarDQFull), it & 1, ctl, kSiteDQFull);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const int q0 = (i_first + it) * kBlockM;
+        const int q0 = walk.i * kBlockM;
         const bool det = p.dq_part != nullptr;
         float* acc = det ? p.dq_part + (static_cast<size_t>(kt * p.BH + bh) * p.N + q0) * D + dcol
-                         : p.dq_acc + (static_cast<size_t>(bh) * p.N + q0) * D + dcol;
+                         : p.dq_acc + (static_cast<size_t>(walk.bh) * p.N + q0) * D + dcol;
         uint32_t r[4][32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) tmem_ld32(t_dqt + b * 32, r[b]);
@@ -505,7 +533,8 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         }
       }
     } else {
-    for (int it = 0; it < n_iter; ++it) {
+    Walk walk(i_first, i_last, bq0);
+    for (int it = 0; it < n_iter; ++it, walk.next()) {
       const int s = it % C::kStages;
       bool ok = mbar_wait(bar(C::kBarDQFull), it & 1, ctl, kSiteDQFull);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -549,7 +578,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       fence_proxy_async_smem();
       named_bar_sync(C::kDrainBarrier, kBlockM);
       if (leader) {
-        const int q0 = (i_first + it) * kBlockM;
+        const int q0 = walk.i * kBlockM;
         if (p.dq_part != nullptr) {  // not taken any more (see BwdParams)
 #pragma unroll 1
           for (int ch = 0; ch < C::kDqChunks; ++ch)
@@ -557,7 +586,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         } else {
 #pragma unroll 1
           for (int ch = 0; ch < C::kDqChunks; ++ch)
-            tma_reduce_add_3d(&p.tm_dq, smem_u32(chunk_base(ch)), ch * C::kDqCols, q0, bh);
+            tma_reduce_add_3d(&p.tm_dq, smem_u32(chunk_base(ch)), ch * C::kDqCols, q0, walk.bh);
         }
         bulk_commit();
         bulk_wait_read<0>();  // the TMA has read the staged tile: stage s is free
@@ -578,10 +607,13 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const f32x2 c2 = f2_pack(p.c, p.c);
     bool ok = true;
-    for (int it = 0; it < n_iter; ++it) {
+    Walk walk(i_first, i_last, bq0);
+    for (int it = 0; it < n_iter; ++it, walk.next()) {
       const int s = it % C::kStages;
-      const int i = i_first + it;
-      const bool diag = p.causal && i == kt;
+      const int i = walk.i;
+      // window: also the tiles whose last rows are past some key's window
+      const bool diag = kWindow ? i == kt || (i - kt) * kBlockM + kBlockM - 1 >= p.window
+                                : p.causal && i == kt;
       // S^T_i complete implies Q_i landed: the compute warps read no stage data
       ok = mbar_wait(bar(C::kBarSFull), it & 1, ctl, kSiteSFull);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -623,7 +655,24 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         p0 = ex2_mufu(x0);
         p1 = ex2_mufu(x1);
       };
-      if (diag) {  // uniform: only the diagonal tile pays for the mask
+      if (kWindow && diag) {
+        // the key sees the query columns [lo, lo + window) of the tile
+        const int lo = (kt - i) * kBlockM + kr - wg * 64;
+        const int hi = lo + p.window;
+        auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          const uint32_t seen = below(hi - ch * 32) & ~below(lo - ch * 32);
+#pragma unroll
+          for (int e2 = 0; e2 < 16; ++e2) {
+            float p0, p1;
+            exp_pair(ch, e2, p0, p1);
+            if (!(seen & (1u << (2 * e2)))) p0 = 0.0f;
+            if (!(seen & (2u << (2 * e2)))) p1 = 0.0f;
+            pw[ch * 16 + e2] = pack_bf16x2(p0, p1);
+          }
+        }
+      } else if (diag) {  // uniform: only the diagonal tile pays for the mask
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
@@ -745,6 +794,21 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         tmem_ld32(lane_base + col + h * 64 + 32, r[1]);
         tmem_ld_wait(r[0]);
         reg_fence(r[1]);
+        if constexpr (kWindow) {
+          // The first tokens also get the rows of the queries whose windows
+          // have left them: their sums are joined in fp32 afterwards.
+          if (p.sink_main != nullptr && kt == 0 && kr < p.sinks) {
+            float4* dst = reinterpret_cast<float4*>(
+                p.sink_main +
+                ((static_cast<size_t>(bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D + h * 64);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const uint32_t* x = &r[c >> 3][(c & 7) * 4];
+              dst[c] = make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
+                                   __uint_as_float(x[3]));
+            }
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint32_t* x = &r[c >> 2][(c & 3) * 8];
@@ -790,10 +854,18 @@ __global__ void __launch_bounds__(BwdCfg<D, true>::kThreads, 1)
   bwd_body<D, true>(p);
 }
 
-template <int D, bool kNoDQ = false>
+template <int D>
+__global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
+    fa_bwd_window_kernel(const __grid_constant__ BwdParams p) {
+  bwd_body<D, false, true>(p);
+}
+
+template <int D, bool kNoDQ = false, bool kWindow = false>
 cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
   using C = BwdCfg<D, kNoDQ>;
-  void (*kernel)(BwdParams) = kNoDQ ? fa_bwd_dkdv_kernel<D> : fa_bwd_kernel<D>;
+  void (*kernel)(BwdParams) = kWindow ? fa_bwd_window_kernel<D>
+                              : kNoDQ ? fa_bwd_dkdv_kernel<D>
+                                      : fa_bwd_kernel<D>;
   // The setmaxnreg split assumes the launch allocation; refuse to run a build
   // whose register count differs (an over-committed split would never finish).
   cudaFuncAttributes attr;
@@ -815,6 +887,12 @@ cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
 cudaError_t launch_bwd_main(const BwdParams& p, int d, cudaStream_t stream) {
   if (d == 128) return launch_bwd_d<128>(p, stream);
   if (d == 64) return launch_bwd_d<64>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream) {
+  if (d == 128) return launch_bwd_d<128, false, true>(p, stream);
+  if (d == 64) return launch_bwd_d<64, false, true>(p, stream);
   return cudaErrorInvalidValue;
 }
 

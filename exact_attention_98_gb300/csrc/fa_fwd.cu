@@ -150,6 +150,10 @@ struct FwdItem {
   int nmax;
   int part;        // partial slot ((block - split_from) * num_splits + range), -1: none
   __device__ __forceinline__ int nkv(int t) const { return t ? nkv1 : nkv0; }
+  __device__ __forceinline__ int q_head(int) const { return bh; }
+  __device__ __forceinline__ int q_row(int t) const { return q0 + t * kBlockM; }
+  __device__ __forceinline__ int kv_head() const { return bh; }
+  __device__ __forceinline__ int key_tile(int j) const { return kb + j; }
 };
 
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int w, int n_ktiles) {
@@ -198,6 +202,52 @@ __device__ __forceinline__ FwdItem pair_item(const FwdParams& p, int w, int n_kt
   return it;
 }
 
+// Window work item: two 128-row query tiles that walk one list of key tiles, the
+// first tokens' (tiles 0 .. first-1) and then the window's.  Where the group of
+// query heads that share a key head is even, they are one query tile of two
+// neighbouring heads, whose lists are the same; otherwise two neighbouring
+// tiles of one head, where the later tile also walks (and masks) the tile that
+// only the earlier one's window still reaches.
+struct WinItem {
+  int head0, head1;  // query heads (batch-major) of the two tiles
+  int row0, row1;    // their first rows
+  int kv;            // key head (batch-major)
+  int first;         // tiles of the first tokens
+  int skip;          // window's first tile - first
+  int nkv0, nkv1;    // tiles of the list that each query tile sees (0: no such tile)
+  int nmax;
+  static constexpr int part = -1;
+  __device__ __forceinline__ int nkv(int t) const { return t ? nkv1 : nkv0; }
+  __device__ __forceinline__ int q_head(int t) const { return t ? head1 : head0; }
+  __device__ __forceinline__ int q_row(int t) const { return t ? row1 : row0; }
+  __device__ __forceinline__ int kv_head() const { return kv; }
+  __device__ __forceinline__ int key_tile(int j) const { return j < first ? j : j + skip; }
+};
+
+__device__ __forceinline__ WinItem win_item(const FwdParams& p, int w) {
+  WinItem it;
+  int unit, q0;
+  // the last query blocks first, as for causal problems (they see most)
+  fwd_block(w, 1, p.div_bh, p.div_qblk, unit, q0, p.win_tiles * kBlockM);
+  it.row0 = q0;
+  if (p.win_tiles == 1) {
+    it.head0 = 2 * unit;
+    it.head1 = 2 * unit + 1;
+    it.row1 = q0;
+  } else {
+    it.head0 = it.head1 = unit;
+    it.row1 = q0 + kBlockM;
+  }
+  it.kv = p.div_group.div(it.head0);
+  const int win_tile = max(0, q0 - p.window + 1) / kBlockN;
+  it.first = min((p.sinks + kBlockN - 1) / kBlockN, win_tile);
+  it.skip = win_tile - it.first;
+  it.nkv0 = it.first + q0 / kBlockN - win_tile + 1;
+  it.nkv1 = it.row1 >= p.N ? 0 : it.first + it.row1 / kBlockN - win_tile + 1;
+  it.nmax = max(it.nkv0, it.nkv1);
+  return it;
+}
+
 // The r-th item of this CTA (of this pair): persistent CTAs (pairs) walk the
 // item list in rounds of G = gridDim.x (pairs: gridDim.x / 2), alternating
 // direction (0..G-1, then G-1..0), so that with the heaviest items first
@@ -212,7 +262,8 @@ __device__ __forceinline__ int fwd_item_index(int r) {
 // POLY: of every 8 exponentials of the softmax (a non-edge row tile), those
 // at positions 0 .. POLY-1 are evaluated by the polynomial on the FMA pipe
 // (exp2_poly2 for a pair, exp2_poly for a lone one), the rest by MUFU ex2.
-template <int D, int POLY, bool FP8, bool PAIR = false>
+// WINDOW: sliding window with first tokens and shared key heads (win_item).
+template <int D, int POLY, bool FP8, bool PAIR = false, bool WINDOW = false>
 __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using C = FwdCfg<D, FP8, PAIR>;
@@ -232,6 +283,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
   auto item_of = [&](int wi) {
     if constexpr (PAIR) return pair_item(p, wi, n_ktiles);
+    else if constexpr (WINDOW) return win_item(p, wi);
     else return fwd_item(p, wi, n_ktiles);
   };
 
@@ -341,7 +393,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       for (int round = 0; ok; ++round) {
         const int wi = fwd_item_index(round);
         if (wi >= p.n_items) break;
-        const FwdItem item = fwd_item(p, wi, n_ktiles);
+        const auto item = item_of(wi);
         if (item.nmax == 0) continue;  // a key range past every row's keys
         if (q_items > 0 && !(ok = mbar_wait(bar(C::kBarQEmpty), (q_items - 1) & 1, ctl, kSiteQEmpty)))
           break;
@@ -349,11 +401,11 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
         for (int t = 0; t < 2; ++t) {
           if constexpr (FP8) {
             tma_load_3d(q_smem + t * C::kTileBytes, &p.tm_q, bar(C::kBarQFull), 0,
-                        item.q0 + t * kBlockM, item.bh);
+                        item.q_row(t), item.q_head(t));
           } else {
             for (int h = 0; h < D / 64; ++h)
               tma_load_3d(q_smem + t * C::kTileBytes + h * C::kHalfBytes, &p.tm_q,
-                          bar(C::kBarQFull), h * 64, item.q0 + t * kBlockM, item.bh);
+                          bar(C::kBarQFull), h * 64, item.q_row(t), item.q_head(t));
           }
         }
         items_loaded = ++q_items;
@@ -369,13 +421,13 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
           if constexpr (FP8) {
             // K: [key][d] rows; V^T: [d][key] rows (keys along x)
             if (idx & 1)
-              tma_load_3d(dst, map, bar(C::kBarFull + slot), (item.kb + j) * kBlockN, 0, item.bh);
+              tma_load_3d(dst, map, bar(C::kBarFull + slot), item.key_tile(j) * kBlockN, 0, item.kv_head());
             else
-              tma_load_3d(dst, map, bar(C::kBarFull + slot), 0, (item.kb + j) * kBlockN, item.bh);
+              tma_load_3d(dst, map, bar(C::kBarFull + slot), 0, item.key_tile(j) * kBlockN, item.kv_head());
           } else {
             for (int h = 0; h < D / 64; ++h)
               tma_load_3d(dst + h * C::kHalfBytes, map, bar(C::kBarFull + slot), h * 64,
-                          (item.kb + j) * kBlockN, item.bh);
+                          item.key_tile(j) * kBlockN, item.kv_head());
           }
           issued = gidx + 1;
         }
@@ -495,7 +547,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       for (int round = 0; ok; ++round) {
         const int wi = fwd_item_index<PAIR>(round);
         if (wi >= p.n_items) break;
-        const FwdItem item = item_of(wi);
+        const auto item = item_of(wi);
         if (item.nmax == 0) continue;
         ok = wait(bar(C::kBarQFull), (q_items++) & 1, kSiteQFull);
         if (ok) ok = wait(bar(C::kBarFull + slot_of(base)), parity_of(base), kSiteKFull);
@@ -577,11 +629,26 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       // slot (for the epilogue), kept in a small volatile array (so in local
       // memory, like a spill slot): more live registers in the tile loop
       // below make ptxas spill about 25 others.
-      const FwdItem itm = item_of(wi);
-      volatile int iv[4] = {itm.nkv0, itm.nkv1, itm.kb, (itm.q0 + tile_row0) / kBlockN};
-      if (iv[t] == 0) {
+      // Window: the tile's key tiles, the first tokens' among them, what
+      // separates those from the window's, and the diagonal tile.
+      const auto itm = item_of(wi);
+      volatile int iv[4];
+      if constexpr (WINDOW) {
+        iv[0] = itm.nkv(t);
+        iv[1] = itm.first;
+        iv[2] = itm.skip;
+        iv[3] = itm.q_row(t) / kBlockN;
+      } else {
+        iv[0] = itm.nkv0;
+        iv[1] = itm.nkv1;
+        iv[2] = itm.kb;
+        iv[3] = (itm.q0 + tile_row0) / kBlockN;
+      }
+      if (iv[WINDOW ? 0 : t] == 0) {
+        if constexpr (WINDOW) continue;
         // Split mode: an empty key range still leaves its partial result
         // for the merge (weight exp(-inf) = 0).
+        else {
         const int qp = itm.q0 + tile_row0 + row;
         if (itm.part >= 0 && qp < p.N) {
           const size_t prow = static_cast<size_t>(itm.part) * 2 * kBlockM + t * kBlockM + row;
@@ -591,6 +658,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
           p.lse_part[prow] = -INFINITY;
         }
         continue;
+        }
       }
       if constexpr (FP8) {
         const int qp = itm.q0 + tile_row0 + row;
@@ -603,14 +671,16 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       // row sum of exp2(x - m_used): four f32x2 accumulators (eight partial sums)
       f32x2 l2[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f),
                      f2_pack(0.0f, 0.0f)};
-      for (int j = 0, nk = iv[t]; j < nk; ++j) {
+      for (int j = 0, nk = iv[WINDOW ? 0 : t]; j < nk; ++j) {
         // The key tile and whether it needs a mask, from the small local array
         // before the wait for S, so that the loads' latency hides in it.
-        const int jabs = iv[2] + j;  // key tile index
+        const int jabs = WINDOW ? (j < iv[1] ? j : j + iv[2]) : iv[2] + j;  // key tile index
         // causal: the diagonal tile (pair mode: and the tile after it, which
         // the earlier CTA of the pair masks whole)
-        const bool edge = (p.causal && (PAIR ? jabs >= iv[3] : jabs == iv[3])) ||
-                          (ragged && jabs == n_ktiles - 1);
+        // window: also the tiles that the window of the tile's last row leaves
+        const bool edge = WINDOW ? jabs >= iv[3] || jabs * kBlockN < (iv[3] + 1) * kBlockM - p.window
+                                 : (p.causal && (PAIR ? jabs >= iv[3] : jabs == iv[3])) ||
+                                       (ragged && jabs == n_ktiles - 1);
         ok = mbar_wait(bar(C::kBarSFull + t), phase & 1u, ctl, kSiteSFull);
         phase ^= 1u;
         ok = __all_sync(0xffffffffu, ok);
@@ -625,7 +695,23 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
         reg_fence(r[2]);
         reg_fence(r[3]);
 
-        if (edge) {
+        if (WINDOW && edge) {
+          // the row keeps the columns [lo, lim) of its window and, below lim,
+          // the first tokens
+          const int kbase = jabs * kBlockN;
+          const int lim = iv[3] * kBlockN + row - kbase + 1;
+          const int lo = lim - p.window;
+          const int keep = p.sinks - kbase;
+          auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            const uint32_t seen =
+                below(lim - ch * 32) & (~below(lo - ch * 32) | below(keep - ch * 32));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen & (1u << e))) r[ch][e] = __float_as_uint(-INFINITY);
+          }
+        } else if (edge) {
           // the row keeps its first `lim` columns: keys below N and, causal,
           // not after the query
           const int kbase = jabs * kBlockN;
@@ -687,7 +773,9 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
         // only.  FP8: P * 64 (exp2(x - m_used + 6), so the row sum carries
         // the same factor) -> e4m3, four per column, over the first 32
         // columns of S.
-        const f32x2 negm2 = FP8 ? f2_pack(6.0f - m_used, 6.0f - m_used) : f2_pack(-m_used, -m_used);
+        // Window: a row may have seen no key yet (weights exp2(-inf) = 0).
+        const float m_ref = WINDOW && m_used == -INFINITY ? 0.0f : m_used;
+        const f32x2 negm2 = FP8 ? f2_pack(6.0f - m_used, 6.0f - m_used) : f2_pack(-m_ref, -m_ref);
         if constexpr (FP8) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -768,9 +856,10 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       {
         if (ok) {
           tc_fence_after();
-          const FwdItem item = item_of(wi);
-          const int bh = item.bh;
-          const int qpos = item.q0 + tile_row0 + row;
+          const auto item = item_of(wi);
+          const int bh = item.q_head(t);
+          const int qrow0 = PAIR ? item.q_row(0) + tile_row0 : item.q_row(t);
+          const int qpos = qrow0 + row;
           const int part = item.part;
           const bool in_range = qpos < p.N;
           float inv_l = 1.0f / l;
@@ -801,7 +890,6 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
                                              __uint_as_float(r[ch][2 * e + 1]) * inv_l);
             uint8_t* stage = smem + C::kStageOff + t * C::kStageBytes + row * 128;
             const uint32_t stage_s = sbase + C::kStageOff + t * C::kStageBytes;
-            const int qrow0 = item.q0 + tile_row0;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
               // the buffer's previous bulk store has read it
@@ -902,16 +990,17 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
   }
 }
 
-template <int D, int POLY, bool FP8 = false>
+template <int D, int POLY, bool FP8 = false, bool WINDOW = false>
 cudaError_t launch_fwd_dp(const FwdParams& p, cudaStream_t stream) {
   using C = FwdCfg<D, FP8>;
+  auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW>;
   // The setmaxnreg split assumes the launch allocation; refuse to run a build
   // whose register count differs (an over-committed split would never finish).
   cudaFuncAttributes attr;
-  cudaError_t err = cudaFuncGetAttributes(&attr, fa_fwd_kernel<D, POLY, FP8>);
+  cudaError_t err = cudaFuncGetAttributes(&attr, kernel);
   if (err != cudaSuccess) return err;
   if (attr.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  err = cudaFuncSetAttribute(fa_fwd_kernel<D, POLY, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmemBytes);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM (the kernel holds all of tensor memory),
@@ -921,7 +1010,7 @@ cudaError_t launch_fwd_dp(const FwdParams& p, cudaStream_t stream) {
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (err != cudaSuccess) return err;
   const int blocks = p.n_items < sms ? p.n_items : sms;
-  err = launch_dependent(fa_fwd_kernel<D, POLY, FP8>, dim3(static_cast<unsigned int>(blocks)),
+  err = launch_dependent(kernel, dim3(static_cast<unsigned int>(blocks)),
                          dim3(C::kThreads), C::kSmemBytes, stream, p);
   if (err != cudaSuccess) return err;
   return launched(1);
@@ -979,6 +1068,10 @@ cudaError_t launch_fwd_d(const FwdParams& p, cudaStream_t stream) {
 
 cudaError_t launch_fwd(const FwdParams& p, int d, cudaStream_t stream) {
   if (p.pair) return (d == 128 && !p.fp8) ? launch_fwd_pair(p, stream) : cudaErrorInvalidValue;
+  if (p.window > 0)
+    return d == 128  ? launch_fwd_dp<128, 0, false, true>(p, stream)
+           : d == 64 ? launch_fwd_dp<64, 0, false, true>(p, stream)
+                     : cudaErrorInvalidValue;
   if (p.fp8) return d == 128 ? launch_fwd_dp<128, 0, true>(p, stream) : cudaErrorInvalidValue;
   if (d == 128) return launch_fwd_d<128>(p, stream);
   if (d == 64) return launch_fwd_d<64>(p, stream);

@@ -70,6 +70,16 @@ struct FwdParams {
   // BH, n_qblk and num_splits as multiply-shift divisors for the work-item
   // walk that every role of every CTA repeats per item
   FastDiv div_bh, div_qblk, div_splits;
+  // Sliding window (window > 0; bf16, no split): a row sees the `window` keys up
+  // to itself and the first `sinks` keys.  tm_k and tm_v have B * Hkv slices;
+  // query head h reads key head div_group(h).  A work item is two
+  // query tiles of one head (win_tiles = 2), or one query tile of two heads (1);
+  // n_qblk = ceil(N / (128 win_tiles)), div_bh's divisor the items of one
+  // query block.
+  int window;
+  int sinks;
+  int win_tiles;
+  FastDiv div_group;
 };
 
 // Default share of the forward's exponentials evaluated by the polynomial on
@@ -108,6 +118,45 @@ struct BwdParams {
   float scale;  // applied to dK in the write-out and to dQ in its conversion (dS leaves it out)
   float inv_scale;  // 1 / scale: -LSE / scale is the bias in raw score units
   float log2e;
+  // Sliding window (the window kernel only): a row sees the `window` keys up to
+  // itself (window <= N); `group` query heads share a key head, and K, V, dK,
+  // dV and BH are of the key heads.  With sink_main, the fp32 dV and
+  // (unscaled) dK of the first `sinks` keys go there, [BH, 2 (dK, dV),
+  // sink_rows, d], to be joined with what the first tokens get from
+  // queries whose windows have left them (fa_window.cu).
+  int window;
+  int group;
+  int sinks;
+  int sink_rows;
+  float* sink_main;
+};
+
+// What the sliding-window backward does beside its main kernel (fa_window.cu):
+// D and the start of the dQ accumulator before it, the first tokens' dK and dV
+// after it.
+struct WindowParams {
+  const __nv_bfloat16* q;  // [BHkv * group, N, d]
+  const __nv_bfloat16* k;  // [BHkv, N, d]
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* dout;
+  const float* lse;   // [BHkv * group, N]
+  float* dsum;        // [BHkv * group, N]
+  float* dq_acc;      // [BHkv * group, N, d]
+  float* sink_part;   // [slots + 1, BHkv, 2 (dK, dV), sink_rows, d]; the last slot is the main kernel's
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int N;
+  int BHkv;
+  int group;
+  int window;
+  int sinks;
+  int sink_rows;  // sinks rounded up to 16
+  int slots;      // parts that the rows of a key head's queries are cut into
+  int slot_rows;  // rows of a part, a multiple of 64
+  float c;        // scale * log2(e)
+  float log2e;
+  float scale;
 };
 
 // Backward by CTA pairs (d = 128): a cluster of two CTAs owns two
@@ -200,6 +249,13 @@ cudaError_t launch_bwd_pre(const void* o, const void* dout, float* dsum, float* 
                            long long rows, int d, cudaStream_t stream);
 // Backward main kernel (key/value stationary).
 cudaError_t launch_bwd_main(const BwdParams& p, int d, cudaStream_t stream);
+// The same kernel with a sliding window and shared key heads (p.window, p.group).
+cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream);
+// Before it, where queries see first tokens that their windows have left: D, and
+// those pairs' share of dQ in the accumulator, of dK and dV in sink_part.
+cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream);
+// After it: the first tokens' dK and dV rows from all parts.
+cudaError_t launch_window_join(const WindowParams& p, int d, cudaStream_t stream);
 // The same kernel computing dK and dV only (p.tm_dq, p.dq_acc and p.dq_part
 // unused): the deterministic mode's first pass.
 cudaError_t launch_bwd_dkdv(const BwdParams& p, int d, cudaStream_t stream);

@@ -103,6 +103,12 @@ def _load() -> ctypes.CDLL:
     lib.fa_timing_enable.restype = i
     lib.fa_timing_last_ms.argtypes = [i, ctypes.POINTER(ctypes.c_float)]
     lib.fa_timing_last_ms.restype = i
+    lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp]
+    lib.fa_fwd_window.restype = i
+    lib.fa_bwd_window_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.fa_bwd_window_workspace_bytes.restype = sz
+    lib.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, sz, vp]
+    lib.fa_bwd_window.restype = i
     ll = ctypes.c_longlong
     cache = ctypes.POINTER(PagedCache)
     lib.fa_paged_block_bytes.argtypes = [i, i, i]
@@ -317,6 +323,38 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, scale: float, causal: bool
                               _stream(stream)), "fa_bwd_noalloc")
 
 
+def _check_window(q, q_like, k, kv_like, lse):
+    """As _check_attention, with the key heads' tensors [B, Hkv, N, d]."""
+    B, H, N, d = _check_attention(q, q_like, lse)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("expected k [B, Hkv, N, d]")
+    Hkv = int(k.shape[1])
+    for name, t in kv_like:
+        _check_tensor(t, name, torch.bfloat16, (B, Hkv, N, d), q.device)
+    return B, H, Hkv, N, d
+
+
+def fa_fwd_window(q, k, v, o, lse, scale: float, window: int, sinks: int, stream=None) -> None:
+    B, H, Hkv, N, d = _check_window(q, (("q", q), ("o", o)), k, (("k", k), ("v", v)), lse)
+    _check(lib.fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, N, d,
+                             float(scale), int(window), int(sinks), _stream(stream)), "fa_fwd_window")
+
+
+def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, window: int,
+                                  sinks: int) -> int:
+    return int(lib.fa_bwd_window_workspace_bytes(B, H, Hkv, N, d, window, sinks))
+
+
+def fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, scale: float, window: int, sinks: int, workspace,
+                  stream=None) -> None:
+    B, H, Hkv, N, d = _check_window(q, (("q", q), ("o", o), ("dout", dout), ("dq", dq)), k,
+                                    (("k", k), ("v", v), ("dk", dk), ("dv", dv)), lse)
+    ws_ptr, ws_bytes = _workspace(workspace, q.device)
+    _check(lib.fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq),
+                             _ptr(dk), _ptr(dv), B, H, Hkv, N, d, float(scale), int(window), int(sinks),
+                             ws_ptr, ws_bytes, _stream(stream)), "fa_bwd_window")
+
+
 def fa_paged_block_bytes(format: int, page_size: int, d: int) -> int:
     return int(lib.fa_paged_block_bytes(int(format), int(page_size), int(d)))
 
@@ -507,12 +545,40 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     return dq, dk, dv
 
 
-# --- the paged key/value cache -----------------------------------------------------
-
-
 def _allocating_on(stream):
     """Allocations inside belong to the stream that uses them."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """Causal attention of q [B, H, N, d] over k, v [B, Hkv, N, d] through a
+    sliding window (the `window` keys up to each query, itself included) and
+    the first `sinks` keys; query head h reads key head h / (H / Hkv).  Returns
+    (o, lse)."""
+    B, H, N, d = _shape(q)
+    with _allocating_on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    fa_fwd_window(q, k, v, o, lse, default_scale(d) if scale is None else scale, window, sinks, stream)
+    return o, lse
+
+
+def window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
+                    workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of window_forward; dk and dv [B, Hkv, N, d] are
+    summed over the query heads that share a key head."""
+    B, H, N, d = _shape(q)
+    with _allocating_on(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        if workspace is None:
+            n = fa_bwd_window_workspace_bytes(B, H, int(k.shape[1]), N, d, int(window), int(sinks))
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, default_scale(d) if scale is None else scale, window,
+                  sinks, workspace, stream)
+    return dq, dk, dv
+
+
+# --- the paged key/value cache -----------------------------------------------------
 
 
 def paged_pages(num_pages: int, heads: int, page_size: int, d: int, format: str = "bf16", device="cuda"):

@@ -279,6 +279,39 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
                    float scale, int causal, void* stream);
 
 /*
+ * Causal attention with a sliding window, first tokens that stay visible, and
+ * key/value heads shared by groups of query heads.  Query i sees the keys
+ *   j <= i  with  i - j < window  or  j < sinks,
+ * and query head h reads key head h / (H / Hkv).
+ *   q, o   : bf16 [B, H, N, d]; k, v: bf16 [B, Hkv, N, d]; lse: fp32 [B, H, N]
+ *   Hkv    : key/value heads; H is a multiple of it
+ *   window : keys that a query sees, itself included, at least 1; from N on
+ *            every key before it (plain causal attention, with shared heads)
+ *   sinks  : first keys that every query sees besides, 0 .. 128 (more:
+ *            FA_ERR_UNSUPPORTED)
+ * Otherwise as fa_fwd with causal = 1.  Every element of K and V has to be
+ * finite, also in padding rows of a batch: a masked pair's weight is an exact
+ * 0, and 0 times an infinity or a NaN is not.
+ */
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
+                  int Hkv, int N, int d, float scale, int window, int sinks, void* stream);
+
+/*
+ * Backward of fa_fwd_window, as fa_bwd: dk and dv, bf16 [B, Hkv, N, d], are
+ * summed over the query heads of the group (in fp32, in an order that does not
+ * vary: bit-identical from run to run; dq within the order of its fp32
+ * additions).
+ *   workspace : fa_bwd_window_workspace_bytes() bytes, 256-byte aligned:
+ *               fa_bwd's, then, where queries see first tokens that their
+ *               windows have left, the parts of those tokens' dK and dV
+ */
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks);
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                  const void* dout, void* dq, void* dk, void* dv, int B, int H, int Hkv, int N, int d,
+                  float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/*
  * A paged key/value cache.  The cache is an array of num_pages * Hkv blocks;
  * block (page, head) holds page_size consecutive positions of one key head of
  * one sequence: their K rows, then their V rows.
@@ -447,7 +480,9 @@ int fa_timing_last_ms(int kernel, float* ms);
  * then the merge); fa_bwd three;
  * fa_bwd_deterministic three; fa_fwd_fp8 three (two preparation kernels and
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
- * fa_fwd_2cta one; fa_bwd_2cta three; fa_paged_append and fa_paged_read one;
+ * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three,
+ * or four where queries see first tokens that their windows have left;
+ * fa_paged_append and fa_paged_read one;
  * fa_fwd_paged two (the forward, then the join of segments that several CTAs
  * shared).
  */
