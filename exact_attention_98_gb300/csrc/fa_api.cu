@@ -931,13 +931,13 @@ int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void
              : FA_ERR_CUDA;
 }
 
-// Partial rows of every CTA (two slots of 16 rows each: O, maxima and sums)
-// and the segments' continuations.
+// Partial rows of every worker (two slots of a block's rows each: O, references
+// and sums) and the segments' continuations.
 size_t fa_fwd_paged_workspace_bytes(int d) {
   if (d != 64 && d != 128) return 0;
-  const size_t ctas = static_cast<size_t>(fwd_paged_ctas());
-  return round_up(ctas * 2 * 16 * d * sizeof(float)) + round_up(ctas * 2 * 2 * 16 * sizeof(float)) +
-         round_up(ctas * sizeof(int4));
+  const size_t slots = 2 * static_cast<size_t>(fwd_paged_workers());
+  return round_up(slots * kPagedRows * d * sizeof(float)) + round_up(slots * 2 * kPagedRows * sizeof(float)) +
+         round_up(slots / 2 * sizeof(int4));
 }
 
 int fa_fwd_paged(const fa_paged_cache* cache, const void* q, long long q_row, long long q_head,
@@ -964,17 +964,15 @@ int fa_fwd_paged(const fa_paged_cache* cache, const void* q, long long q_row, lo
       (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0)
     return FA_ERR_WORKSPACE;
   if (need == 0) return FA_ERR_CUDA;
-  const size_t ctas = static_cast<size_t>(fwd_paged_ctas());
+  const size_t slots = 2 * static_cast<size_t>(fwd_paged_workers());
   char* w = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(w);
-  w += round_up(ctas * 2 * 16 * d * sizeof(float));
+  w += round_up(slots * kPagedRows * d * sizeof(float));
   p.part_ml = reinterpret_cast<float*>(w);
-  w += round_up(ctas * 2 * 2 * 16 * sizeof(float));
+  w += round_up(slots * 2 * kPagedRows * sizeof(float));
   p.info = reinterpret_cast<int4*>(w);
   if (!fp4) {
-    const int box = cache->page_size < 64 ? cache->page_size : 64;
-    if (!encode_tile_map(&p.tm, cache->pages, cache->page_size, cache->num_pages * cache->Hkv * 2, d,
-                         static_cast<unsigned int>(box)))
+    if (!encode_tile_map(&p.tm, cache->pages, cache->page_size, cache->num_pages * cache->Hkv * 2, d, 16))
       return FA_ERR_CUDA;
   }
   p.cu = cu_new;
@@ -992,7 +990,7 @@ int fa_fwd_paged(const fa_paged_cache* cache, const void* q, long long q_row, lo
   p.scale = scale * 1.4426950408889634f;
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;
-  const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 63) / 64 + 1;
+  const long long tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 15) / 16 + 1;
   // an upper bound of the units of work, as far as it matters (the grid)
   const long long cap = 1LL << 20;
   long long units = blocks < cap ? blocks * cache->Hkv : cap;

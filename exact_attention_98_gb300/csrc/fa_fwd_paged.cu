@@ -5,31 +5,31 @@
 // these, O = softmax(S) V, LSE = ln sum exp S_j.
 //
 // Bound by HBM: each visible cached row is read once per key head and serves
-// every query head of the group, so the rows of the matrix products are
-// (token, head of the group), 16 of them at a time: products this narrow are
-// far below the tensor cores' rate, and mma.sync (whose operands come from
-// registers, where a 4-bit row is turned into halves anyway) carries them.
+// every query head of the group.  The products are narrow (8 or 16 pairs of a
+// row and a head of the group at a time), far below the tensor cores' rate,
+// and their operands come from registers, where a 4-bit row is turned into
+// halves anyway, so mma.sync carries them, transposed: cached positions (Q K^T)
+// and d (P V) are the products' 16 rows, and the pairs their 8 columns, so that
+// no product is spent on empty rows.
 //
-// Work: a segment is (sequence, key head, block of 16 rows) and a list of
-// 64-position tiles: those of the first tokens, then those of the window.
-// All tiles of all segments are laid out in one line, which the CTAs cut
-// into equal pieces, whatever the lengths of the sequences (read on the
-// device, so that a captured graph serves any lengths).  A CTA that holds
-// the whole of a segment writes its rows; the parts of a segment that
-// several CTAs share go to the workspace (at most two parts per CTA), and a
-// second kernel joins them by their maxima and sums.
-//
-// A CTA: four warps of 16 positions of each tile, each with its own running
-// maxima, sums and accumulators (joined at the end of a segment), and a
-// fifth that copies the tiles' pages into a ring of stages in shared memory:
-// bf16 by tiled TMA with the 128-byte swizzle that ldmatrix reads without
-// conflicts, 4-bit blocks as plain bulk copies, codes and scales together.
+// Work: a segment is (sequence, key head, block of 8 kTiles rows) and a list of
+// units of 32 (bf16: 16) positions: those of the first tokens, then those of
+// the window.  All units of all segments are laid out in one line, which
+// the grid's warps cut into equal pieces, whatever the lengths of the
+// sequences (read on the device, so that a captured graph serves any
+// lengths).  A warp that holds the whole of a segment writes its rows; the
+// parts of a segment that several warps share go to the workspace (at most
+// two parts per warp), and a second kernel joins them by their maxima and
+// sums.  Warps share nothing else: each copies its units' rows into a ring of
+// its own in shared memory, two units ahead of its products, bf16 by tiled TMA
+// with the 128-byte swizzle that ldmatrix reads without conflicts, 4-bit codes
+// and scales as plain bulk copies.
 //
 // 4 bits: codes become halves exactly (e2m1 x e4m3 has six bits), so the only
 // roundings are those of P to fp16 and of the result.  Q is scaled to fp16
 // by a power of two per row.  The products are free to permute d: lane
-// (g, c) of a warp reads of key g the codes [c d/4, (c+1) d/4) in one load,
-// and of the keys 2c, 2c+1 (V) the codes [g d/8, (g+1) d/8).
+// (g, c) of a warp reads of keys g and g + 8 the codes [c D/4, (c+1) D/4) in one
+// load each, and of the keys 2c, 2c+1, 2c+8, 2c+9 (V) the codes [g D/8, (g+1) D/8).
 #include <limits.h>
 
 #include "fa_paged.cuh"
@@ -37,49 +37,48 @@
 namespace fa {
 namespace {
 
-constexpr int kTileKeys = 64;
-constexpr int kRows = 16;         // rows of a segment
-constexpr int kWarps = 4;         // compute warps
-constexpr int kFwdThreads = 160;  // and the one that loads
-constexpr int kCtasPerSm = 2;
-
 enum : unsigned int {
   kSitePagedFull = 0x511,
-  kSitePagedEmpty = 0x512,
 };
 
-// Rows and sums keep a maximum that is at most this much (log2 units) below
-// the true one, so that accumulators are rescaled rarely.  bf16 keeps the
-// dominant weight near 1 (its rounding error reaches O); fp16's spacing is 8
-// times finer and its range holds 2^8 with room below.
+// A running reference may stay this much (log2 units) below the true maximum
+// before the sums and accumulators are rescaled.  bf16 keeps the dominant
+// weight near 1 (its rounding error reaches O); fp16's spacing is 8 times finer
+// and its range holds 2^8 with room below.
 template <bool FP4>
 __device__ constexpr float kSlack = FP4 ? 8.0f : 2.0f;
 
-template <int D, bool FP4>
+template <int D, bool FP4, int TILES>
 struct PagedCfg {
-  static constexpr int kStageBytes = FP4 ? 2 * kTileKeys * (D / 2 + D / 16) : 2 * kTileKeys * D * 2;
-  static constexpr int kStages = FP4 ? (D == 128 ? 8 : 12) : (D == 128 ? 3 : 5);
-  static constexpr int kJoinOff = kStages * kStageBytes;  // [4 warps][16 rows][32] fp32
-  static constexpr int kJoinBytes = kWarps * kRows * 32 * 4;
-  static constexpr int kStatOff = kJoinOff + kJoinBytes;  // [4 warps][2][16]: maxima, sums
-  static constexpr int kBarOff = kStatOff + kWarps * 2 * kRows * 4;
-  static constexpr int kAbortOff = kBarOff + 2 * kStages * 8;
-  static constexpr int kScanOff = kAbortOff + 16;  // long long [8] for the scan
-  static constexpr int kSmemBytes = kScanOff + 8 * 8 + 1024;
-  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
+  static constexpr int kRows = 8 * TILES;            // rows of a block
+  static constexpr int kUnit = FP4 ? 32 : 16;        // positions of a unit
+  static constexpr int kWarps = FP4 && TILES == 2 ? 12 : 8;
+  static constexpr int kCtas = FP4 && TILES == 1 ? 2 : 1;  // per SM
+  static constexpr int kWorkers = kWarps * kCtas;    // warps per SM
+  static constexpr int kStages = 3;
+  static constexpr int kRowBytes = FP4 ? D / 2 + D / 16 : 2 * D;
+  static constexpr int kHalf = kUnit * kRowBytes;    // K rows of a unit
+  static constexpr int kStageBytes = 2 * kHalf;
+  static constexpr int kBarOff = kWarps * kStages * kStageBytes;
+  static constexpr int kStartOff = kBarOff + kWarps * kStages * 8;  // [warps] {sequence, offset}
+  static constexpr int kScanOff = kStartOff + kWarps * 16;
+  static constexpr int kAbortOff = kScanOff + kWarps * 8;
+  static constexpr int kSmemBytes = kAbortOff + 16 + 1024;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
 };
 
 // What a sequence asks for.
 struct Seq {
   int row0, n;      // its rows of q
   int len;          // cached positions
-  int first_tiles;  // tiles of the first tokens
-  int win_tile;     // the window's first tile
-  int tiles;        // units of a segment: its tiles, or 1 without any
-  int loads;        // its tiles
-  int blocks;       // blocks of 16 rows
+  int first;        // units of the first tokens
+  int skip;         // the window's first unit, less `first`
+  int units;        // units of a segment: its loads, or 1 without any
+  int loads;        // units that hold positions
+  int blocks;       // blocks of rows
 };
 
+template <class C>
 __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool report) {
   Seq s;
   const int r0 = p.cu[b], r1 = p.cu[b + 1];
@@ -97,36 +96,38 @@ __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool re
   s.len = max(0, s.len - extra);
   const int p0 = max(0, s.len - s.n);
   const int lo = p.window == INT_MAX ? 0 : max(0, p0 - p.window + 1);
-  const int end = (s.len + kTileKeys - 1) / kTileKeys;
-  s.win_tile = lo / kTileKeys;
-  s.first_tiles = min((min(p.sinks, s.len) + kTileKeys - 1) / kTileKeys, s.win_tile);
-  s.loads = s.n > 0 ? s.first_tiles + end - s.win_tile : 0;
-  s.tiles = max(1, s.loads);
-  s.blocks = (s.n * p.group + kRows - 1) / kRows;
+  const int end = (s.len + C::kUnit - 1) / C::kUnit;
+  const int win = lo / C::kUnit;
+  s.first = min((min(p.sinks, s.len) + C::kUnit - 1) / C::kUnit, win);
+  s.skip = win - s.first;
+  s.loads = s.n > 0 ? end - s.skip : 0;
+  s.units = max(1, s.loads);
+  s.blocks = (s.n * p.group + C::kRows - 1) / C::kRows;
   return s;
 }
 
 __device__ __forceinline__ long long seq_units(const FwdPagedParams& p, const Seq& s) {
-  return static_cast<long long>(s.tiles) * s.blocks * p.c.Hkv;
+  return static_cast<long long>(s.units) * s.blocks * p.c.Hkv;
 }
 
-// A CTA's place in the line of units.
+// A warp's place in the line of units.
 struct Walk {
-  long long left;  // units left to this CTA
-  int b;           // sequence
+  int left;  // units left to this warp
+  int b;     // sequence
+  int seg;   // key head * blocks + block of rows
+  int unit;  // within the segment
   Seq s;
-  int seg;         // key head * blocks + block of rows
-  int tile;        // first unit within the segment
 };
 
 // Moves to the next segment after `done` units of this one.
+template <class C>
 __device__ __forceinline__ void walk_next(const FwdPagedParams& p, Walk& w, int done) {
   w.left -= done;
-  w.tile = 0;
+  w.unit = 0;
   if (++w.seg < w.s.blocks * p.c.Hkv) return;
   w.seg = 0;
   while (w.left > 0 && w.b + 1 < p.c.B) {
-    w.s = paged_seq(p, ++w.b, false);
+    w.s = paged_seq<C>(p, ++w.b, false);
     if (w.s.blocks > 0) return;
   }
 }
@@ -143,19 +144,23 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
+// An 8x8 block of 16-bit values (lane (g, c): row g, columns 2c, 2c + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   if constexpr (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -171,35 +176,103 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-template <int D, bool FP4>
-__global__ void __launch_bounds__(kFwdThreads, kCtasPerSm)
+// This warp's copies: the units of its piece in order, each into the next stage.
+template <int D, bool FP4, int TILES>
+struct Loader {
+  using C = PagedCfg<D, FP4, TILES>;
+  Walk w;
+  int page;    // lane: page number of its place in the batch (below), -1: none
+  int batch0;  // first unit of the batch of page numbers, -1: to be loaded
+  int issued;  // units
+
+  // Page numbers come 32 at a time, one per lane: of 32 units, or where a
+  // unit spans two pages (4 bits, pages of 16) of 16.
+  __device__ __forceinline__ void next(const FwdPagedParams& p, uint32_t ring, uint32_t bars, int lane) {
+    while (w.left > 0 && w.unit >= w.s.loads) {  // a segment's end, or one without positions
+      const int rest = w.s.loads == 0 ? 1 : 0;
+      walk_next<C>(p, w, rest);
+      batch0 = -1;
+    }
+    if (w.left <= 0) return;
+    const bool two = C::kUnit > (1 << p.c.page_shift);
+    const int per = two ? 16 : 32;
+    auto unit_of = [&](int u) { return u < w.s.first ? u : u + w.s.skip; };
+    if (batch0 < 0 || w.unit >= batch0 + per) {
+      batch0 = w.unit;
+      const int u = batch0 + (two ? lane >> 1 : lane);
+      const int key = unit_of(u) * C::kUnit + (two ? (lane & 1) * 16 : 0);
+      page = -1;
+      if (u < w.s.loads && u < w.unit + w.left && key < w.s.len) {
+        page = p.c.page_table[static_cast<size_t>(w.b) * p.c.max_pages + (key >> p.c.page_shift)];
+        if (page < 0 || page >= p.c.num_pages) {
+          record_status(p.status, kStatusInvalid, kSitePagedPage);
+          page = -1;
+        }
+      }
+    }
+    const int stage = issued % C::kStages;
+    const uint32_t dst = ring + stage * C::kStageBytes;
+    const uint32_t bar = bars + 8 * stage;
+    const int key0 = unit_of(w.unit) * C::kUnit;
+    const int in_page = key0 & ((1 << p.c.page_shift) - 1);
+    const int kvh = w.seg / w.s.blocks;
+    // lanes 0-3 (and 4-7 for a second page): K and V, codes and scales or 64 columns each
+    const int sub = two ? (lane >> 2) & 1 : 0;
+    const int from = __shfl_sync(0xffffffffu, page, two ? (w.unit - batch0) * 2 + sub : w.unit - batch0);
+    const int subs = two ? 2 : 1;
+    const unsigned int live = __ballot_sync(0xffffffffu, from >= 0 && lane < 4 * subs);
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * (C::kStageBytes / (4 * subs)));
+    __syncwarp();
+    if (from >= 0 && lane < 4 * subs) {
+      const size_t block = static_cast<size_t>(from) * p.c.Hkv + kvh;
+      const int kv = (lane >> 1) & 1, part = lane & 1;
+      if constexpr (FP4) {
+        const int keys = C::kUnit / subs;
+        const size_t half = paged_half_bytes(true, 1 << p.c.page_shift, D);
+        const uint8_t* src = p.c.pages + (block * 2 + kv) * half;
+        // both parts of a half add up to kHalf / subs bytes
+        if (part == 0)
+          bulk_load(dst + kv * C::kHalf + sub * keys * (D / 2), src + static_cast<size_t>(in_page) * (D / 2),
+                    keys * (D / 2), bar);
+        else
+          bulk_load(dst + kv * C::kHalf + C::kUnit * (D / 2) + sub * keys * (D / 16),
+                    src + (static_cast<size_t>(D / 2) << p.c.page_shift) + in_page * (D / 16), keys * (D / 16), bar);
+      } else if (part < D / 64) {
+        tma_load_3d(dst + kv * C::kHalf + part * (C::kUnit * 128), &p.tm, bar, part * 64, in_page,
+                    static_cast<int>(block * 2 + kv));
+      }
+    }
+    ++issued;
+    ++w.unit;
+    --w.left;
+    if (w.left == 0) return;
+  }
+};
+
+template <int D, bool FP4, int TILES>
+__global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg<D, FP4, TILES>::kCtas)
     fa_fwd_paged_kernel(const __grid_constant__ FwdPagedParams p) {
-  using C = PagedCfg<D, FP4>;
-  constexpr int kSteps = D / 16;    // k16 steps of Q K^T
-  constexpr int kNTiles = D / 8;    // n8 tiles of P V
+  using C = PagedCfg<D, FP4, TILES>;
+  constexpr int kSteps = D / 16;  // k16 steps of Q K^T, and m16 tiles of P V
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbortOff);
   const WaitCtl ctl{abort_flag, p.status};
-  auto full = [&](int s) -> uint32_t { return sbase + C::kBarOff + 8u * s; };
-  auto empty = [&](int s) -> uint32_t { return sbase + C::kBarOff + 8u * (C::kStages + s); };
   const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kWarps);
-    }
+    for (int s = 0; s < C::kWarps * C::kStages; ++s) mbar_init(sbase + C::kBarOff + 8 * s, 1);
     fence_mbar_init();
   }
   grid_dependency_wait();
   __syncthreads();
 
-  // ---- this CTA's piece of the line of units
+  // ---- this warp's piece of the line of units
   long long* scan = reinterpret_cast<long long*>(smem + C::kScanOff);
+  long long* start = reinterpret_cast<long long*>(smem + C::kStartOff);
   auto block_scan = [&](long long v, long long& total) {  // inclusive, over the CTA's threads
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -210,556 +283,549 @@ __global__ void __launch_bounds__(kFwdThreads, kCtasPerSm)
     if (lane == 31) scan[warp] = v;
     __syncthreads();
     total = 0;
-    for (int w = 0; w < kFwdThreads / 32; ++w) {
+    for (int w = 0; w < C::kWarps; ++w) {
       if (w < warp) v += scan[w];
       total += scan[w];
     }
     return v;
   };
   long long total = 0;
-  for (int b0 = 0; b0 < p.c.B; b0 += kFwdThreads) {
+  for (int b0 = 0; b0 < p.c.B; b0 += 32 * C::kWarps) {
     const int b = b0 + threadIdx.x;
     long long t;
-    block_scan(b < p.c.B ? seq_units(p, paged_seq(p, b, blockIdx.x == 0)) : 0, t);
+    block_scan(b < p.c.B ? seq_units(p, paged_seq<C>(p, b, blockIdx.x == 0)) : 0, t);
     total += t;
   }
-  const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  if (blockIdx.x >= ctas) {
-    if (threadIdx.x == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  auto piece = [&](long long c) { return total / ctas * c + min(c, total % ctas); };
-  const long long u0 = piece(blockIdx.x);
+  // worker i: warp i / grid of CTA i % grid, so that few units spread over the SMs
+  const int grid = static_cast<int>(gridDim.x);
+  const long long workers = min(static_cast<long long>(grid) * C::kWarps, total);
+  const long long quot = total / max(workers, 1LL), rem = total - quot * workers;
+  auto piece = [&](long long i) { return quot * i + min(i, rem); };
+  const long long me = static_cast<long long>(warp) * grid + blockIdx.x;
   long long before = 0;
-  for (int b0 = 0; b0 < p.c.B; b0 += kFwdThreads) {
+  for (int b0 = 0; b0 < p.c.B; b0 += 32 * C::kWarps) {
     const int b = b0 + threadIdx.x;
-    const long long mine = b < p.c.B ? seq_units(p, paged_seq(p, b, false)) : 0;
+    const long long mine = b < p.c.B ? seq_units(p, paged_seq<C>(p, b, false)) : 0;
     long long t;
     const long long end = before + block_scan(mine, t);
-    if (u0 < end && u0 >= end - mine) {
-      scan[6] = b;
-      scan[7] = u0 - (end - mine);
+    for (int w = 0; w < C::kWarps; ++w) {
+      const long long i = static_cast<long long>(w) * grid + blockIdx.x;
+      const long long u0 = piece(i);
+      if (i < workers && u0 < end && u0 >= end - mine) {
+        start[2 * w] = b;
+        start[2 * w + 1] = u0 - (end - mine);
+      }
     }
     before += t;
-    if (u0 < before) break;  // the same for every thread
   }
   __syncthreads();
+  if (lane == 0) p.info[me] = make_int4(0, 0, 0, 0);
+  if (me >= workers) return;
   Walk w;
-  w.left = piece(blockIdx.x + 1) - u0;
-  w.b = static_cast<int>(scan[6]);
-  w.s = paged_seq(p, w.b, false);
-  w.seg = static_cast<int>(scan[7] / w.s.tiles);
-  w.tile = static_cast<int>(scan[7] % w.s.tiles);
+  w.left = static_cast<int>(piece(me + 1) - piece(me));
+  w.b = static_cast<int>(start[2 * warp]);
+  w.s = paged_seq<C>(p, w.b, false);
+  w.seg = static_cast<int>(start[2 * warp + 1] / w.s.units);
+  w.unit = static_cast<int>(start[2 * warp + 1] % w.s.units);
 
-  const int sub_keys = min(1 << p.c.page_shift, kTileKeys);  // positions that one copy brings
-  const int sub_shift = min(p.c.page_shift, 6);
-  const int subs = kTileKeys >> sub_shift;  // copies of a tile
+  const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
+  const uint32_t ring_s = sbase + warp * C::kStages * C::kStageBytes;
+  const uint32_t bars = sbase + C::kBarOff + warp * C::kStages * 8;
+  Loader<D, FP4, TILES> load;
+  load.w = w;
+  load.batch0 = -1;
+  load.page = -1;
+  load.issued = 0;
+  for (int i = 0; i < C::kStages; ++i) load.next(p, ring_s, bars, lane);
 
-  if (warp == kWarps) {
-    // ---------------------------------------------------------------- loads
-    int used = 0;
-    bool ok = true;
-    while (w.left > 0 && ok) {
-      const int kvh = w.seg / w.s.blocks;
-      const int t1 = static_cast<int>(min(static_cast<long long>(w.s.tiles), w.tile + w.left));
-      const int n_load = min(t1, w.s.loads);
-      const int* table = p.c.page_table + static_cast<size_t>(w.b) * p.c.max_pages;
-      const int batch = 32 >> (6 - sub_shift);  // tiles whose page numbers one load by the warp brings
-      int ids = -1;  // lane: page of tile (lane / subs) of the batch, part lane % subs
-      for (int i = w.tile; i < n_load; ++i) {
-        const int in_batch = (i - w.tile) % batch;
-        auto tile_of = [&](int u) { return u < w.s.first_tiles ? u : u - w.s.first_tiles + w.s.win_tile; };
-        if (in_batch == 0) {
-          const int u = i + lane / subs;
-          const int key = tile_of(u) * kTileKeys + (lane % subs) * sub_keys;
-          ids = -1;  // behind the sequence: not loaded
-          if (u < n_load && key < w.s.len) {
-            ids = table[key >> p.c.page_shift];
-            if (ids < 0 || ids >= p.c.num_pages) {
-              record_status(p.status, kStatusInvalid, kSitePagedPage);
-              ids = -1;
-            }
-          }
-        }
-        const int stage = used % C::kStages;
-        const int use = used / C::kStages;
-        if (use > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(empty(stage), (use - 1) & 1, ctl, kSitePagedEmpty));
-          if (!ok) break;
-        }
-        const uint32_t dst = sbase + stage * C::kStageBytes;
-        const int tile = tile_of(i);
-        // the page that this lane copies
-        int mine = __shfl_sync(0xffffffffu, ids, in_batch * subs + (lane % subs));
-        if (lane >= subs) mine = -1;
-        const unsigned int live = __ballot_sync(0xffffffffu, mine >= 0);
-        const uint32_t sub_bytes = C::kStageBytes >> (6 - sub_shift);
-        if (lane == 0) mbar_arrive_expect_tx(full(stage), __popc(live) * sub_bytes);
-        __syncwarp();
-        if (mine >= 0) {
-          const size_t block = static_cast<size_t>(mine) * p.c.Hkv + kvh;
-          // 128-position pages: the tile is one half of the page
-          const int in_page = p.c.page_shift > 6 ? (tile * kTileKeys) & ((1 << p.c.page_shift) - 1) : 0;
-          if constexpr (FP4) {
-            const size_t half = paged_half_bytes(true, 1 << p.c.page_shift, D);
-            const uint8_t* from = p.c.pages + block * 2 * half;
-            const uint32_t to = dst + lane * sub_bytes;
-            if (p.c.page_shift <= 6) {
-              bulk_load(to, from, sub_bytes, full(stage));
-            } else {
-#pragma unroll
-              for (int kv = 0; kv < 2; ++kv) {
-                const uint8_t* f = from + kv * half;
-                const uint32_t t = to + kv * (sub_bytes / 2);
-                bulk_load(t, f + static_cast<size_t>(in_page) * (D / 2), kTileKeys * (D / 2), full(stage));
-                bulk_load(t + kTileKeys * (D / 2),
-                          f + (static_cast<size_t>(D / 2) << p.c.page_shift) + in_page * (D / 16),
-                          kTileKeys * (D / 16), full(stage));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tma_load_3d(dst + (kv * (D / 64) + h) * (kTileKeys * 128) + lane * sub_keys * 128, &p.tm,
-                            full(stage), h * 64, in_page, static_cast<int>(block * 2 + kv));
-          }
-        }
-        __syncwarp();
-        ++used;
-      }
-      walk_next(p, w, t1 - w.tile);
-    }
-    // every copy lands before shared memory is released (waits only on the
-    // give-up path)
-    if (!ok)
-      for (int u = max(0, used - C::kStages); u < used; ++u)
-        mbar_wait_drain(full(u % C::kStages), (u / C::kStages) & 1);
-    return;
-  }
-
-  // ------------------------------------------------------------------ compute
   const int g = lane >> 2, c = lane & 3;
-  float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
-  float* stat = reinterpret_cast<float*>(smem + C::kStatOff);
   int used = 0;
-  if (threadIdx.x == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
+  bool ok = true;
   while (w.left > 0) {
     const int kvh = w.seg / w.s.blocks;
     const int block = w.seg - kvh * w.s.blocks;
-    const int t1 = static_cast<int>(min(static_cast<long long>(w.s.tiles), w.tile + w.left));
-    const int n_load = min(t1, w.s.loads);
-    // rows g and g + 8 of the block: their token, head and position
-    int row_at[2], pos[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = block * kRows + g + 8 * r;
-      const int tok = row / p.group;
-      const bool in = tok < w.s.n;
-      row_at[r] = in ? tok : -1;
-      pos[r] = in ? w.s.len - w.s.n + tok : -1;
-    }
-    const int last_row = min(w.s.n * p.group, (block + 1) * kRows) - 1;
-    const int p_lo = w.s.len - w.s.n + (block * kRows) / p.group;  // the rows' positions: least and most
-    const int p_hi = w.s.len - w.s.n + last_row / p.group;
+    const int u1 = min(w.s.units, w.unit + w.left);
+    const int n_load = min(u1, w.s.loads);
+    const int n_pairs = w.s.n * p.group;
+    const int pair0 = block * C::kRows;
+    const int pos0 = w.s.len - w.s.n;  // position of the first new row
+    // the block's rows' positions, least and most
+    const int p_lo = pos0 + pair0 / p.group;
+    const int p_hi = pos0 + (min(n_pairs, pair0 + C::kRows) - 1) / p.group;
 
-    // Q as the products' A operand
-    uint32_t qa[kSteps][4];
-    float mul[2];
+    // Q as the products' B operand: lane (g, c) holds of pair g the elements
+    // (4 bits) c D/4 + 4 s + {0, 1} and + {2, 3}, (bf16) 16 s + 2c + {0, 1} and + 8
+    uint32_t qb[TILES][kSteps][2];
+    float mul[TILES][2];  // of pairs 2c, 2c + 1, as the scores have them
+    int pos[TILES][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int head = kvh * p.group + (block * kRows + g + 8 * r) % p.group;
-      const __nv_bfloat16* src =
-          p.q + (w.s.row0 + static_cast<long long>(max(row_at[r], 0))) * p.q_row + head * p.q_head;
-      mul[r] = p.scale;
+    for (int t = 0; t < TILES; ++t) {
+      const int pair = pair0 + t * 8 + g;
+      const int tok = pair / p.group;
+      const bool in = pair < n_pairs;
+      const __nv_bfloat16* src = p.q + (w.s.row0 + static_cast<long long>(in ? tok : 0)) * p.q_row +
+                                 (kvh * p.group + (pair - tok * p.group)) * p.q_head;
+      float f = p.scale;
       if constexpr (FP4) {
-        // d = c D/4 + 4 s + {0, 1} (a0) and + {2, 3} (a2)
         uint4 raw[D / 32];
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (row_at[r] >= 0) raw[i] = *reinterpret_cast<const uint4*>(src + c * (D / 4) + 8 * i);
+          if (in) raw[i] = *reinterpret_cast<const uint4*>(src + c * (D / 4) + 8 * i);
           const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[e] << 16)),
-                                     fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // a power of two brings the row's largest magnitude into [1, 2):
-        // down is 2^-e, up its inverse (kept in the normal range)
+        // down is 2^-e, f takes its inverse (both kept in the normal range)
         const int e = min(253, max(1, static_cast<int>((__float_as_uint(amax) >> 23) & 255u)));
         const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        mul[r] *= __uint_as_float(static_cast<uint32_t>(e) << 23);
-        if (p.c.k_scale) mul[r] *= p.c.k_scale[kvh];
+        f *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+        if (p.c.k_scale) f *= p.c.k_scale[kvh];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-          for (int e2 = 0; e2 < 4; ++e2)
-            qa[2 * i + (e2 >> 1)][(e2 & 1) * 2 + r] =
-                pack_f16x2(__uint_as_float(x[e2] << 16) * down, __uint_as_float(x[e2] & 0xFFFF0000u) * down);
+          for (int k = 0; k < 4; ++k)
+            qb[t][2 * i + (k >> 1)][k & 1] =
+                pack_f16x2(__uint_as_float(x[k] << 16) * down, __uint_as_float(x[k] & 0xFFFF0000u) * down);
         }
       } else {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+        for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-          for (int k8 = 0; k8 < 2; ++k8) {
-            uint32_t x = 0u;
-            if (row_at[r] >= 0) x = *reinterpret_cast<const uint32_t*>(src + s * 16 + k8 * 8 + 2 * c);
-            qa[s][k8 * 2 + r] = x;
-          }
+          for (int u = 0; u < 2; ++u)
+            qb[t][k][u] = in ? *reinterpret_cast<const uint32_t*>(src + k * 16 + u * 8 + 2 * c) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mul[t][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + e));
+        const int pr = pair0 + t * 8 + 2 * c + e;
+        pos[t][e] = pr < n_pairs ? pos0 + pr / p.group : -1;
       }
     }
 
-    float acc[kNTiles][4];
+    float acc[TILES][kSteps][4];
+    float ref[TILES][2], lim[TILES][2], l[TILES][2];  // reference (log2 units), how far above it is too far, sums
 #pragma unroll
-    for (int j = 0; j < kNTiles; ++j)
+    for (int t = 0; t < TILES; ++t) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY};  // running maxima, log2 units
-    float l[2] = {0.0f, 0.0f};            // this lane's share of the sums
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][j][e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ref[t][e] = 0.0f;
+        lim[t][e] = -INFINITY;  // nothing seen yet: any score moves the reference
+        l[t][e] = 0.0f;
+      }
+    }
 
-    for (int i = w.tile; i < n_load; ++i, ++used) {
-      const int tile = i < w.s.first_tiles ? i : i - w.s.first_tiles + w.s.win_tile;
-      const int key0 = tile * kTileKeys + warp * 16;  // this warp's 16 positions
+    for (int u = w.unit; u < n_load; ++u, ++used) {
       const int stage = used % C::kStages;
-      mbar_wait(full(stage), (used / C::kStages) & 1, ctl, kSitePagedFull);
-      __syncwarp();
-      const uint8_t* st = smem + stage * C::kStageBytes;
-      const uint32_t st_s = sbase + stage * C::kStageBytes;
+      if (ok) ok = mbar_wait_warp(bars + 8 * stage, (used / C::kStages) & 1, ctl, kSitePagedFull);
+      const int unit_key = (u < w.s.first ? u : u + w.s.skip) * C::kUnit;
+      const uint8_t* st = ring + stage * C::kStageBytes;
+      const uint32_t st_s = ring_s + stage * C::kStageBytes;
       // every position visible to every row?
-      const bool edge = key0 + 15 > p_lo || (static_cast<long long>(key0) <= static_cast<long long>(p_hi) - p.window &&
-                                             key0 + 16 > p.sinks);
-      // 4 bits: the sub-block that holds this warp's positions
-      const int sub = (warp * 16) >> sub_shift;
-      const int in_sub = (warp * 16) & (sub_keys - 1);
-      const uint8_t* kblk = st + sub * (C::kStageBytes >> (6 - sub_shift));
-      const uint8_t* vblk = kblk + (C::kStageBytes >> (7 - sub_shift));
-
-      // S = Q K^T: position key0 + 8 nt + 2c + {0, 1} of rows g (0, 1), g + 8 (2, 3)
-      float s[2][4];
+      const bool edge =
+          unit_key + C::kUnit - 1 > p_lo ||
+          (static_cast<long long>(unit_key) <= static_cast<long long>(p_hi) - p.window && unit_key + C::kUnit > p.sinks);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int grp = 0; grp < C::kUnit / 16; ++grp) {
+        const int key0 = unit_key + grp * 16;
+        // S^T = K Q^T: key key0 + g (0, 1) or + 8 (2, 3) of pairs 2c, 2c + 1
+        float s[TILES][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-      if constexpr (FP4) {
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int key = in_sub + nt * 8 + g;
-          uint32_t codes[D / 32];
-          const uint8_t* kc = kblk + key * (D / 2) + c * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kc);
-            codes[0] = x.x; codes[1] = x.y; codes[2] = x.z; codes[3] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(kc);
-            codes[0] = x.x; codes[1] = x.y;
-          }
-          const uint8_t* ks = kblk + (D / 2) * sub_keys + key * (D / 16) + c * (D / 64);
-          uint32_t sc[D / 64];  // the scales of this lane's 16-element blocks, twice each
+          for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
+        if constexpr (FP4) {
+          uint32_t codes[2][D / 32];
+          uint32_t sc[2][D / 64];  // the scales of this lane's blocks of 16, twice each
 #pragma unroll
-          for (int k = 0; k < D / 64; ++k) sc[k] = e4m3x2_to_f16x2(ks[k] * 0x101u);
-#pragma unroll
-          for (int wd = 0; wd < D / 32; ++wd) {
-            uint32_t h[4];
-            e2m1x8_to_f16x2(codes[wd], h);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = hmul2(h[k], sc[wd >> 1]);
-            mma16816<true>(s[nt], qa[2 * wd], h[0], h[1]);
-            mma16816<true>(s[nt], qa[2 * wd + 1], h[2], h[3]);
-          }
-        }
-      } else {
-        // lanes 0-7, 8-15: keys 0-7, both halves of 16 elements; 16-31: keys 8-15
-        const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-        const int hi = (lane >> 3) & 1;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t b[4];
-          const int chunk = (k & 3) * 2 + hi;
-          ldmatrix_x4(st_s + (k >> 2) * (kTileKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), b);
-          mma16816<false>(s[0], qa[k], b[0], b[1]);
-          mma16816<false>(s[1], qa[k], b[2], b[3]);
-        }
-      }
-
-      // scaled scores; masked ones -inf
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[nt][e] *= mul[e >> 1];
-          if (edge) {
-            const int j = key0 + nt * 8 + 2 * c + (e & 1);
-            const int q = pos[e >> 1];
-            if (!(j <= q && (static_cast<long long>(q) - j < p.window || j < p.sinks))) s[nt][e] = -INFINITY;
-          }
-        }
-      float mx[2], ref[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-      }
-      // the reference moves only when it is left behind by more than the slack
-      const bool move0 = mx[0] > m[0] + kSlack<FP4>, move1 = mx[1] > m[1] + kSlack<FP4>;
-      if (__any_sync(0xffffffffu, move0 || move1)) {
-        const float a0 = move0 ? ex2_mufu(m[0] - mx[0]) : 1.0f;
-        const float a1 = move1 ? ex2_mufu(m[1] - mx[1]) : 1.0f;
-        if (move0) m[0] = mx[0];
-        if (move1) m[1] = mx[1];
-        l[0] *= a0;
-        l[1] *= a1;
-#pragma unroll
-        for (int j = 0; j < kNTiles; ++j) {
-          acc[j][0] *= a0;
-          acc[j][1] *= a0;
-          acc[j][2] *= a1;
-          acc[j][3] *= a1;
-        }
-      }
-      ref[0] = m[0] == -INFINITY ? 0.0f : m[0];
-      ref[1] = m[1] == -INFINITY ? 0.0f : m[1];
-      uint32_t pa[4];  // P as the A operand: (row g, nt 0), (g + 8, nt 0), (g, nt 1), (g + 8, nt 1)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float x = ex2_mufu(s[nt][2 * r] - ref[r]), y = ex2_mufu(s[nt][2 * r + 1] - ref[r]);
-          l[r] += x + y;
-          pa[nt * 2 + r] = FP4 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-        }
-
-      // O += P V.  A position that no row sees has weight 0, but its row of V
-      // may hold anything (the rest of a page, infinities): it is zeroed.
-      // Bit 2 nt + e: position key0 + 8 nt + 2c + e.
-      unsigned int keep = 15u;
-      if (edge) {
-        keep = 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = key0 + (k >> 1) * 8 + 2 * c + (k & 1);
-          const bool seen = j <= p_hi && (j < p.sinks || static_cast<long long>(p_lo) - j < p.window);
-          keep |= seen ? 1u << k : 0u;
-        }
-      }
-      if constexpr (FP4) {
-        // n-tile j of lane g is d = g D/8 + j
-        uint32_t sc[2];  // scales of the keys' pairs
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint8_t* vs = vblk + (D / 2) * sub_keys + (in_sub + nt * 8 + 2 * c) * (D / 16) + (g * D) / 128;
-          const uint32_t lo = (keep >> (2 * nt)) & 1u ? vs[0] : 0u;
-          const uint32_t hi = (keep >> (2 * nt + 1)) & 1u ? vs[D / 16] : 0u;
-          sc[nt] = e4m3x2_to_f16x2(lo | (hi << 8));
-        }
-#pragma unroll
-        for (int wd = 0; wd < D / 64; ++wd) {
-          uint32_t even[2][4], odd[2][4];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const uint8_t* vc = vblk + (in_sub + nt * 8 + 2 * c) * (D / 2) + g * (D / 16) + wd * 4;
-            const uint32_t a = *reinterpret_cast<const uint32_t*>(vc);
-            const uint32_t b = *reinterpret_cast<const uint32_t*>(vc + D / 2);
-            // byte i: element 2i (or 2i+1) of key 2c low, of key 2c+1 high
-            e2m1x8_to_f16x2((a & 0x0F0F0F0Fu) | ((b & 0x0F0F0F0Fu) << 4), even[nt]);
-            e2m1x8_to_f16x2(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd[nt]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              even[nt][k] = hmul2(even[nt][k], sc[nt]);
-              odd[nt][k] = hmul2(odd[nt][k], sc[nt]);
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const int row = grp * 16 + k8 * 8 + g;
+            const uint8_t* kc = st + row * (D / 2) + c * (D / 8);
+            const uint8_t* ks = st + C::kUnit * (D / 2) + row * (D / 16) + c * (D / 64);
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(kc);
+              codes[k8][0] = x.x; codes[k8][1] = x.y; codes[k8][2] = x.z; codes[k8][3] = x.w;
+              const uint32_t two = *reinterpret_cast<const unsigned short*>(ks);
+              const uint32_t h = e4m3x2_to_f16x2(two);
+              sc[k8][0] = __byte_perm(h, 0u, 0x1010);
+              sc[k8][1] = __byte_perm(h, 0u, 0x3232);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(kc);
+              codes[k8][0] = x.x; codes[k8][1] = x.y;
+              sc[k8][0] = e4m3x2_to_f16x2(*ks * 0x101u);
             }
           }
 #pragma unroll
+          for (int wd = 0; wd < D / 32; ++wd) {
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16x2(codes[0][wd], x);
+            e2m1x8_to_f16x2(codes[1][wd], y);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {hmul2(x[2 * k], sc[0][wd >> 1]), hmul2(y[2 * k], sc[1][wd >> 1]),
+                                     hmul2(x[2 * k + 1], sc[0][wd >> 1]), hmul2(y[2 * k + 1], sc[1][wd >> 1])};
+#pragma unroll
+              for (int t = 0; t < TILES; ++t) mma16816<true>(s[t], a, qb[t][2 * wd + k]);
+            }
+          }
+        } else {
+          // lanes 0-15: keys 0-15, the first 8 of 16 elements; 16-31: the other 8
+          const int row = grp * 16 + (lane & 15);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t a[4];
+            const int chunk = (k & 3) * 2 + (lane >> 4);
+            ldmatrix_x4(st_s + (k >> 2) * (C::kUnit * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) mma16816<false>(s[t], a, qb[t][k]);
+          }
+        }
+
+        // scores relative to the references; masked ones -inf
+        bool over = false;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[t][e] = fmaf(s[t][e], mul[t][e & 1], -ref[t][e & 1]);
+            if (edge) {
+              const int j = key0 + g + (e >> 1) * 8;
+              const int q = pos[t][e & 1];
+              if (!(j <= q && (static_cast<long long>(q) - j < p.window || j < p.sinks))) s[t][e] = -INFINITY;
+            }
+          }
+          over = over || fmaxf(s[t][0], s[t][2]) > lim[t][0] || fmaxf(s[t][1], s[t][3]) > lim[t][1];
+        }
+        if (__any_sync(0xffffffffu, over)) {
+          // some reference is too far below: all that are behind move up
+#pragma unroll
+          for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(s[t][e], s[t][e + 2]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              if (mx > lim[t][e]) {
+                const float a = lim[t][e] == -INFINITY ? 0.0f : ex2_mufu(-mx);
+                ref[t][e] += mx;
+                lim[t][e] = kSlack<FP4>;
+                s[t][e] -= mx;
+                s[t][e + 2] -= mx;
+                l[t][e] *= a;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+                  acc[t][j][e] *= a;
+                  acc[t][j][e + 2] *= a;
+                }
+              }
+            }
+        }
+        uint32_t pb[TILES][2];  // P as the B operand: keys 2c, 2c + 1 (and + 8) of pair g
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const float x = ex2_mufu(s[t][2 * k8]), y = ex2_mufu(s[t][2 * k8 + 1]);
+            l[t][0] += x;
+            l[t][1] += y;
+            pb[t][k8] = transpose8x8(FP4 ? pack_f16x2(x, y) : pack_bf16x2(x, y));
+          }
+
+        // O^T += V^T P^T.  A position that no row sees has weight 0, but its
+        // row of V may hold anything (the rest of a page, infinities): it is
+        // zeroed.  Bit k: position key0 + 2c + {0, 1, 8, 9}[k].
+        unsigned int keep = 15u;
+        if (edge) {
+          keep = 0u;
+#pragma unroll
           for (int k = 0; k < 4; ++k) {
-            mma16816<true>(acc[wd * 8 + 2 * k], pa, even[0][k], even[1][k]);
-            mma16816<true>(acc[wd * 8 + 2 * k + 1], pa, odd[0][k], odd[1][k]);
+            const int j = key0 + (k >> 1) * 8 + 2 * c + (k & 1);
+            const bool seen = j <= p_hi && (j < p.sinks || static_cast<long long>(p_lo) - j < p.window);
+            keep |= seen ? 1u << k : 0u;
           }
         }
-      } else {
-        // lanes 0-7: keys 0-7 of columns 8j..; 8-15: keys 8-15; 16-31: the next 8 columns
-        const int row = warp * 16 + (lane & 15);
-        const int hi = lane >> 4;
-        const uint32_t k01 = ((keep & 1u) ? 0xFFFFu : 0u) | ((keep & 2u) ? 0xFFFF0000u : 0u);
-        const uint32_t k23 = ((keep & 4u) ? 0xFFFFu : 0u) | ((keep & 8u) ? 0xFFFF0000u : 0u);
+        if constexpr (FP4) {
+          // rows g, g + 8 of m-tile j are d = g D/8 + 2j, + 1
+          const uint8_t* vc = st + C::kHalf + (grp * 16 + 2 * c) * (D / 2) + g * (D / 16);
+          const uint8_t* vs = st + C::kHalf + C::kUnit * (D / 2) + (grp * 16 + 2 * c) * (D / 16) + (g * D) / 128;
+          uint32_t sc[2];  // scales of the keys' pairs
 #pragma unroll
-        for (int j = 0; j < kNTiles; j += 2) {
-          uint32_t b[4];
-          const int chunk = (j & 7) + hi;
-          ldmatrix_x4_t(st_s + (D / 64 + (j >> 3)) * (kTileKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), b);
-          if (edge) {
-            b[0] &= k01; b[1] &= k23; b[2] &= k01; b[3] &= k23;
+          for (int k8 = 0; k8 < 2; ++k8) {
+            const uint32_t lo = (keep >> (2 * k8)) & 1u ? vs[k8 * 8 * (D / 16)] : 0u;
+            const uint32_t hi = (keep >> (2 * k8 + 1)) & 1u ? vs[(k8 * 8 + 1) * (D / 16)] : 0u;
+            sc[k8] = e4m3x2_to_f16x2(lo | (hi << 8));
           }
-          mma16816<false>(acc[j], pa, b[0], b[1]);
-          mma16816<false>(acc[j + 1], pa, b[2], b[3]);
+          uint32_t codes[2][2][D / 64];  // [+0, +8][key][word]
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint8_t* at = vc + (k8 * 8 + k) * (D / 2);
+              if constexpr (D == 128) {
+                const uint2 x = *reinterpret_cast<const uint2*>(at);
+                codes[k8][k][0] = x.x;
+                codes[k8][k][1] = x.y;
+              } else {
+                codes[k8][k][0] = *reinterpret_cast<const uint32_t*>(at);
+              }
+            }
+#pragma unroll
+          for (int wd = 0; wd < D / 64; ++wd) {
+            uint32_t even[2][4], odd[2][4];
+#pragma unroll
+            for (int k8 = 0; k8 < 2; ++k8) {
+              const uint32_t a = codes[k8][0][wd], b = codes[k8][1][wd];
+              // byte i: element 2i (or 2i + 1), of the even key low, of the odd key high
+              e2m1x8_to_f16x2((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even[k8]);
+              e2m1x8_to_f16x2(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd[k8]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a[4] = {hmul2(even[0][k], sc[0]), hmul2(odd[0][k], sc[0]), hmul2(even[1][k], sc[1]),
+                                     hmul2(odd[1][k], sc[1])};
+#pragma unroll
+              for (int t = 0; t < TILES; ++t) mma16816<true>(acc[t][wd * 4 + k], a, pb[t]);
+            }
+          }
+        } else {
+          // rows g, g + 8 of m-tile j are d = 16 j + g, + 8: lanes 0-7 keys 0-7 of
+          // columns 16j.., 8-15 the next 8 columns, 16-31 keys 8-15
+          const int row = grp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t k01 = ((keep & 1u) ? 0xFFFFu : 0u) | ((keep & 2u) ? 0xFFFF0000u : 0u);
+          const uint32_t k89 = ((keep & 4u) ? 0xFFFFu : 0u) | ((keep & 8u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) {
+            uint32_t a[4];
+            const int chunk = (j & 3) * 2 + ((lane >> 3) & 1);
+            ldmatrix_x4_t(st_s + C::kHalf + (j >> 2) * (C::kUnit * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+            if (edge) {
+              a[0] &= k01; a[1] &= k01; a[2] &= k89; a[3] &= k89;
+            }
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) mma16816<false>(acc[t][j], a, pb[t]);
+          }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(stage));
+      __syncwarp();  // every lane has read the stage
+      load.next(p, ring_s, bars, lane);
     }
 
-    // ---- the four warps' parts of the rows joined
+    // ---- the segment's rows, or this warp's part of them
+    const bool whole = w.unit == 0 && u1 == w.s.units;
+    const size_t slot = 2 * static_cast<size_t>(me) + (w.unit == 0 ? 1 : 0);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (c == 0) {
-        stat[(warp * 2) * kRows + g + 8 * r] = m[r];
-        stat[(warp * 2 + 1) * kRows + g + 8 * r] = l[r];
-      }
-    }
-    named_bar_sync(1, 32 * kWarps);
-    float weight[2];
+    for (int t = 0; t < TILES; ++t)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = -INFINITY;
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[t][e];
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stat[(k * 2) * kRows + g + 8 * r]);
-      weight[r] = m[r] == -INFINITY ? 0.0f : ex2_mufu(m[r] - top);
-    }
-    // thread: 4 of 32 columns of a row, round by round
-    const int jr = threadIdx.x >> 3, jc = threadIdx.x & 7;
-    float top = -INFINITY, sum = 0.0f;
+        for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float top = lim[t][e] == -INFINITY ? -INFINITY : ref[t][e];
+        const int r = t * 8 + 2 * c + e;
+        if (!whole) {
+          float* out = p.part_o + (slot * C::kRows + r) * D;
+          if constexpr (FP4) {
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stat[(k * 2) * kRows + jr]);
+            for (int j = 0; j < kSteps; j += 2)
+              *reinterpret_cast<float4*>(out + g * (D / 8) + 2 * j) =
+                  make_float4(acc[t][j][e], acc[t][j][e + 2], acc[t][j + 1][e], acc[t][j + 1][e + 2]);
+          } else {
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const float mk = stat[(k * 2) * kRows + jr];
-      if (mk != -INFINITY) sum += stat[(k * 2 + 1) * kRows + jr] * ex2_mufu(mk - top);
-    }
-    const bool whole = w.tile == 0 && t1 == w.s.tiles;
-    const int out_row = block * kRows + jr;
-    const int tok = out_row / p.group;
-    const bool in = tok < w.s.n;
-    const int head = kvh * p.group + out_row - tok * p.group;
-    const size_t at = (static_cast<size_t>(w.s.row0) + tok) * p.H + head;
-    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.tile == 0 ? 1 : 0);
-    float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    if (FP4 && p.c.v_scale) inv *= p.c.v_scale[kvh];
-#pragma unroll
-    for (int round = 0; round < kNTiles / 4; ++round) {
-      if (round > 0) named_bar_sync(1, 32 * kWarps);
-#pragma unroll
-      for (int j4 = 0; j4 < 4; ++j4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = FP4 ? (2 * c + (e & 1)) * 4 + j4 : j4 * 8 + 2 * c + (e & 1);
-          join[(warp * kRows + g + 8 * (e >> 1)) * 32 + col] = acc[round * 4 + j4][e] * weight[e >> 1];
+            for (int j = 0; j < kSteps; ++j) {
+              out[16 * j + g] = acc[t][j][e];
+              out[16 * j + 8 + g] = acc[t][j][e + 2];
+            }
+          }
+          if (g == 0) {
+            p.part_ml[slot * 2 * C::kRows + r] = top;
+            p.part_ml[slot * 2 * C::kRows + C::kRows + r] = sum;
+          }
+          continue;
         }
-      named_bar_sync(1, 32 * kWarps);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int pair = pair0 + r;
+        if (pair >= n_pairs) continue;
+        const int tok = pair / p.group;
+        const size_t at = (static_cast<size_t>(w.s.row0) + tok) * p.H + kvh * p.group + (pair - tok * p.group);
+        float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (FP4 && p.c.v_scale) inv *= p.c.v_scale[kvh];
+        __nv_bfloat16* out = p.o + at * D;
+        if constexpr (FP4) {
+          uint32_t x[kSteps];
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(join + (k * kRows + jr) * 32 + jc * 4);
-        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+          for (int j = 0; j < kSteps; ++j) x[j] = pack_bf16x2(acc[t][j][e] * inv, acc[t][j][e + 2] * inv);
+#pragma unroll
+          for (int j = 0; j < kSteps; j += 4)
+            *reinterpret_cast<uint4*>(out + g * (D / 8) + 2 * j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) {
+            out[16 * j + g] = __float2bfloat16_rn(acc[t][j][e] * inv);
+            out[16 * j + 8 + g] = __float2bfloat16_rn(acc[t][j][e + 2] * inv);
+          }
+        }
+        if (g == 0) p.lse[at] = sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
       }
-      const int d0 = FP4 ? jc * (D / 8) + round * 4 : round * 32 + jc * 4;
-      if (!whole) {
-        *reinterpret_cast<float4*>(p.part_o + (slot * kRows + jr) * D + d0) = x;
-      } else if (in) {
-        *reinterpret_cast<uint2*>(p.o + at * D + d0) =
-            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-      }
-    }
-    if (jc == 0) {
-      if (!whole) {
-        p.part_ml[slot * 2 * kRows + jr] = top;
-        p.part_ml[slot * 2 * kRows + kRows + jr] = sum;
-      } else if (in) {
-        p.lse[at] = sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
-      }
-    }
-    if (threadIdx.x == 0 && w.tile == 0 && !whole) {
-      // the segment goes on in the CTAs after this one: how many
-      const long long rest = w.s.tiles - t1;
+    if (lane == 0 && w.unit == 0 && !whole) {
+      // the segment goes on in the workers after this one: how many
+      const int rest = w.s.units - u1;
       int parts = 1;
-      for (long long c2 = static_cast<long long>(blockIdx.x) + 1, got = 0; got < rest; ++c2, ++parts)
-        got += piece(c2 + 1) - piece(c2);
-      p.info[blockIdx.x] = make_int4(parts, w.b, w.seg, 0);
+      for (long long i = me + 1, got = 0; got < rest; ++i, ++parts) got += piece(i + 1) - piece(i);
+      p.info[me] = make_int4(parts, w.b, w.seg, 0);
     }
-    named_bar_sync(1, 32 * kWarps);  // stat and join are free again
-    walk_next(p, w, t1 - w.tile);
+    walk_next<C>(p, w, u1 - w.unit);
   }
+  // (every copy has been waited for, but on the give-up path)
+  if (!ok)
+    for (int i = max(0, load.issued - C::kStages); i < load.issued; ++i)
+      mbar_wait_drain(bars + 8 * (i % C::kStages), (i / C::kStages) & 1);
 }
 
-// Joins the parts of the segment that starts in CTA blockIdx.x and goes on in
-// the CTAs after it: the first part is that CTA's second slot, the others the
-// following CTAs' first ones.  A thread takes 4 columns of a row.
-template <int D, bool FP4>
-__global__ void __launch_bounds__(kRows * D / 4)
-    fa_fwd_paged_join_kernel(const __grid_constant__ FwdPagedParams p) {
+// Joins the parts of the segments that start in the workers of this block (8 of
+// them, blockIdx.x) and go on in the workers after them: the first part is that
+// worker's second slot, the others the following workers' first ones.
+// blockIdx.y: 32 columns.  A thread takes 4 columns of a row and every
+// kGroups-th part.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWorkers = 8;
+
+template <int D, bool FP4, int TILES>
+__global__ void __launch_bounds__(kJoinThreads) fa_fwd_paged_join_kernel(const __grid_constant__ FwdPagedParams p,
+                                                                         int workers) {
+  using C = PagedCfg<D, FP4, TILES>;
+  constexpr int kGroups = kJoinThreads / (C::kRows * 8);
+  __shared__ float4 sx[kGroups][C::kRows * 8];
+  __shared__ float2 sml[kGroups][C::kRows * 8];
+  const int at = threadIdx.x % (C::kRows * 8), grp = threadIdx.x / (C::kRows * 8);
+  const int row = at / 8, d0 = blockIdx.y * 32 + (at % 8) * 4;
   grid_dependency_wait();
-  const int4 info = p.info[blockIdx.x];
-  if (info.x == 0) return;
-  const Seq s = paged_seq(p, info.y, false);
-  const int kvh = info.z / s.blocks;
-  const int block = info.z - kvh * s.blocks;
-  const int row = threadIdx.x / (D / 4);
-  const int d0 = (threadIdx.x % (D / 4)) * 4;
-  const int out_row = block * kRows + row;
-  const int tok = out_row / p.group;
-  if (tok >= s.n) return;
-  auto slot = [&](int k) {
-    return 2 * (static_cast<size_t>(blockIdx.x) + k) + (k == 0 ? 1 : 0);
-  };
-  float top = -INFINITY;
-  for (int k = 0; k < info.x; ++k) top = fmaxf(top, p.part_ml[slot(k) * 2 * kRows + row]);
-  float sum = 0.0f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < info.x; ++k) {
-    const float mk = p.part_ml[slot(k) * 2 * kRows + row];
-    const float lk = p.part_ml[slot(k) * 2 * kRows + kRows + row];
-    const float4 y = *reinterpret_cast<const float4*>(p.part_o + (slot(k) * kRows + row) * D + d0);
-    const float wk = mk == -INFINITY ? 0.0f : ex2_mufu(mk - top);
-    sum += lk * wk;
-    x.x += y.x * wk; x.y += y.y * wk; x.z += y.z * wk; x.w += y.w * wk;
+  for (int i = 0; i < kJoinWorkers; ++i) {
+    const int me = blockIdx.x * kJoinWorkers + i;
+    if (me >= workers) return;
+    const int4 info = p.info[me];
+    if (info.x == 0) continue;
+    float m = -INFINITY, l = 0.0f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 4;
+    for (int k0 = grp; k0 < info.x; k0 += kBatch * kGroups) {
+      float mk[kBatch], lk[kBatch];
+      float4 y[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int k = k0 + b * kGroups;
+        mk[b] = -INFINITY;
+        lk[b] = 0.0f;
+        y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < info.x) {
+          const size_t slot = 2 * (static_cast<size_t>(me) + k) + (k == 0 ? 1 : 0);
+          mk[b] = p.part_ml[slot * 2 * C::kRows + row];
+          lk[b] = p.part_ml[slot * 2 * C::kRows + C::kRows + row];
+          y[b] = *reinterpret_cast<const float4*>(p.part_o + (slot * C::kRows + row) * D + d0);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) top = fmaxf(top, mk[b]);
+      // a part that saw nothing has maximum -inf, and sums (0, or what a
+      // NaN score left) that still count
+      const float a = m == -INFINITY ? 1.0f : ex2_mufu(m - top);
+      l *= a;
+      x.x *= a; x.y *= a; x.z *= a; x.w *= a;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float wk = mk[b] == -INFINITY ? 1.0f : ex2_mufu(mk[b] - top);
+        l += lk[b] * wk;
+        x.x += y[b].x * wk; x.y += y[b].y * wk; x.z += y[b].z * wk; x.w += y[b].w * wk;
+      }
+      m = top;
+    }
+    __syncthreads();  // the segment before has been read
+    sx[grp][at] = x;
+    sml[grp][at] = make_float2(m, l);
+    __syncthreads();
+    if (grp != 0) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) top = fmaxf(top, sml[k][at].x);
+    float sum = 0.0f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const float2 ml = sml[k][at];
+      const float4 y = sx[k][at];
+      const float wk = ml.x == -INFINITY ? 1.0f : ex2_mufu(ml.x - top);
+      sum += ml.y * wk;
+      x.x += y.x * wk; x.y += y.y * wk; x.z += y.z * wk; x.w += y.w * wk;
+    }
+    const Seq s = paged_seq<C>(p, info.y, false);
+    const int kvh = info.z / s.blocks;
+    const int pair = (info.z - kvh * s.blocks) * C::kRows + row;
+    const int tok = pair / p.group;
+    if (tok >= s.n) continue;
+    float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (FP4 && p.c.v_scale) inv *= p.c.v_scale[kvh];
+    const size_t to = (static_cast<size_t>(s.row0) + tok) * p.H + kvh * p.group + pair - tok * p.group;
+    *reinterpret_cast<uint2*>(p.o + to * D + d0) =
+        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+    if (d0 == 0) p.lse[to] = sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
   }
-  float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  if (FP4 && p.c.v_scale) inv *= p.c.v_scale[kvh];
-  const size_t at = (static_cast<size_t>(s.row0) + tok) * p.H + kvh * p.group + out_row - tok * p.group;
-  *reinterpret_cast<uint2*>(p.o + at * D + d0) =
-      make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-  if (d0 == 0) p.lse[at] = sum == 0.0f ? -INFINITY : top * 0.6931471805599453f + logf(sum);
 }
 
-template <int D, bool FP4>
-cudaError_t launch_dp(const FwdPagedParams& p, long long max_units, cudaStream_t stream) {
-  using C = PagedCfg<D, FP4>;
-  cudaError_t err = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, FP4>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (err != cudaSuccess) return err;
-  const int ctas = fwd_paged_ctas();
-  if (ctas <= 0) return cudaErrorInvalidConfiguration;
-  const unsigned int grid = static_cast<unsigned int>(max_units < ctas ? max_units : ctas);
-  err = launch_dependent(fa_fwd_paged_kernel<D, FP4>, dim3(grid), dim3(kFwdThreads), C::kSmemBytes, stream, p);
-  if (err != cudaSuccess) return err;
-  err = launched(1);
-  if (err != cudaSuccess) return err;
-  err = launch_dependent(fa_fwd_paged_join_kernel<D, FP4>, dim3(grid), dim3(kRows * D / 4), 0, stream, p);
-  if (err != cudaSuccess) return err;
-  return launched(1);
-}
-
-}  // namespace
-
-int fwd_paged_ctas() {
+int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
-  return sms * kCtasPerSm;
+  return sms;
 }
+
+template <int D, bool FP4, int TILES>
+cudaError_t launch_dp(const FwdPagedParams& p, long long max_units, cudaStream_t stream) {
+  using C = PagedCfg<D, FP4, TILES>;
+  static_assert(C::kWorkers <= kPagedWorkersPerSm && C::kRows <= kPagedRows, "the workspace's shape");
+  cudaError_t err = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, FP4, TILES>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  const int ctas = sm_count() * C::kCtas;
+  if (ctas <= 0) return cudaErrorInvalidConfiguration;
+  const int grid = static_cast<int>(max_units < ctas ? max_units : ctas);
+  err = launch_dependent(fa_fwd_paged_kernel<D, FP4, TILES>, dim3(static_cast<unsigned int>(grid)),
+                         dim3(32 * C::kWarps), C::kSmemBytes, stream, p);
+  if (err != cudaSuccess) return err;
+  err = launched(1);
+  if (err != cudaSuccess) return err;
+  const int workers = grid * C::kWarps;
+  err = launch_dependent(fa_fwd_paged_join_kernel<D, FP4, TILES>,
+                         dim3(static_cast<unsigned int>((workers + kJoinWorkers - 1) / kJoinWorkers), D / 32),
+                         dim3(kJoinThreads), 0, stream, p, workers);
+  if (err != cudaSuccess) return err;
+  return launched(1);
+}
+
+template <int D, bool FP4>
+cudaError_t launch_d(const FwdPagedParams& p, long long max_units, cudaStream_t stream) {
+  // one tile of 8 pairs holds a block where no sequence has more
+  return static_cast<long long>(p.max_new) * p.group <= 8 ? launch_dp<D, FP4, 1>(p, max_units, stream)
+                                                          : launch_dp<D, FP4, 2>(p, max_units, stream);
+}
+
+}  // namespace
+
+int fwd_paged_workers() { return sm_count() * kPagedWorkersPerSm; }
 
 cudaError_t launch_fwd_paged(const FwdPagedParams& p, int d, bool fp4, long long max_units,
                              cudaStream_t stream) {
-  if (d == 128) return fp4 ? launch_dp<128, true>(p, max_units, stream) : launch_dp<128, false>(p, max_units, stream);
-  return fp4 ? launch_dp<64, true>(p, max_units, stream) : launch_dp<64, false>(p, max_units, stream);
+  if (d == 128) return fp4 ? launch_d<128, true>(p, max_units, stream) : launch_d<128, false>(p, max_units, stream);
+  return fp4 ? launch_d<64, true>(p, max_units, stream) : launch_d<64, false>(p, max_units, stream);
 }
 
 }  // namespace fa

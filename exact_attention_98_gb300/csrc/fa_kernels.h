@@ -310,7 +310,7 @@ cudaError_t launch_paged_append(PagedAppendParams p, int d, bool fp4, cudaStream
 cudaError_t launch_paged_read(PagedReadParams p, int d, bool fp4, cudaStream_t stream);
 
 struct FwdPagedParams {
-  CUtensorMap tm;  // bf16 cache: (d, page_size, num_pages * Hkv * 2), box {64, min(page_size, 64), 1}
+  CUtensorMap tm;  // bf16 cache: (d, page_size, num_pages * Hkv * 2), box {64, 16, 1}
   PagedView c;
   const int* cu;
   int rows;
@@ -324,17 +324,20 @@ struct FwdPagedParams {
   int window;  // INT_MAX: none
   int sinks;
   float scale;  // times log2(e): scores enter exp2 in these units
-  // workspace: two partial slots per CTA of 16 rows each, and where CTA c's last segment goes on
-  float* part_o;   // [2 * ctas, 16, d], not normalised
-  float* part_ml;  // [2 * ctas, 2, 16]: row maxima in log2 units, row sums
-  int4* info;      // [ctas]: {parts, sequence, key head * blocks of rows + block, 0}
+  // workspace: two partial slots per worker (a warp) of a block's rows each, and
+  // where worker i's last segment goes on
+  float* part_o;   // [2 * workers, rows of a block, d], not normalised
+  float* part_ml;  // [2 * workers, 2, rows of a block]: references in log2 units, row sums
+  int4* info;      // [workers]: {parts, sequence, key head * blocks of rows + block, 0}
   unsigned int* status;
 };
 
-// CTAs of the paged forward on the current device (0 on an error): its
-// workspace has two partial slots for each.
-int fwd_paged_ctas();
-// One launch of the forward and one of the merge of its split segments.
+// Warps of the paged forward at most, per SM and on the current device (0 on an
+// error), and rows of a block at most: its workspace.
+constexpr int kPagedWorkersPerSm = 16;
+constexpr int kPagedRows = 16;
+int fwd_paged_workers();
+// One launch of the forward and one of the join of its split segments.
 cudaError_t launch_fwd_paged(const FwdPagedParams& p, int d, bool fp4, long long max_units,
                              cudaStream_t stream);
 
