@@ -52,6 +52,7 @@ template <int D, bool FP4, int TILES>
 struct PagedCfg {
   static constexpr int kRows = 8 * TILES;            // rows of a block
   static constexpr int kUnit = FP4 ? 32 : 16;        // positions of a unit
+  static constexpr int kLeast = 64 / kUnit;          // units of a warp's piece at least
   static constexpr int kWarps = FP4 && TILES == 2 ? 12 : 8;
   static constexpr int kCtas = FP4 && TILES == 1 ? 2 : 1;  // per SM
   static constexpr int kWorkers = kWarps * kCtas;    // warps per SM
@@ -182,24 +183,26 @@ struct Loader {
   using C = PagedCfg<D, FP4, TILES>;
   Walk w;
   int page;    // lane: page number of its place in the batch (below), -1: none
-  int batch0;  // first unit of the batch of page numbers, -1: to be loaded
-  int issued;  // units
+  int batch;   // units of the batch of page numbers left, 0: to be loaded
+  int stage;   // the next copy's
+  int kvh;     // w.seg's key head
 
   // Page numbers come 32 at a time, one per lane: of 32 units, or where a
   // unit spans two pages (4 bits, pages of 16) of 16.
   __device__ __forceinline__ void next(const FwdPagedParams& p, uint32_t ring, uint32_t bars, int lane) {
-    while (w.left > 0 && w.unit >= w.s.loads) {  // a segment's end, or one without positions
-      const int rest = w.s.loads == 0 ? 1 : 0;
-      walk_next<C>(p, w, rest);
-      batch0 = -1;
-    }
     if (w.left <= 0) return;
+    while (w.unit >= w.s.loads) {  // a segment's end, or one without positions
+      walk_next<C>(p, w, w.s.loads == 0 ? 1 : 0);
+      batch = 0;
+      if (w.left <= 0) return;
+      kvh = w.seg / w.s.blocks;
+    }
     const bool two = C::kUnit > (1 << p.c.page_shift);
     const int per = two ? 16 : 32;
     auto unit_of = [&](int u) { return u < w.s.first ? u : u + w.s.skip; };
-    if (batch0 < 0 || w.unit >= batch0 + per) {
-      batch0 = w.unit;
-      const int u = batch0 + (two ? lane >> 1 : lane);
+    if (batch == 0) {
+      batch = per;
+      const int u = w.unit + (two ? lane >> 1 : lane);
       const int key = unit_of(u) * C::kUnit + (two ? (lane & 1) * 16 : 0);
       page = -1;
       if (u < w.s.loads && u < w.unit + w.left && key < w.s.len) {
@@ -210,27 +213,24 @@ struct Loader {
         }
       }
     }
-    const int stage = issued % C::kStages;
     const uint32_t dst = ring + stage * C::kStageBytes;
     const uint32_t bar = bars + 8 * stage;
-    const int key0 = unit_of(w.unit) * C::kUnit;
-    const int in_page = key0 & ((1 << p.c.page_shift) - 1);
-    const int kvh = w.seg / w.s.blocks;
+    const int in_page = (unit_of(w.unit) * C::kUnit) & ((1 << p.c.page_shift) - 1);
     // lanes 0-3 (and 4-7 for a second page): K and V, codes and scales or 64 columns each
     const int sub = two ? (lane >> 2) & 1 : 0;
-    const int from = __shfl_sync(0xffffffffu, page, two ? (w.unit - batch0) * 2 + sub : w.unit - batch0);
+    const int from = __shfl_sync(0xffffffffu, page, two ? (per - batch) * 2 + sub : per - batch);
     const int subs = two ? 2 : 1;
     const unsigned int live = __ballot_sync(0xffffffffu, from >= 0 && lane < 4 * subs);
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * (C::kStageBytes / (4 * subs)));
+    if (lane == 0) mbar_arrive_expect_tx(bar, two ? __popc(live) * (C::kStageBytes / 8) : live ? C::kStageBytes : 0);
     __syncwarp();
     if (from >= 0 && lane < 4 * subs) {
       const size_t block = static_cast<size_t>(from) * p.c.Hkv + kvh;
       const int kv = (lane >> 1) & 1, part = lane & 1;
       if constexpr (FP4) {
-        const int keys = C::kUnit / subs;
+        const int keys = two ? C::kUnit / 2 : C::kUnit;
         const size_t half = paged_half_bytes(true, 1 << p.c.page_shift, D);
         const uint8_t* src = p.c.pages + (block * 2 + kv) * half;
-        // both parts of a half add up to kHalf / subs bytes
+        // both parts of a half add up to its share of kHalf bytes
         if (part == 0)
           bulk_load(dst + kv * C::kHalf + sub * keys * (D / 2), src + static_cast<size_t>(in_page) * (D / 2),
                     keys * (D / 2), bar);
@@ -242,10 +242,10 @@ struct Loader {
                     static_cast<int>(block * 2 + kv));
       }
     }
-    ++issued;
+    stage = stage == C::kStages - 1 ? 0 : stage + 1;
+    --batch;
     ++w.unit;
     --w.left;
-    if (w.left == 0) return;
   }
 };
 
@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
     fa_fwd_paged_kernel(const __grid_constant__ FwdPagedParams p) {
   using C = PagedCfg<D, FP4, TILES>;
   constexpr int kSteps = D / 16;  // k16 steps of Q K^T, and m16 tiles of P V
+  constexpr int kGroups = C::kUnit / 16;  // k16 steps of P V in a unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
@@ -289,25 +290,34 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
     }
     return v;
   };
-  long long total = 0;
+  long long total = 0, mine = 0, end = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += 32 * C::kWarps) {
     const int b = b0 + threadIdx.x;
     long long t;
-    block_scan(b < p.c.B ? seq_units(p, paged_seq<C>(p, b, blockIdx.x == 0)) : 0, t);
+    mine = b < p.c.B ? seq_units(p, paged_seq<C>(p, b, blockIdx.x == 0)) : 0;
+    end = total + block_scan(mine, t);
     total += t;
   }
   // worker i: warp i / grid of CTA i % grid, so that few units spread over the SMs
   const int grid = static_cast<int>(gridDim.x);
-  const long long workers = min(static_cast<long long>(grid) * C::kWarps, total);
-  const long long quot = total / max(workers, 1LL), rem = total - quot * workers;
+  const long long workers =
+      max(1LL, min(static_cast<long long>(grid) * C::kWarps, (total + C::kLeast - 1) / C::kLeast));
+  const long long quot = total <= 0x7fffffffLL
+                             ? static_cast<long long>(static_cast<unsigned int>(total) / static_cast<unsigned int>(workers))
+                             : total / workers;
+  const long long rem = total - quot * workers;
   auto piece = [&](long long i) { return quot * i + min(i, rem); };
   const long long me = static_cast<long long>(warp) * grid + blockIdx.x;
+  const bool once = p.c.B <= 32 * C::kWarps;  // the scan above still holds every sequence
   long long before = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += 32 * C::kWarps) {
     const int b = b0 + threadIdx.x;
-    const long long mine = b < p.c.B ? seq_units(p, paged_seq<C>(p, b, false)) : 0;
-    long long t;
-    const long long end = before + block_scan(mine, t);
+    if (!once) {
+      long long t;
+      mine = b < p.c.B ? seq_units(p, paged_seq<C>(p, b, false)) : 0;
+      end = before + block_scan(mine, t);
+      before += t;
+    }
     for (int w = 0; w < C::kWarps; ++w) {
       const long long i = static_cast<long long>(w) * grid + blockIdx.x;
       const long long u0 = piece(i);
@@ -316,30 +326,34 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
         start[2 * w + 1] = u0 - (end - mine);
       }
     }
-    before += t;
   }
   __syncthreads();
   if (lane == 0) p.info[me] = make_int4(0, 0, 0, 0);
-  if (me >= workers) return;
+  if (me >= workers || total == 0) return;
   Walk w;
   w.left = static_cast<int>(piece(me + 1) - piece(me));
   w.b = static_cast<int>(start[2 * warp]);
   w.s = paged_seq<C>(p, w.b, false);
-  w.seg = static_cast<int>(start[2 * warp + 1] / w.s.units);
-  w.unit = static_cast<int>(start[2 * warp + 1] % w.s.units);
+  // (a sequence's units: sized by its row of the page table, times its segments)
+  const long long at = start[2 * warp + 1];
+  w.seg = at <= 0x7fffffffLL ? static_cast<int>(static_cast<unsigned int>(at) / static_cast<unsigned int>(w.s.units))
+                             : static_cast<int>(at / w.s.units);
+  w.unit = static_cast<int>(at - static_cast<long long>(w.seg) * w.s.units);
 
   const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
   const uint32_t ring_s = sbase + warp * C::kStages * C::kStageBytes;
   const uint32_t bars = sbase + C::kBarOff + warp * C::kStages * 8;
   Loader<D, FP4, TILES> load;
   load.w = w;
-  load.batch0 = -1;
+  load.batch = 0;
   load.page = -1;
-  load.issued = 0;
+  load.stage = 0;
+  load.kvh = w.seg / max(1, w.s.blocks);
   for (int i = 0; i < C::kStages; ++i) load.next(p, ring_s, bars, lane);
 
   const int g = lane >> 2, c = lane & 3;
-  int used = 0;
+  int stage = 0;
+  uint32_t parity = 0;
   bool ok = true;
   while (w.left > 0) {
     const int kvh = w.seg / w.s.blocks;
@@ -350,8 +364,8 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
     const int pair0 = block * C::kRows;
     const int pos0 = w.s.len - w.s.n;  // position of the first new row
     // the block's rows' positions, least and most
-    const int p_lo = pos0 + pair0 / p.group;
-    const int p_hi = pos0 + (min(n_pairs, pair0 + C::kRows) - 1) / p.group;
+    const int p_lo = max(-1, pos0 + pair0 / p.group);
+    const int p_hi = max(-1, pos0 + (min(n_pairs, pair0 + C::kRows) - 1) / p.group);
 
     // Q as the products' B operand: lane (g, c) holds of pair g the elements
     // (4 bits) c D/4 + 4 s + {0, 1} and + {2, 3}, (bf16) 16 s + 2c + {0, 1} and + 8
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
       for (int e = 0; e < 2; ++e) {
         mul[t][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + e));
         const int pr = pair0 + t * 8 + 2 * c + e;
-        pos[t][e] = pr < n_pairs ? pos0 + pr / p.group : -1;
+        pos[t][e] = pr < n_pairs ? max(-1, pos0 + pr / p.group) : -1;
       }
     }
 
@@ -425,25 +439,28 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
       }
     }
 
-    for (int u = w.unit; u < n_load; ++u, ++used) {
-      const int stage = used % C::kStages;
-      if (ok) ok = mbar_wait_warp(bars + 8 * stage, (used / C::kStages) & 1, ctl, kSitePagedFull);
+    for (int u = w.unit; u < n_load; ++u) {
+      if (ok && !mbar_wait_warp(bars + 8 * stage, parity, ctl, kSitePagedFull)) {
+        // given up: no more copies; those in flight (this stage's and the ones
+        // after it) land before shared memory is released
+        ok = false;
+        for (int i = 0; i < C::kStages; ++i)
+          mbar_wait_drain(bars + 8 * ((stage + i) % C::kStages), parity ^ (stage + i >= C::kStages ? 1u : 0u));
+      }
       const int unit_key = (u < w.s.first ? u : u + w.s.skip) * C::kUnit;
       const uint8_t* st = ring + stage * C::kStageBytes;
       const uint32_t st_s = ring_s + stage * C::kStageBytes;
       // every position visible to every row?
       const bool edge =
-          unit_key + C::kUnit - 1 > p_lo ||
-          (static_cast<long long>(unit_key) <= static_cast<long long>(p_hi) - p.window && unit_key + C::kUnit > p.sinks);
+          unit_key + C::kUnit - 1 > p_lo || (unit_key < p_hi - p.window + 1 && unit_key + C::kUnit > p.sinks);
+      // S^T = K Q^T: key unit_key + 16 grp + g (0, 1) or + 8 (2, 3) of pairs 2c, 2c + 1
+      float s[kGroups][TILES][4];
 #pragma unroll
-      for (int grp = 0; grp < C::kUnit / 16; ++grp) {
-        const int key0 = unit_key + grp * 16;
-        // S^T = K Q^T: key key0 + g (0, 1) or + 8 (2, 3) of pairs 2c, 2c + 1
-        float s[TILES][4];
+      for (int grp = 0; grp < kGroups; ++grp) {
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) s[grp][t][e] = 0.0f;
         if constexpr (FP4) {
           uint32_t codes[2][D / 32];
           uint32_t sc[2][D / 64];  // the scales of this lane's blocks of 16, twice each
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
               const uint32_t a[4] = {hmul2(x[2 * k], sc[0][wd >> 1]), hmul2(y[2 * k], sc[1][wd >> 1]),
                                      hmul2(x[2 * k + 1], sc[0][wd >> 1]), hmul2(y[2 * k + 1], sc[1][wd >> 1])};
 #pragma unroll
-              for (int t = 0; t < TILES; ++t) mma16816<true>(s[t], a, qb[t][2 * wd + k]);
+              for (int t = 0; t < TILES; ++t) mma16816<true>(s[grp][t], a, qb[t][2 * wd + k]);
             }
           }
         } else {
@@ -487,73 +504,95 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
             const int chunk = (k & 3) * 2 + (lane >> 4);
             ldmatrix_x4(st_s + (k >> 2) * (C::kUnit * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) mma16816<false>(s[t], a, qb[t][k]);
+            for (int t = 0; t < TILES; ++t) mma16816<false>(s[grp][t], a, qb[t][k]);
           }
         }
+      }
 
-        // scores relative to the references; masked ones -inf
-        bool over = false;
+      // scores relative to the references
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
+      for (int grp = 0; grp < kGroups; ++grp)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[t][e] = fmaf(s[t][e], mul[t][e & 1], -ref[t][e & 1]);
-            if (edge) {
-              const int j = key0 + g + (e >> 1) * 8;
-              const int q = pos[t][e & 1];
-              if (!(j <= q && (static_cast<long long>(q) - j < p.window || j < p.sinks))) s[t][e] = -INFINITY;
-            }
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[grp][t][e] = fmaf(s[grp][t][e], mul[t][e & 1], -ref[t][e & 1]);
+      // Masked scores are -inf.  A position that no row sees has weight 0, but
+      // its row of V may hold anything (the rest of a page, infinities): it is
+      // zeroed.  Bit 4 grp + k of keep: position 16 grp + 2c + {0, 1, 8, 9}[k].
+      unsigned int keep = 0xFFu;
+      if (edge) {
+        keep = 0u;
+#pragma unroll 1
+        for (int grp = 0; grp < kGroups; ++grp) {
+          const int key0 = unit_key + grp * 16;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = key0 + (k >> 1) * 8 + 2 * c + (k & 1);
+            if (j <= p_hi && (j < p.sinks || j > p_lo - p.window)) keep |= 1u << (4 * grp + k);
           }
-          over = over || fmaxf(s[t][0], s[t][2]) > lim[t][0] || fmaxf(s[t][1], s[t][3]) > lim[t][1];
         }
-        if (__any_sync(0xffffffffu, over)) {
-          // some reference is too far below: all that are behind move up
+#pragma unroll
+        for (int grp = 0; grp < kGroups; ++grp)
 #pragma unroll
           for (int t = 0; t < TILES; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(s[t][e], s[t][e + 2]);
+            for (int e = 0; e < 4; ++e) {
+              const int j = unit_key + grp * 16 + g + (e >> 1) * 8;
+              const int q = pos[t][e & 1];
+              if (j > q || (j <= q - p.window && j >= p.sinks)) s[grp][t][e] = -INFINITY;
+            }
+      }
+      bool over = false;
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              if (mx > lim[t][e]) {
-                const float a = lim[t][e] == -INFINITY ? 0.0f : ex2_mufu(-mx);
-                ref[t][e] += mx;
-                lim[t][e] = kSlack<FP4>;
-                s[t][e] -= mx;
-                s[t][e + 2] -= mx;
-                l[t][e] *= a;
+      for (int t = 0; t < TILES; ++t)
 #pragma unroll
-                for (int j = 0; j < kSteps; ++j) {
-                  acc[t][j][e] *= a;
-                  acc[t][j][e + 2] *= a;
-                }
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(s[0][t][e], s[0][t][e + 2]);
+          if constexpr (kGroups == 2) mx = fmax3(mx, s[1][t][e], s[1][t][e + 2]);
+          over = over || mx > lim[t][e];
+        }
+      if (__any_sync(0xffffffffu, over)) {
+        // some reference is too far below: all that are behind move up
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(s[0][t][e], s[0][t][e + 2]);
+            if constexpr (kGroups == 2) mx = fmax3(mx, s[1][t][e], s[1][t][e + 2]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (mx > lim[t][e]) {
+              const float a = lim[t][e] == -INFINITY ? 0.0f : ex2_mufu(-mx);
+              ref[t][e] += mx;
+              lim[t][e] = kSlack<FP4>;
+#pragma unroll
+              for (int grp = 0; grp < kGroups; ++grp) {
+                s[grp][t][e] -= mx;
+                s[grp][t][e + 2] -= mx;
+              }
+              l[t][e] *= a;
+#pragma unroll
+              for (int j = 0; j < kSteps; ++j) {
+                acc[t][j][e] *= a;
+                acc[t][j][e + 2] *= a;
               }
             }
-        }
+          }
+      }
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int grp = 0; grp < kGroups; ++grp) {
         uint32_t pb[TILES][2];  // P as the B operand: keys 2c, 2c + 1 (and + 8) of pair g
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
           for (int k8 = 0; k8 < 2; ++k8) {
-            const float x = ex2_mufu(s[t][2 * k8]), y = ex2_mufu(s[t][2 * k8 + 1]);
+            const float x = ex2_mufu(s[grp][t][2 * k8]), y = ex2_mufu(s[grp][t][2 * k8 + 1]);
             l[t][0] += x;
             l[t][1] += y;
             pb[t][k8] = transpose8x8(FP4 ? pack_f16x2(x, y) : pack_bf16x2(x, y));
           }
-
-        // O^T += V^T P^T.  A position that no row sees has weight 0, but its
-        // row of V may hold anything (the rest of a page, infinities): it is
-        // zeroed.  Bit k: position key0 + 2c + {0, 1, 8, 9}[k].
-        unsigned int keep = 15u;
-        if (edge) {
-          keep = 0u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = key0 + (k >> 1) * 8 + 2 * c + (k & 1);
-            const bool seen = j <= p_hi && (j < p.sinks || static_cast<long long>(p_lo) - j < p.window);
-            keep |= seen ? 1u << k : 0u;
-          }
-        }
         if constexpr (FP4) {
           // rows g, g + 8 of m-tile j are d = g D/8 + 2j, + 1
           const uint8_t* vc = st + C::kHalf + (grp * 16 + 2 * c) * (D / 2) + g * (D / 16);
@@ -561,9 +600,12 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
           uint32_t sc[2];  // scales of the keys' pairs
 #pragma unroll
           for (int k8 = 0; k8 < 2; ++k8) {
-            const uint32_t lo = (keep >> (2 * k8)) & 1u ? vs[k8 * 8 * (D / 16)] : 0u;
-            const uint32_t hi = (keep >> (2 * k8 + 1)) & 1u ? vs[(k8 * 8 + 1) * (D / 16)] : 0u;
-            sc[k8] = e4m3x2_to_f16x2(lo | (hi << 8));
+            uint32_t two = vs[k8 * 8 * (D / 16)] | (static_cast<uint32_t>(vs[(k8 * 8 + 1) * (D / 16)]) << 8);
+            if (edge) {
+              const unsigned int bits = keep >> (4 * grp + 2 * k8);
+              two &= ((bits & 1u) ? 0xFFu : 0u) | ((bits & 2u) ? 0xFF00u : 0u);
+            }
+            sc[k8] = e4m3x2_to_f16x2(two);
           }
           uint32_t codes[2][2][D / 64];  // [+0, +8][key][word]
 #pragma unroll
@@ -601,8 +643,9 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
           // rows g, g + 8 of m-tile j are d = 16 j + g, + 8: lanes 0-7 keys 0-7 of
           // columns 16j.., 8-15 the next 8 columns, 16-31 keys 8-15
           const int row = grp * 16 + (lane & 7) + ((lane >> 4) << 3);
-          const uint32_t k01 = ((keep & 1u) ? 0xFFFFu : 0u) | ((keep & 2u) ? 0xFFFF0000u : 0u);
-          const uint32_t k89 = ((keep & 4u) ? 0xFFFFu : 0u) | ((keep & 8u) ? 0xFFFF0000u : 0u);
+          const unsigned int bits = keep >> (4 * grp);
+          const uint32_t k01 = ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
+          const uint32_t k89 = ((bits & 4u) ? 0xFFFFu : 0u) | ((bits & 8u) ? 0xFFFF0000u : 0u);
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
             uint32_t a[4];
@@ -617,7 +660,11 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
         }
       }
       __syncwarp();  // every lane has read the stage
-      load.next(p, ring_s, bars, lane);
+      if (ok) load.next(p, ring_s, bars, lane);
+      if (++stage == C::kStages) {
+        stage = 0;
+        parity ^= 1u;
+      }
     }
 
     // ---- the segment's rows, or this warp's part of them
@@ -684,10 +731,6 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
     }
     walk_next<C>(p, w, u1 - w.unit);
   }
-  // (every copy has been waited for, but on the give-up path)
-  if (!ok)
-    for (int i = max(0, load.issued - C::kStages); i < load.issued; ++i)
-      mbar_wait_drain(bars + 8 * (i % C::kStages), (i / C::kStages) & 1);
 }
 
 // Joins the parts of the segments that start in the workers of this block (8 of
@@ -715,7 +758,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_fwd_paged_join_kernel(const _
     if (info.x == 0) continue;
     float m = -INFINITY, l = 0.0f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     for (int k0 = grp; k0 < info.x; k0 += kBatch * kGroups) {
       float mk[kBatch], lk[kBatch];
       float4 y[kBatch];
