@@ -27,6 +27,19 @@ cudaError_t launched(unsigned int n) {
   return err;
 }
 
+// Number of SMs of the current device (the persistent forward's grid).
+int sm_count() {
+  static std::mutex mu;
+  static int counts[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (counts[dev] == 0 &&
+      cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    counts[dev] = 0;
+  return counts[dev];
+}
+
 namespace {
 
 int g_last_site = 0;
@@ -176,19 +189,6 @@ int check_shape(int B, int H, int N, int d, float scale, bool* empty) {
   // grid sizes and int row indices inside the kernels
   if (bh > (1LL << 30) || static_cast<long long>(N) * bh > (1LL << 40)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
-}
-
-// Number of SMs of the current device (the persistent forward's grid).
-int sm_count() {
-  static std::mutex mu;
-  static int counts[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  if (counts[dev] == 0 &&
-      cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    counts[dev] = 0;
-  return counts[dev];
 }
 
 constexpr int kMaxSinks = 128;  // first tokens of a sliding window: one key tile
@@ -374,7 +374,7 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, i
     if ((reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0) return FA_ERR_WORKSPACE;
   }
 
-  FwdParams p;
+  FwdParams p = {};
   const int BH = B * H;
   const long long rows = static_cast<long long>(BH) * N;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

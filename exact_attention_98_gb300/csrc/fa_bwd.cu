@@ -863,17 +863,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
 template <int D, bool kNoDQ = false, bool kWindow = false>
 cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
   using C = BwdCfg<D, kNoDQ>;
-  void (*kernel)(BwdParams) = kWindow ? fa_bwd_window_kernel<D>
-                              : kNoDQ ? fa_bwd_dkdv_kernel<D>
-                                      : fa_bwd_kernel<D>;
-  // The setmaxnreg split assumes the launch allocation; refuse to run a build
-  // whose register count differs (an over-committed split would never finish).
-  cudaFuncAttributes attr;
-  cudaError_t err = cudaFuncGetAttributes(&attr, kernel);
-  if (err != cudaSuccess) return err;
-  if (attr.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes);
+  constexpr void (*kernel)(BwdParams) = kWindow ? fa_bwd_window_kernel<D>
+                                        : kNoDQ ? fa_bwd_dkdv_kernel<D>
+                                                : fa_bwd_kernel<D>;
+  cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   const long long blocks = static_cast<long long>(p.n_kblk) * p.BH;
   err = launch_dependent(kernel, dim3(static_cast<unsigned int>(blocks)), dim3(C::kThreads),

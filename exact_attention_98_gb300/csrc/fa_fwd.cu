@@ -993,22 +993,13 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
 template <int D, int POLY, bool FP8 = false, bool WINDOW = false>
 cudaError_t launch_fwd_dp(const FwdParams& p, cudaStream_t stream) {
   using C = FwdCfg<D, FP8>;
-  auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW>;
-  // The setmaxnreg split assumes the launch allocation; refuse to run a build
-  // whose register count differs (an over-committed split would never finish).
-  cudaFuncAttributes attr;
-  cudaError_t err = cudaFuncGetAttributes(&attr, kernel);
-  if (err != cudaSuccess) return err;
-  if (attr.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes);
+  constexpr auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW>;
+  cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM (the kernel holds all of tensor memory),
   // each walking the work items (see fwd_item_index).
-  int dev = 0, sms = 0;
-  err = cudaGetDevice(&dev);
-  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (err != cudaSuccess) return err;
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   const int blocks = p.n_items < sms ? p.n_items : sms;
   err = launch_dependent(kernel, dim3(static_cast<unsigned int>(blocks)),
                          dim3(C::kThreads), C::kSmemBytes, stream, p);

@@ -51,12 +51,13 @@ __device__ constexpr float kSlack = FP4 ? 8.0f : 2.0f;
 template <int D, bool FP4, int TILES>
 struct PagedCfg {
   static constexpr int kRows = 8 * TILES;            // rows of a block
-  static constexpr int kUnit = FP4 ? 32 : 16;        // positions of a unit
+  static constexpr int kUnitShift = FP4 ? (TILES == 2 ? 6 : 6) : 4;
+  static constexpr int kUnit = 1 << kUnitShift;      // positions of a unit
   static constexpr int kLeast = 64 / kUnit;          // units of a warp's piece at least
-  static constexpr int kWarps = FP4 && TILES == 2 ? 12 : 8;
-  static constexpr int kCtas = FP4 && TILES == 1 ? 2 : 1;  // per SM
+  static constexpr int kWarps = FP4 ? (TILES == 2 ? 8 : 12) : 8;
+  static constexpr int kCtas = 1;  // per SM
   static constexpr int kWorkers = kWarps * kCtas;    // warps per SM
-  static constexpr int kStages = 3;
+  static constexpr int kStages = FP4 ? (TILES == 2 ? 3 : 2) : 3;
   static constexpr int kRowBytes = FP4 ? D / 2 + D / 16 : 2 * D;
   static constexpr int kHalf = kUnit * kRowBytes;    // K rows of a unit
   static constexpr int kStageBytes = 2 * kHalf;
@@ -182,64 +183,67 @@ template <int D, bool FP4, int TILES>
 struct Loader {
   using C = PagedCfg<D, FP4, TILES>;
   Walk w;
-  int page;    // lane: page number of its place in the batch (below), -1: none
-  int batch;   // units of the batch of page numbers left, 0: to be loaded
+  // Page numbers come 32 at a time, one per lane: a batch of 32 units, or fewer
+  // where a unit spans several pages.  A lane keeps where its page's part of the
+  // unit starts: 4 bits, the address of its K codes (null: nothing to copy);
+  // bf16, block * 2 (-1: nothing).
+  unsigned long long at;
+  int batch;   // units of the batch left, 0: to be loaded
   int stage;   // the next copy's
-  int kvh;     // w.seg's key head
 
-  // Page numbers come 32 at a time, one per lane: of 32 units, or where a
-  // unit spans two pages (4 bits, pages of 16) of 16.
   __device__ __forceinline__ void next(const FwdPagedParams& p, uint32_t ring, uint32_t bars, int lane) {
     if (w.left <= 0) return;
     while (w.unit >= w.s.loads) {  // a segment's end, or one without positions
       walk_next<C>(p, w, w.s.loads == 0 ? 1 : 0);
       batch = 0;
       if (w.left <= 0) return;
-      kvh = w.seg / w.s.blocks;
     }
-    const bool two = C::kUnit > (1 << p.c.page_shift);
-    const int per = two ? 16 : 32;
-    auto unit_of = [&](int u) { return u < w.s.first ? u : u + w.s.skip; };
+    const int shift = min(p.c.page_shift, C::kUnitShift);  // positions of a page within a unit
+    const int subs_shift = C::kUnitShift - shift;
+    const int first_key = (w.unit < w.s.first ? w.unit : w.unit + w.s.skip) * C::kUnit;
+    const int page_mask = (1 << p.c.page_shift) - 1;
     if (batch == 0) {
-      batch = per;
-      const int u = w.unit + (two ? lane >> 1 : lane);
-      const int key = unit_of(u) * C::kUnit + (two ? (lane & 1) * 16 : 0);
-      page = -1;
+      batch = 32 >> subs_shift;
+      const int u = w.unit + (lane >> subs_shift);
+      const int key = (u < w.s.first ? u : u + w.s.skip) * C::kUnit + ((lane & ((1 << subs_shift) - 1)) << shift);
+      at = FP4 ? 0ull : ~0ull;
       if (u < w.s.loads && u < w.unit + w.left && key < w.s.len) {
-        page = p.c.page_table[static_cast<size_t>(w.b) * p.c.max_pages + (key >> p.c.page_shift)];
+        const int page = p.c.page_table[static_cast<size_t>(w.b) * p.c.max_pages + (key >> p.c.page_shift)];
         if (page < 0 || page >= p.c.num_pages) {
           record_status(p.status, kStatusInvalid, kSitePagedPage);
-          page = -1;
+        } else {
+          const size_t block2 = (static_cast<size_t>(page) * p.c.Hkv + w.seg / w.s.blocks) * 2;
+          at = block2;
+          if constexpr (FP4)
+            at = reinterpret_cast<unsigned long long>(p.c.pages) +
+                 block2 * paged_half_bytes(true, 1 << p.c.page_shift, D) +
+                 static_cast<unsigned int>((key & page_mask) * (D / 2));
         }
       }
     }
     const uint32_t dst = ring + stage * C::kStageBytes;
     const uint32_t bar = bars + 8 * stage;
-    const int in_page = (unit_of(w.unit) * C::kUnit) & ((1 << p.c.page_shift) - 1);
-    // lanes 0-3 (and 4-7 for a second page): K and V, codes and scales or 64 columns each
-    const int sub = two ? (lane >> 2) & 1 : 0;
-    const int from = __shfl_sync(0xffffffffu, page, two ? (per - batch) * 2 + sub : per - batch);
-    const int subs = two ? 2 : 1;
-    const unsigned int live = __ballot_sync(0xffffffffu, from >= 0 && lane < 4 * subs);
-    if (lane == 0) mbar_arrive_expect_tx(bar, two ? __popc(live) * (C::kStageBytes / 8) : live ? C::kStageBytes : 0);
+    // lanes 4 sub + 0..3: of page `sub` of the unit K and V, codes and scales or
+    // 64 columns each
+    const int sub = (lane >> 2) & ((1 << subs_shift) - 1);
+    const unsigned long long from =
+        __shfl_sync(0xffffffffu, at, (((32 >> subs_shift) - batch) << subs_shift) + sub);
+    const bool mine = lane < (4 << subs_shift) && from != (FP4 ? 0ull : ~0ull);
+    const unsigned int live = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * (C::kStageBytes / 4 >> subs_shift));
     __syncwarp();
-    if (from >= 0 && lane < 4 * subs) {
-      const size_t block = static_cast<size_t>(from) * p.c.Hkv + kvh;
+    if (mine) {
       const int kv = (lane >> 1) & 1, part = lane & 1;
       if constexpr (FP4) {
-        const int keys = two ? C::kUnit / 2 : C::kUnit;
-        const size_t half = paged_half_bytes(true, 1 << p.c.page_shift, D);
-        const uint8_t* src = p.c.pages + (block * 2 + kv) * half;
-        // both parts of a half add up to its share of kHalf bytes
-        if (part == 0)
-          bulk_load(dst + kv * C::kHalf + sub * keys * (D / 2), src + static_cast<size_t>(in_page) * (D / 2),
-                    keys * (D / 2), bar);
-        else
-          bulk_load(dst + kv * C::kHalf + C::kUnit * (D / 2) + sub * keys * (D / 16),
-                    src + (static_cast<size_t>(D / 2) << p.c.page_shift) + in_page * (D / 16), keys * (D / 16), bar);
+        const uint32_t half = static_cast<uint32_t>(paged_half_bytes(true, 1 << p.c.page_shift, D));
+        // the scales of a row stand behind the page's codes
+        const uint32_t in_page = (first_key + (sub << shift)) & page_mask;
+        const uint32_t src = kv * half + (part ? ((D / 2) << p.c.page_shift) - in_page * (D / 2 - D / 16) : 0u);
+        const uint32_t to = kv * C::kHalf + (part ? C::kUnit * (D / 2) + (sub << shift) * (D / 16) : (sub << shift) * (D / 2));
+        bulk_load(dst + to, reinterpret_cast<const uint8_t*>(from) + src, (part ? D / 16 : D / 2) << shift, bar);
       } else if (part < D / 64) {
-        tma_load_3d(dst + kv * C::kHalf + part * (C::kUnit * 128), &p.tm, bar, part * 64, in_page,
-                    static_cast<int>(block * 2 + kv));
+        tma_load_3d(dst + kv * C::kHalf + part * (C::kUnit * 128), &p.tm, bar, part * 64, first_key & page_mask,
+                    static_cast<int>(from) + kv);
       }
     }
     stage = stage == C::kStages - 1 ? 0 : stage + 1;
@@ -346,9 +350,8 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
   Loader<D, FP4, TILES> load;
   load.w = w;
   load.batch = 0;
-  load.page = -1;
+  load.at = 0;
   load.stage = 0;
-  load.kvh = w.seg / max(1, w.s.blocks);
   for (int i = 0; i < C::kStages; ++i) load.next(p, ring_s, bars, lane);
 
   const int g = lane >> 2, c = lane & 3;
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
       // Masked scores are -inf.  A position that no row sees has weight 0, but
       // its row of V may hold anything (the rest of a page, infinities): it is
       // zeroed.  Bit 4 grp + k of keep: position 16 grp + 2c + {0, 1, 8, 9}[k].
-      unsigned int keep = 0xFFu;
+      unsigned int keep = 0xFFFFu;
       if (edge) {
         keep = 0u;
 #pragma unroll 1
@@ -548,7 +551,8 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float mx = fmaxf(s[0][t][e], s[0][t][e + 2]);
-          if constexpr (kGroups == 2) mx = fmax3(mx, s[1][t][e], s[1][t][e + 2]);
+#pragma unroll
+          for (int grp = 1; grp < kGroups; ++grp) mx = fmax3(mx, s[grp][t][e], s[grp][t][e + 2]);
           over = over || mx > lim[t][e];
         }
       if (__any_sync(0xffffffffu, over)) {
@@ -558,7 +562,8 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mx = fmaxf(s[0][t][e], s[0][t][e + 2]);
-            if constexpr (kGroups == 2) mx = fmax3(mx, s[1][t][e], s[1][t][e + 2]);
+#pragma unroll
+            for (int grp = 1; grp < kGroups; ++grp) mx = fmax3(mx, s[grp][t][e], s[grp][t][e + 2]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             if (mx > lim[t][e]) {
@@ -823,20 +828,11 @@ __global__ void __launch_bounds__(kJoinThreads) fa_fwd_paged_join_kernel(const _
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 template <int D, bool FP4, int TILES>
 cudaError_t launch_dp(const FwdPagedParams& p, long long max_units, cudaStream_t stream) {
   using C = PagedCfg<D, FP4, TILES>;
   static_assert(C::kWorkers <= kPagedWorkersPerSm && C::kRows <= kPagedRows, "the workspace's shape");
-  cudaError_t err = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, FP4, TILES>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t err = configure_kernel<fa_fwd_paged_kernel<D, FP4, TILES>>(C::kSmemBytes);
   if (err != cudaSuccess) return err;
   const int ctas = sm_count() * C::kCtas;
   if (ctas <= 0) return cudaErrorInvalidConfiguration;

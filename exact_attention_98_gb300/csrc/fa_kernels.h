@@ -9,6 +9,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "fa_fastdiv.h"
@@ -231,6 +232,32 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// Number of SMs of the current device (0 on an error); looked up once per device.
+int sm_count();
+
+// Raises Kernel's limit of dynamic shared memory on the current device, and
+// refuses a build whose register count differs from `regs` (0: any): a
+// setmaxnreg split assumes the launch allocation, and an over-committed one
+// would never finish.  Asks the runtime once per device.
+template <auto* Kernel>
+cudaError_t configure_kernel(int smem, int regs = 0) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if (regs > 0) {
+    cudaFuncAttributes attr;
+    err = cudaFuncGetAttributes(&attr, Kernel);
+    if (err != cudaSuccess) return err;
+    if (attr.numRegs != regs) return cudaErrorInvalidConfiguration;
+  }
+  err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return err;
 }
 
 // The launch wrappers end with `return launched(n)`: the launch error of the

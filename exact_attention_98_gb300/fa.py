@@ -11,7 +11,6 @@ this module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -147,22 +146,27 @@ def _check(code: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
+    """The cudaStream_t of `stream`, or of the current stream of the current
+    device (looked up without building a torch.cuda.Stream, which takes 3 us)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _shape(q):
     if q.dim() != 4:
         raise ValueError("expected [B, H, N, d]")
-    return tuple(int(x) for x in q.shape)
+    return tuple(q.shape)
 
 
 def _check_tensor(t, name, dtype, shape, device=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and (device is None or t.device == device) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
@@ -359,10 +363,6 @@ def fa_paged_block_bytes(format: int, page_size: int, d: int) -> int:
     return int(lib.fa_paged_block_bytes(int(format), int(page_size), int(d)))
 
 
-def _check_ints(t, name, shape, device):
-    _check_tensor(t, name, torch.int32, shape, device)
-
-
 def _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale):
     """The cache's descriptor from its tensors (see paged_append); the
     tensors have to outlive the call that takes it."""
@@ -374,31 +374,30 @@ def _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale):
                          f"cuda:{torch.cuda.current_device()}")
     if not pages.is_contiguous():
         raise ValueError("pages must be contiguous")
+    shape = pages.shape
     if pages.dtype == torch.bfloat16:
-        if pages.dim() != 5 or pages.shape[2] != 2 or pages.shape[4] != d:
-            raise ValueError(f"bf16 pages are [num_pages, Hkv, 2, page_size, {d}], got "
-                             f"{tuple(pages.shape)}")
-        fmt, page_size = FA_CACHE_BF16, int(pages.shape[3])
+        if len(shape) != 5 or shape[2] != 2 or shape[4] != d:
+            raise ValueError(f"bf16 pages are [num_pages, Hkv, 2, page_size, {d}], got {tuple(shape)}")
+        fmt, page_size = FA_CACHE_BF16, shape[3]
     elif pages.dtype == torch.uint8:
         row = d // 2 + d // 16
-        if pages.dim() != 4 or pages.shape[2] != 2 or pages.shape[3] % row != 0:
+        if len(shape) != 4 or shape[2] != 2 or row == 0 or shape[3] % row != 0:
             raise ValueError(f"4-bit pages are uint8 [num_pages, Hkv, 2, page_size * {row}], got "
-                             f"{tuple(pages.shape)}")
-        fmt, page_size = FA_CACHE_FP4, int(pages.shape[3]) // row
+                             f"{tuple(shape)}")
+        fmt, page_size = FA_CACHE_FP4, shape[3] // row
     else:
         raise ValueError(f"pages must be torch.bfloat16 or torch.uint8 (4 bits), got {pages.dtype}")
-    num_pages, Hkv = int(pages.shape[0]), int(pages.shape[1])
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = (int(x) for x in page_table.shape)
-    _check_ints(page_table, "page_table", (B, max_pages), dev)
-    _check_ints(seq_lens, "seq_lens", (B,), dev)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None:
-            _check_tensor(t, name, torch.float32, (Hkv,), dev)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return PagedCache(ptr(pages), ptr(page_table), ptr(seq_lens), ptr(k_scale), ptr(v_scale), fmt, B,
-                      Hkv, d, num_pages, page_size, max_pages)
+    B, max_pages = page_table.shape
+    _check_tensor(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    _check_tensor(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if k_scale is not None:
+        _check_tensor(k_scale, "k_scale", torch.float32, (shape[1],), dev)
+    if v_scale is not None:
+        _check_tensor(v_scale, "v_scale", torch.float32, (shape[1],), dev)
+    return PagedCache(pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(k_scale),
+                      _ptr(v_scale), fmt, B, shape[1], d, shape[0], page_size, max_pages)
 
 
 def _rows(t, name, heads, d, device, rows=None):
@@ -408,13 +407,15 @@ def _rows(t, name, heads, d, device, rows=None):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) or (
-            rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or (
+            rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                          f"[{'rows' if rows is None else rows}, {'H' if heads is None else heads}, {d}]")
-    if t.numel() and t.stride(2) != 1:
+    row, head, one = t.stride()
+    if one != 1 and t.numel():
         raise ValueError(f"{name}'s rows of {d} values must be contiguous")
-    return int(t.shape[0]), t.stride(0), t.stride(1)
+    return shape[0], row, head
 
 
 def fa_paged_append(cache: PagedCache, k, k_row, k_head, v, v_row, v_head, cu_new, rows, q, q_row,
@@ -431,7 +432,7 @@ def fa_paged_read(cache: PagedCache, cu_new, rows, k, v, stream=None) -> None:
 
 
 def fa_fwd_paged_workspace_bytes(d: int) -> int:
-    return int(lib.fa_fwd_paged_workspace_bytes(int(d)))
+    return lib.fa_fwd_paged_workspace_bytes(d)
 
 
 def fa_fwd_paged(cache: PagedCache, q, q_row, q_head, o, lse, cu_new, rows, max_new, H, scale, window,
@@ -545,9 +546,12 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     return dq, dk, dv
 
 
-def _allocating_on(stream):
-    """Allocations inside belong to the stream that uses them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(stream, device, *shapes_and_types):
+    """Uninitialised tensors whose memory belongs to the stream that uses them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return [torch.empty(s, dtype=t, device=device) for s, t in shapes_and_types]
+    return [torch.empty(s, dtype=t, device=device) for s, t in shapes_and_types]
 
 
 def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
@@ -556,9 +560,7 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = N
     the first `sinks` keys; query head h reads key head h / (H / Hkv).  Returns
     (o, lse)."""
     B, H, N, d = _shape(q)
-    with _allocating_on(stream):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    o, lse = _empty(stream, q.device, (q.shape, torch.bfloat16), ((B, H, N), torch.float32))
     fa_fwd_window(q, k, v, o, lse, default_scale(d) if scale is None else scale, window, sinks, stream)
     return o, lse
 
@@ -568,11 +570,11 @@ def window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: f
     """Gradients (dq, dk, dv) of window_forward; dk and dv [B, Hkv, N, d] are
     summed over the query heads that share a key head."""
     B, H, N, d = _shape(q)
-    with _allocating_on(stream):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        if workspace is None:
-            n = fa_bwd_window_workspace_bytes(B, H, int(k.shape[1]), N, d, int(window), int(sinks))
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    dq, dk, dv = _empty(stream, q.device, (q.shape, torch.bfloat16), (k.shape, torch.bfloat16),
+                        (v.shape, torch.bfloat16))
+    if workspace is None:
+        n = fa_bwd_window_workspace_bytes(B, H, k.shape[1], N, d, window, sinks) if k.dim() == 4 else 0
+        workspace, = _empty(stream, q.device, (max(n, 1), torch.uint8))
     fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, default_scale(d) if scale is None else scale, window,
                   sinks, workspace, stream)
     return dq, dk, dv
@@ -614,25 +616,24 @@ def paged_append(k, v, pages, page_table, seq_lens, cu_new, q=None, rope=None, i
     result are not written."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k [rows, Hkv, d]")
-    d = int(k.shape[2])
+    d = k.shape[2]
     cache = _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale)
     dev = pages.device
     rows, k_row, k_head = _rows(k, "k", cache.Hkv, d, dev)
     _, v_row, v_head = _rows(v, "v", cache.Hkv, d, dev, rows)
-    _check_ints(cu_new, "cu_new", (cache.B + 1,), dev)
+    _check_tensor(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
     H = q_row = q_head = rope_len = rot = 0
     q_out = None
     if q is not None:
         _, q_row, q_head = _rows(q, "q", None, d, dev, rows)
-        H = int(q.shape[1])
-        with _allocating_on(stream):
-            q_out = torch.empty((rows, H, d), dtype=torch.bfloat16, device=dev)
+        H = q.shape[1]
+        q_out, = _empty(stream, dev, ((rows, H, d), torch.bfloat16))
         if H == 0:
             q = None
     if rope is not None:
         if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
             raise ValueError("rope must be [length, rot]")
-        rope_len, rot = (int(x) for x in rope.shape)
+        rope_len, rot = rope.shape
         _check_tensor(rope, "rope", torch.float32, (rope_len, rot), dev)
     fa_paged_append(cache, k, k_row, k_head, v, v_row, v_head, cu_new, rows, q, q_row, q_head,
                     None if q is None else q_out, H, rope, rope_len, rot, interleaved, stream)
@@ -643,12 +644,10 @@ def paged_read(pages, page_table, seq_lens, cu_new, rows: int, d: int, k_scale=N
                stream=None):
     """The last rows of each sequence (cu_new as in paged_append) out of the
     cache: (k, v), each bf16 [rows, Hkv, d]; padding rows are not written."""
-    cache = _paged_cache(pages, page_table, seq_lens, int(d), k_scale, v_scale)
-    _check_ints(cu_new, "cu_new", (cache.B + 1,), pages.device)
-    with _allocating_on(stream):
-        k, v = (torch.empty((int(rows), cache.Hkv, int(d)), dtype=torch.bfloat16, device=pages.device)
-                for _ in range(2))
-    fa_paged_read(cache, cu_new, int(rows), k, v, stream)
+    cache = _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale)
+    _check_tensor(cu_new, "cu_new", torch.int32, (cache.B + 1,), pages.device)
+    k, v = _empty(stream, pages.device, *[((rows, cache.Hkv, d), torch.bfloat16)] * 2)
+    fa_paged_read(cache, cu_new, rows, k, v, stream)
     return k, v
 
 
@@ -662,16 +661,14 @@ def paged_forward(q, pages, page_table, seq_lens, cu_new, max_new: int = 1, wind
     sinks: first positions that it sees besides."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("expected q [rows, H, d]")
-    H, d = int(q.shape[1]), int(q.shape[2])
+    H, d = q.shape[1:]
     cache = _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale)
     dev = pages.device
     rows, q_row, q_head = _rows(q, "q", H, d, dev)
-    _check_ints(cu_new, "cu_new", (cache.B + 1,), dev)
-    with _allocating_on(stream):
-        o = torch.empty((rows, H, d), dtype=torch.bfloat16, device=dev)
-        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(max(fa_fwd_paged_workspace_bytes(d), 1), dtype=torch.uint8, device=dev)
-    fa_fwd_paged(cache, q, q_row, q_head, o, lse, cu_new, rows, int(max_new), H,
-                 default_scale(d) if scale is None else scale, int(window), int(sinks), workspace, stream)
+    _check_tensor(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
+    o, lse = _empty(stream, dev, ((rows, H, d), torch.bfloat16), ((rows, H), torch.float32))
+    if workspace is None:
+        workspace, = _empty(stream, dev, (max(fa_fwd_paged_workspace_bytes(d), 1), torch.uint8))
+    fa_fwd_paged(cache, q, q_row, q_head, o, lse, cu_new, rows, max_new, H,
+                 default_scale(d) if scale is None else scale, window, sinks, workspace, stream)
     return o, lse
