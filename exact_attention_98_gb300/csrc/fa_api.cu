@@ -886,7 +886,7 @@ int fa_paged_append(const fa_paged_cache* cache, const void* k, long long k_row,
   if (q && (!row_strides_ok(q, q_row, q_head, d) || !q_out || !aligned16(q_out)))
     return FA_ERR_INVALID_ARG;
   if (rot > 0 && (!rope || !aligned16(rope))) return FA_ERR_INVALID_ARG;
-  if ((q ? H : 0) + 2LL * cache->Hkv > 0x7fffffffLL - 64) return FA_ERR_UNSUPPORTED;
+  if ((q ? H : 0) + 2LL * cache->Hkv > (1 << 28)) return FA_ERR_UNSUPPORTED;  // rows of a block's tokens are an int
   p.cu = cu_new;
   p.rows = rows;
   p.k = static_cast<const __nv_bfloat16*>(k);
@@ -900,6 +900,7 @@ int fa_paged_append(const fa_paged_cache* cache, const void* k, long long k_row,
   p.q_row = q_row;
   p.q_head = q_head;
   p.H = q ? H : 0;
+  p.div_heads = FastDiv(static_cast<uint32_t>(p.H + 2 * cache->Hkv));
   p.rope = rope;
   p.rope_len = rope_len;
   p.rot = rot;
@@ -923,6 +924,8 @@ int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void
   p.rows = rows;
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
+  if (2LL * cache->Hkv > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  p.div_heads = FastDiv(static_cast<uint32_t>(2 * cache->Hkv));
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;
   return launch_paged_read(p, cache->d, cache->format == FA_CACHE_FP4,

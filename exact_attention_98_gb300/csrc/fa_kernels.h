@@ -320,6 +320,7 @@ struct PagedAppendParams {
   int rope_len;
   int rot;  // 0: no rotation
   int interleaved;
+  FastDiv div_heads;  // H + 2 Hkv (rows of a token)
   unsigned int* status;
 };
 
@@ -330,6 +331,7 @@ struct PagedReadParams {
   int tokens;
   __nv_bfloat16* k;  // [rows, Hkv, d]
   __nv_bfloat16* v;
+  FastDiv div_heads;  // 2 Hkv (rows of a token)
   unsigned int* status;
 };
 
