@@ -900,7 +900,8 @@ int fa_paged_append(const fa_paged_cache* cache, const void* k, long long k_row,
   p.q_row = q_row;
   p.q_head = q_head;
   p.H = q ? H : 0;
-  p.div_heads = FastDiv(static_cast<uint32_t>(p.H + 2 * cache->Hkv));
+  p.div_q = FastDiv(static_cast<uint32_t>(q ? H : 1));
+  p.div_kv = FastDiv(static_cast<uint32_t>(2 * cache->Hkv));
   p.rope = rope;
   p.rope_len = rope_len;
   p.rot = rot;

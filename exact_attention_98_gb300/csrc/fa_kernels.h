@@ -320,7 +320,7 @@ struct PagedAppendParams {
   int rope_len;
   int rot;  // 0: no rotation
   int interleaved;
-  FastDiv div_heads;  // H + 2 Hkv (rows of a token)
+  FastDiv div_q, div_kv;  // rows of a token: H (1 without Q), 2 Hkv
   unsigned int* status;
 };
 

@@ -19,79 +19,141 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens of a block
+constexpr int kAppendBlocks = 4;  // blocks of the append on an SM at least
 
+// Eight elements of a row in fp32, as pairs for the packed instructions.
 struct Row8 {
-  float x[8];
+  f32x2 x[4];
 };
 
 __device__ __forceinline__ Row8 unpack8(const uint4& v) {
   Row8 r;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.x[2 * i] = __uint_as_float(w[i] << 16);
-    r.x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) r.x[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   return r;
 }
 
 __device__ __forceinline__ uint4 pack8(const Row8& r) {
-  return make_uint4(pack_bf16x2(r.x[0], r.x[1]), pack_bf16x2(r.x[2], r.x[3]),
-                    pack_bf16x2(r.x[4], r.x[5]), pack_bf16x2(r.x[6], r.x[7]));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(r.x[i], lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float turn(float a, float b, float cos, float sin) {
-  return __fsub_rn(__fmul_rn(a, cos), __fmul_rn(b, sin));
+// a c - b s and a c + b s, each product and sum rounded.  The sums are scalar:
+// the compiler joins a packed product and a packed sum into one fused operation
+// with one rounding.
+__device__ __forceinline__ f32x2 turn(f32x2 a, f32x2 b, f32x2 c, f32x2 s) {
+  float p0, p1, q0, q1;
+  f2_unpack(f2_mul(a, c), p0, p1);
+  f2_unpack(f2_mul(b, s), q0, q1);
+  return f2_pack(__fsub_rn(p0, q0), __fsub_rn(p1, q1));
 }
-__device__ __forceinline__ float turn_back(float a, float b, float cos, float sin) {
-  return __fadd_rn(__fmul_rn(a, cos), __fmul_rn(b, sin));
+__device__ __forceinline__ f32x2 turn_back(f32x2 a, f32x2 b, f32x2 c, f32x2 s) {
+  float p0, p1, q0, q1;
+  f2_unpack(f2_mul(a, c), p0, p1);
+  f2_unpack(f2_mul(b, s), q0, q1);
+  return f2_pack(__fadd_rn(p0, q0), __fadd_rn(p1, q1));
 }
 
-// x / g rounded to nearest with r = 1 / g rounded to nearest: the quotient's
-// error, exact in one fused operation, corrects it (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990).  Holds
-// away from overflow and underflow; the sign of a zero is x's.
+// The largest magnitude, NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float amax8(const Row8& r) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(r.x[i], lo, hi);
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(lo)), "f"(fabsf(hi)));
+  }
+  return m;
+}
+
+// Quotients by g rounded to nearest, with r = 1 / g rounded to nearest: the
+// quotient's error, exact in one fused operation, corrects it (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990).  Holds away from overflow and underflow; a negative zero becomes zero.
 __device__ __forceinline__ float divide(float x, float g, float r) {
   const float q = __fmul_rn(x, r);
-  return copysignf(fmaf(fmaf(-q, g, x), r, q), x);
+  return fmaf(fmaf(-q, g, x), r, q);
+}
+__device__ __forceinline__ f32x2 divide(f32x2 x, f32x2 minus_g, f32x2 r) {
+  const f32x2 q = f2_mul(x, r);
+  return f2_fma(f2_fma(q, minus_g, x), r, q);
 }
 
-// Eight of a block's 16 elements over the head's factor, their largest magnitude
-// (NaN where one is not finite).
-__device__ __forceinline__ float scale8(Row8& x, float g) {
-  float amax = 0.0f, zero = 0.0f;
-  if (g != 1.0f) {
-    const float r = __frcp_rn(g);
-    const bool fast = g > 0x1p-60f && g < 0x1p60f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x.x[i] = fast && fabsf(x.x[i]) < 0x1p60f ? divide(x.x[i], g, r) : __fdiv_rn(x.x[i], g);
+// The head's factor as the quantisation uses it.
+struct Factor {
+  float g, r;  // 1 / g rounded to nearest
+  bool fits;   // with magnitudes below 2^60, divide() holds
+};
+__device__ __forceinline__ Factor factor_of(const float* factors, int kvh) {
+  Factor f{1.0f, 1.0f, true};
+  if (factors) {
+    f.g = factors[kvh];
+    f.r = __frcp_rn(f.g);
+    f.fits = f.g > 0x1p-60f && f.g < 0x1p60f;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    amax = fmaxf(amax, fabsf(x.x[i]));
-    zero = fmaf(x.x[i], 0.0f, zero);
-  }
-  return amax + zero;
+  return f;
 }
 
-// The block's scale byte from its largest magnitude (NaN: 0x7F), and its codes.
-// An element's quotient by the scale has to be on the right side of the borders
-// between codes: these times the scale are exact in fp32, and two fp32 numbers
-// that differ do so by more than a quotient's rounding, so the rounded quotient
-// is on the exact one's side.
-__device__ __forceinline__ uint32_t scale_byte(float amax) {
-  const float s = __fdiv_rn(amax, 6.0f);
+// The scale byte of a block whose largest magnitude is amax: e4m3(amax / g / 6)
+// (rounding keeps order, so the largest quotient is the largest magnitude's);
+// 0x7F, a NaN, if it is not finite.
+__device__ __forceinline__ uint32_t scale_byte(float amax, const Factor& f) {
+  constexpr float kSixth = 1.0f / 6.0f;
+  float s;
+  if (f.fits && amax < 0x1p60f)
+    s = divide(divide(amax, f.g, f.r), 6.0f, kSixth);
+  else
+    s = __fdiv_rn(__fdiv_rn(amax, f.g), 6.0f);
   unsigned short two;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(s));
-  return amax == amax ? two & 0xFFu : 0x7Fu;
+  return s < INFINITY ? two & 0xFFu : 0x7Fu;
 }
-__device__ __forceinline__ uint32_t codes8(const Row8& y, uint32_t byte) {
+
+// 1 / s of an e4m3 scale, rounded to nearest (one Newton step on the hardware's
+// approximation; the tests run every scale through it).
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(fmaf(-s, r, 1.0f), r, r);
+}
+
+// Codes of eight elements x of a block with that scale byte.  y = x / g and z =
+// y / s are rounded one by one.  (The order of z and a border between codes is
+// that of y and border * s, exact in fp32: two fp32 numbers that differ do so by
+// more than a quotient's rounding.)
+__device__ __forceinline__ uint32_t codes8(const Row8& x, const Factor& f, bool small, uint32_t byte) {
   if (byte == 0u || byte == 0x7Fu) return 0u;  // zero at this precision, or not finite
   const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(byte))));
-  const float r = __frcp_rn(s);
+  Row8 y;
+  if (small) {
+    const f32x2 r2 = f2_pack(f.r, f.r), n2 = f2_pack(-f.g, -f.g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.x[i] = divide(x.x[i], n2, r2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f2_unpack(x.x[i], lo, hi);
+      y.x[i] = f2_pack(__fdiv_rn(lo, f.g), __fdiv_rn(hi, f.g));
+    }
+  }
+  const float r = reciprocal(s);
+  const f32x2 r2 = f2_pack(r, r), n2 = f2_pack(-s, -s);
   float z[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = divide(y.x[i], s, r);
+  for (int i = 0; i < 4; ++i) f2_unpack(divide(y.x[i], n2, r2), z[2 * i], z[2 * i + 1]);
   uint32_t codes;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -119,43 +181,92 @@ __device__ __forceinline__ int chunk_owner(int x, int rot, bool interleaved) {
   return x < half8 ? 2 * x : 2 * (x - half8) + 1;
 }
 
-// A block of threads takes `tokens` rows of the batch; a thread two chunks of 8
-// elements of every 32nd (d = 128) or 64th (d = 64) of their heads' rows (Q heads,
-// then K heads, then V heads, token by token), the next row's loads ahead of
-// the present one's work.
+// cos and sin of the eight pairs of a thread's chunks, and their rotation.
+struct Turn {
+  f32x2 cos[4], sin[4];
+  int token = -1;  // of the block, whose position they are for
+
+  __device__ __forceinline__ void load(const PagedAppendParams& p, int k, int pos, int2 ch) {
+    if (k == token) return;
+    token = k;
+    const float* at = p.rope + static_cast<size_t>(pos) * p.rot + (p.interleaved ? ch.x * 4 : ch.x * 8);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(at + 4 * u);
+      const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(at + (p.rot >> 1) + 4 * u);
+      cos[2 * u] = c.x; cos[2 * u + 1] = c.y;
+      sin[2 * u] = s.x; sin[2 * u + 1] = s.y;
+    }
+  }
+
+  __device__ __forceinline__ void apply(Row8& x, Row8& y, bool interleaved) const {
+    if (interleaved) {  // four pairs in each chunk
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        // two pairs: their first elements together, their second ones together
+        Row8& row = u < 2 ? x : y;
+        float a0, b0, a1, b1;
+        f2_unpack(row.x[2 * (u & 1)], a0, b0);
+        f2_unpack(row.x[2 * (u & 1) + 1], a1, b1);
+        const f32x2 a = f2_pack(a0, a1), b = f2_pack(b0, b1);
+        f2_unpack(turn(a, b, cos[u], sin[u]), a0, a1);
+        f2_unpack(turn_back(b, a, cos[u], sin[u]), b0, b1);
+        row.x[2 * (u & 1)] = f2_pack(a0, b0);
+        row.x[2 * (u & 1) + 1] = f2_pack(a1, b1);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const f32x2 a = x.x[u], b = y.x[u];
+        x.x[u] = turn(a, b, cos[u], sin[u]);
+        y.x[u] = turn_back(b, a, cos[u], sin[u]);
+      }
+    }
+  }
+};
+
+// A block of threads takes `tokens` rows of the batch: a thread two chunks of 8
+// elements of every 32nd (d = 128) or 64th (d = 64) row of their heads, Q's first,
+// then K's and V's, the next row's loads ahead of the present one's work.
 template <int D, bool FP4>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int kPer = D / 16;  // threads of a row
   constexpr int kSlots = kThreads / kPer;
   grid_dependency_wait();
   __shared__ PagedRow rows[kMaxTokens];
   const int t0 = blockIdx.x * p.tokens;
-  const int hq = p.H;  // 0 without Q
-  const int heads = static_cast<int>(p.div_heads.d);
+  const int tokens = min(p.tokens, p.rows - t0);
   const int i = threadIdx.x % kPer;
   const int2 ch = chunk_pair(i, p.rot, p.interleaved);
-  const int n_rows = min(p.tokens, p.rows - t0) * heads;
-  auto source = [&](int r) {
-    const int k = p.div_heads.div(r), h = r - k * heads;
-    const long long t = t0 + k;
-    return h < hq                ? p.q + t * p.q_row + h * p.q_head
-           : h < hq + p.c.Hkv    ? p.k + t * p.k_row + (h - hq) * p.k_head
-                                 : p.v + t * p.v_row + (h - hq - p.c.Hkv) * p.v_head;
-  };
+  const bool turned = ch.x * 8 < p.rot;
+
+  // a thread's elements of the next row of Q (of K or V)
   uint4 next0 = make_uint4(0u, 0u, 0u, 0u), next1 = next0;
-  auto fetch = [&](int r) {
-    if (r < n_rows) {
-      const __nv_bfloat16* src = source(r);
+  const int q_rows = tokens * p.H;
+  auto fetch_q = [&](int r) {
+    if (r < q_rows) {
+      const int k = p.div_q.div(r), h = r - k * p.H;
+      const __nv_bfloat16* src = p.q + static_cast<long long>(t0 + k) * p.q_row + h * p.q_head;
+      next0 = *reinterpret_cast<const uint4*>(src + ch.x * 8);
+      next1 = *reinterpret_cast<const uint4*>(src + ch.y * 8);
+    }
+  };
+  const int kv_heads = 2 * p.c.Hkv, kv_rows = tokens * kv_heads;
+  auto fetch_kv = [&](int r) {
+    if (r < kv_rows) {
+      const int k = p.div_kv.div(r), h = r - k * kv_heads;
+      const __nv_bfloat16* src = h < p.c.Hkv
+                                     ? p.k + static_cast<long long>(t0 + k) * p.k_row + h * p.k_head
+                                     : p.v + static_cast<long long>(t0 + k) * p.v_row + (h - p.c.Hkv) * p.v_head;
       next0 = *reinterpret_cast<const uint4*>(src + ch.x * 8);
       next1 = *reinterpret_cast<const uint4*>(src + ch.y * 8);
     }
   };
   int r = threadIdx.x / kPer;
-  fetch(r);
-  if (threadIdx.x < p.tokens) {
-    const int t = t0 + threadIdx.x;
-    PagedRow row{-1, 0, -1};
-    if (t < p.rows) row = paged_row(p.c, p.cu, t, p.status);
+  if (q_rows > 0) fetch_q(r);
+  else fetch_kv(r);
+  if (threadIdx.x < tokens) {
+    PagedRow row = paged_row(p.c, p.cu, t0 + threadIdx.x, p.status);
     if (row.page >= 0 && p.rot > 0 && row.pos >= p.rope_len) {
       record_status(p.status, kStatusInvalid, kSitePagedLength);
       row.page = -1;
@@ -163,85 +274,62 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     rows[threadIdx.x] = row;
   }
   __syncthreads();
-  const int half = p.rot >> 1;
+
+  Turn rope;
+  for (; r < q_rows; r += kSlots) {
+    Row8 x = unpack8(next0), y = unpack8(next1);
+    fetch_q(r + kSlots);
+    const int k = p.div_q.div(r);
+    if (rows[k].page < 0) continue;
+    if (turned) {
+      rope.load(p, k, rows[k].pos, ch);
+      rope.apply(x, y, p.interleaved);
+    }
+    __nv_bfloat16* to = p.q_out + (static_cast<long long>(t0) * p.H + r) * D;
+    *reinterpret_cast<uint4*>(to + ch.x * 8) = pack8(x);
+    *reinterpret_cast<uint4*>(to + ch.y * 8) = pack8(y);
+  }
+
+  r = threadIdx.x / kPer;
+  if (q_rows > 0) fetch_kv(r);
   const size_t half_bytes = paged_half_bytes(FP4, 1 << p.c.page_shift, D);
   // 4 bits: the other eight elements of each chunk's block of 16 are with these
   // threads of the row
   const int own0 = chunk_owner(ch.x ^ 1, p.rot, p.interleaved), own1 = chunk_owner(ch.y ^ 1, p.rot, p.interleaved);
   const int lane0 = (lane_id() & ~(kPer - 1)) + (own0 >> 1), lane1 = (lane_id() & ~(kPer - 1)) + (own1 >> 1);
-  int at_token = -1;
-  float cos[8], sin[8];
   // a warp's rows run together (the shuffles below): all its lanes take part
   // until the last of its rows
-  for (int r_warp = (threadIdx.x & ~31) / kPer; r_warp < n_rows; r_warp += kSlots, r += kSlots) {
-    const bool live = r < n_rows;
+  for (int r_warp = (threadIdx.x & ~31) / kPer; r_warp < kv_rows; r_warp += kSlots, r += kSlots) {
     Row8 x = unpack8(next0), y = unpack8(next1);
-    fetch(r + kSlots);
-    const int k = live ? p.div_heads.div(r) : 0, h = r - k * heads;
+    fetch_kv(r + kSlots);
+    const bool live = r < kv_rows;
+    const int k = live ? p.div_kv.div(r) : 0, h = r - k * kv_heads;
     const PagedRow row = rows[k];
-    const bool is_q = h < hq;
-    const bool is_k = !is_q && h < hq + p.c.Hkv;
-    const int kvh = is_q ? 0 : (h - hq) - (is_k ? 0 : p.c.Hkv);
     const bool use = live && row.page >= 0;
-    if (use && (is_q || is_k) && ch.x * 8 < p.rot) {
-      if (k != at_token) {
-        at_token = k;
-        const float* at = p.rope + static_cast<size_t>(row.pos) * p.rot + (p.interleaved ? ch.x * 4 : ch.x * 8);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float4 c = *reinterpret_cast<const float4*>(at + 4 * u);
-          const float4 s = *reinterpret_cast<const float4*>(at + half + 4 * u);
-          cos[4 * u] = c.x; cos[4 * u + 1] = c.y; cos[4 * u + 2] = c.z; cos[4 * u + 3] = c.w;
-          sin[4 * u] = s.x; sin[4 * u + 1] = s.y; sin[4 * u + 2] = s.z; sin[4 * u + 3] = s.w;
-        }
-      }
-      if (p.interleaved) {  // pairs 8 i .. 8 i + 7: four in each chunk
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float a = x.x[2 * u], b = x.x[2 * u + 1], e = y.x[2 * u], f = y.x[2 * u + 1];
-          x.x[2 * u] = turn(a, b, cos[u], sin[u]);
-          x.x[2 * u + 1] = turn_back(b, a, cos[u], sin[u]);
-          y.x[2 * u] = turn(e, f, cos[4 + u], sin[4 + u]);
-          y.x[2 * u + 1] = turn_back(f, e, cos[4 + u], sin[4 + u]);
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float a = x.x[u], b = y.x[u];
-          x.x[u] = turn(a, b, cos[u], sin[u]);
-          y.x[u] = turn_back(b, a, cos[u], sin[u]);
-        }
-      }
-    }
-    if (use && is_q) {
-      __nv_bfloat16* to = p.q_out + ((static_cast<long long>(t0) + k) * p.H + h) * D;
-      *reinterpret_cast<uint4*>(to + ch.x * 8) = pack8(x);
-      *reinterpret_cast<uint4*>(to + ch.y * 8) = pack8(y);
+    const bool is_k = h < p.c.Hkv;
+    const int kvh = is_k ? h : h - p.c.Hkv;
+    if (use && is_k && turned) {
+      rope.load(p, k, row.pos, ch);
+      rope.apply(x, y, p.interleaved);
     }
     uint8_t* to = p.c.pages + (static_cast<size_t>(use ? row.page : 0) * p.c.Hkv + kvh) * 2 * half_bytes +
                   (is_k ? 0 : half_bytes);
     if constexpr (FP4) {
-      const float* factor = is_k ? p.c.k_scale : p.c.v_scale;
-      const bool cached = use && !is_q;
-      const float g = cached && factor ? factor[kvh] : 1.0f;
-      if (__any_sync(0xffffffffu, cached)) {
-        const float m0 = scale8(x, g), m1 = scale8(y, g);
-        const float a0 = __shfl_sync(0xffffffffu, m0, lane0), a1 = __shfl_sync(0xffffffffu, m1, lane0);
-        const float b0 = __shfl_sync(0xffffffffu, m0, lane1), b1 = __shfl_sync(0xffffffffu, m1, lane1);
-        const float o0 = own0 & 1 ? a1 : a0, o1 = own1 & 1 ? b1 : b0;
-        // (0 times each added: NaN where either is)
-        const uint32_t byte0 = scale_byte(fmaxf(m0, o0) + fmaf(m0, 0.0f, o0 * 0.0f));
-        const uint32_t byte1 = scale_byte(fmaxf(m1, o1) + fmaf(m1, 0.0f, o1 * 0.0f));
-        if (cached) {
-          uint8_t* codes = to + static_cast<size_t>(row.offset) * (D / 2);
-          uint8_t* scales = to + (static_cast<size_t>(D / 2) << p.c.page_shift) + row.offset * (D / 16);
-          *reinterpret_cast<uint32_t*>(codes + ch.x * 4) = codes8(x, byte0);
-          *reinterpret_cast<uint32_t*>(codes + ch.y * 4) = codes8(y, byte1);
-          if ((ch.x & 1) == 0) scales[ch.x >> 1] = static_cast<uint8_t>(byte0);
-          if ((ch.y & 1) == 0) scales[ch.y >> 1] = static_cast<uint8_t>(byte1);
-        }
-      }
-    } else if (use && !is_q) {
+      const float m0 = amax8(x), m1 = amax8(y);
+      const float a0 = __shfl_sync(0xffffffffu, m0, lane0), a1 = __shfl_sync(0xffffffffu, m1, lane0);
+      const float b0 = __shfl_sync(0xffffffffu, m0, lane1), b1 = __shfl_sync(0xffffffffu, m1, lane1);
+      const float block0 = max_abs(m0, own0 & 1 ? a1 : a0), block1 = max_abs(m1, own1 & 1 ? b1 : b0);
+      if (!use) continue;
+      const Factor f = factor_of(is_k ? p.c.k_scale : p.c.v_scale, kvh);
+      const uint32_t byte0 = scale_byte(block0, f), byte1 = scale_byte(block1, f);
+      const bool small = f.fits && fmaxf(block0, block1) < 0x1p60f;
+      uint8_t* codes = to + static_cast<size_t>(row.offset) * (D / 2);
+      uint8_t* scales = to + (static_cast<size_t>(D / 2) << p.c.page_shift) + row.offset * (D / 16);
+      *reinterpret_cast<uint32_t*>(codes + ch.x * 4) = codes8(x, f, small, byte0);
+      *reinterpret_cast<uint32_t*>(codes + ch.y * 4) = codes8(y, f, small, byte1);
+      if ((ch.x & 1) == 0) scales[ch.x >> 1] = static_cast<uint8_t>(byte0);
+      if ((ch.y & 1) == 0) scales[ch.y >> 1] = static_cast<uint8_t>(byte1);
+    } else if (use) {
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(to) + static_cast<size_t>(row.offset) * D;
       *reinterpret_cast<uint4*>(out + ch.x * 8) = pack8(x);
       *reinterpret_cast<uint4*>(out + ch.y * 8) = pack8(y);

@@ -378,8 +378,8 @@ size_t fa_paged_block_bytes(int format, int page_size, int d);
  * K and Q are rotated, V is not.  bf16 caches take the results rounded once.
  * 4-bit caches take, with y = x / g in fp32 and per 16 elements, the scale
  * s = e4m3(max |y| / 6) (at most 448) and the codes e2m1(y / s), to nearest,
- * ties to even; a scale that rounds to 0 stores zeros, a block with an
- * infinity or a NaN reads back as NaN.
+ * ties to even; a negative zero becomes zero, a scale that rounds to 0 stores
+ * zeros, a block with an infinity or a NaN reads back as NaN.
  */
 int fa_paged_append(const fa_paged_cache* cache, const void* k, long long k_row, long long k_head,
                     const void* v, long long v_row, long long v_head, const int* cu_new, int rows,

@@ -32,7 +32,7 @@ def quantise(x: np.ndarray, g: float):
         byte = nearest(np.abs(y).max(-1) / np.float32(6), E4M3)
         s = E4M3[byte].astype(np.float32)
         z = np.where(s[..., None] > 0, y / np.where(s > 0, s, np.float32(1))[..., None], np.float32(0))
-    code = nearest(np.abs(z), E2M1) + np.where(np.signbit(z), 8, 0)
+    code = nearest(np.abs(z), E2M1) + np.where(z < 0, 8, 0)
     code = np.where((bad | (byte == 0))[..., None], 0, code)
     return code.reshape(x.shape).astype(np.uint8), np.where(bad, 0x7F, byte).astype(np.uint8)
 

@@ -257,6 +257,39 @@ def test_append_and_read(fmt, d, page, rot, interleaved, Hkv, group, lens, new):
     assert torch.equal(got_v[:T].cpu(), v_read.to(torch.bfloat16))
 
 
+def test_every_scale():
+    """Each e4m3 scale there is, with elements on, just below and just above every border between its
+    codes: the codes of the definition, byte for byte."""
+    from exact_attention_98_gb300 import fa
+    from paged import E2M1, E4M3
+
+    d, T = 64, 0
+    rows = []
+    for s in E4M3[1:]:
+        # largest magnitude 6 s (its sixth is s exactly); the others around the borders
+        borders = np.float32((E2M1[1:] + E2M1[:-1]) / 2 * s)
+        x = np.concatenate([[6 * s], borders, np.nextafter(borders, np.float32(0))[:4],
+                            np.nextafter(borders, np.float32(np.inf))[3:]]).astype(np.float32)
+        rows.append(np.concatenate([x, np.zeros(16 - len(x), np.float32)]))
+    blocks = np.stack(rows)
+    # bf16 holds the borders times a scale (7 bits); what it rounds away from them stays a number to quantise
+    k = bf16(np.concatenate([blocks, -blocks, blocks[::-1], blocks], 1)).cuda()[:, None]
+    T = k.shape[0]
+    pages = fa.paged_pages(8, 1, 16, d, "fp4")
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([T], [0, T]))
+    for g in (None, 1.0, 0.7, 3.3e-7):
+        f = None if g is None else torch.tensor([g], device="cuda")
+        x = k if g is None else (k.float() * g).to(torch.bfloat16)
+        fa.paged_append(x, x, pages, table, lens, cu, k_scale=f, v_scale=f)
+        ok(fa)
+        raw = pages[:, 0, 0].cpu().numpy()
+        codes, scales = raw[:, : 16 * 32].reshape(-1, 32)[:T], raw[:, 16 * 32:].reshape(-1, 4)[:T]
+        want, byte = quantise(x[:, 0].float().cpu().numpy(), 1.0 if g is None else g)
+        assert np.array_equal(scales, byte)
+        assert np.array_equal(codes, want[:, 0::2] | (want[:, 1::2] << 4))
+
+
 def test_append_of_what_is_not_finite():
     """4 bits: a block with an infinity or a NaN reads back as NaN, its neighbours as they are."""
     bt = Batch("fp4", 64, 16, 1, [1], [1], scales=False)
