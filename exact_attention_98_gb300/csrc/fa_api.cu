@@ -678,6 +678,30 @@ SinkParts sink_parts(int B, int Hkv, int N, int d, int window, int sinks) {
   return s;
 }
 
+// How the main kernel cuts its last round: items (key tile of a key head) run one
+// per SM, in order; those of a last round that would leave SMs idle are cut into
+// as many parts as fill it, a query tile each at least.
+struct TileParts {
+  int from = 0, parts = 1;
+  size_t bytes = 0;
+};
+TileParts tile_parts(int B, int H, int Hkv, int N, int d, int window) {
+  TileParts t;
+  const int items = ((N + kBlockN - 1) / kBlockN) * B * Hkv;
+  const int sms = sm_count();
+  t.from = items;
+  if (sms <= 0) return t;
+  const int tail = items % sms;
+  if (tail == 0) return t;
+  const long long tiles = static_cast<long long>(H / Hkv) * ((window < N ? window : N) / kBlockM + 1);
+  const int parts = static_cast<int>(sms / tail < tiles ? sms / tail : tiles);
+  if (parts < 2) return t;
+  t.from = items - tail;
+  t.parts = parts;
+  t.bytes = round_up(static_cast<size_t>(tail) * parts * 2 * kBlockN * d * sizeof(float));
+  return t;
+}
+
 }  // namespace
 
 int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
@@ -724,7 +748,9 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
 size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   bool empty = false;
   if (check_window(B, H, Hkv, N, d, 1.0f, window, sinks, &empty) != FA_OK || empty) return 0;
-  return fa_bwd_workspace_bytes(B, H, N, d) + sink_parts(B, Hkv, N, d, window, sinks).bytes;
+  if (static_cast<long long>((N + kBlockN - 1) / kBlockN) * B * Hkv > 0x7fffffffLL) return 0;
+  return fa_bwd_workspace_bytes(B, H, N, d) + sink_parts(B, Hkv, N, d, window, sinks).bytes +
+         tile_parts(B, H, Hkv, N, d, window).bytes;
 }
 
 int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -737,11 +763,14 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
       !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return FA_ERR_INVALID_ARG;
+  const int BH = B * H, BHkv = B * Hkv;
+  if (static_cast<long long>((N + kBlockN - 1) / kBlockN) * BHkv > 0x7fffffffLL ||
+      static_cast<long long>(BHkv) * (2 * kMaxSinks) > 0x3fffffffLL)
+    return FA_ERR_UNSUPPORTED;
   const size_t need = fa_bwd_window_workspace_bytes(B, H, Hkv, N, d, window, sinks);
   if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0) return FA_ERR_WORKSPACE;
 
-  const int BH = B * H, BHkv = B * Hkv;
   const long long rows = static_cast<long long>(BH) * N;
   const SinkParts sp = sink_parts(B, Hkv, N, d, window, sinks);
   char* w = static_cast<char*>(workspace);
@@ -776,11 +805,21 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   p.sinks = sinks < N ? sinks : N;
   p.sink_rows = sp.sink_rows;
   p.sink_main = nullptr;
-  if (static_cast<long long>(p.n_kblk) * BHkv > 0x7fffffffLL ||
-      static_cast<long long>(BHkv) * (2 * kMaxSinks) > 0x7fffffffLL)
-    return FA_ERR_UNSUPPORTED;
+  const TileParts tp = tile_parts(B, H, Hkv, N, d, window);
+  p.split_from = tp.from;
+  p.split_parts = tp.parts;
+  p.tile_part = sink_part + sp.bytes / sizeof(float);
 
   WindowParams wp = {};
+  wp.tile_part = p.tile_part;
+  wp.split_from = tp.from;
+  wp.split_parts = tp.parts;
+  wp.n_kblk = p.n_kblk;
+  wp.dk = static_cast<__nv_bfloat16*>(dk);
+  wp.dv = static_cast<__nv_bfloat16*>(dv);
+  wp.N = N;
+  wp.BHkv = BHkv;
+  wp.scale = scale;
   if (sp.slots > 0) {
     wp.q = static_cast<const __nv_bfloat16*>(q);
     wp.k = static_cast<const __nv_bfloat16*>(k);
@@ -791,10 +830,6 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
     wp.dsum = dsum;
     wp.dq_acc = dq_acc;
     wp.sink_part = sink_part;
-    wp.dk = static_cast<__nv_bfloat16*>(dk);
-    wp.dv = static_cast<__nv_bfloat16*>(dv);
-    wp.N = N;
-    wp.BHkv = BHkv;
     wp.group = p.group;
     wp.window = p.window;
     wp.sinks = p.sinks;
@@ -803,7 +838,6 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
     wp.slot_rows = sp.slot_rows;
     wp.c = p.c;
     wp.log2e = p.log2e;
-    wp.scale = scale;
     p.sink_main = sink_part + static_cast<size_t>(sp.slots) * BHkv * 2 * sp.sink_rows * d;
     if (launch_window_pre(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
   } else if (launch_bwd_pre(o, dout, dsum, dq_acc, rows, d, s) != cudaSuccess) {
@@ -812,7 +846,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   if (timing_record(1, true, s) != cudaSuccess) return FA_ERR_CUDA;
   if (launch_bwd_window(p, d, s) != cudaSuccess) return FA_ERR_CUDA;
   if (timing_record(1, false, s) != cudaSuccess) return FA_ERR_CUDA;
-  if (sp.slots > 0 && launch_window_join(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
+  if ((sp.slots > 0 || tp.parts > 1) && launch_window_join(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
   if (launch_bwd_post(dq_acc, dq, rows * d, scale, s) != cudaSuccess) return FA_ERR_CUDA;
   return FA_OK;
 }

@@ -212,8 +212,14 @@ template <bool kWindow>
 struct QueryWalk {
   int i, bh;
   int i_first, i_last;
-  __device__ __forceinline__ QueryWalk(int i_first_, int i_last_, int bh0)
-      : i(i_first_), bh(bh0), i_first(i_first_), i_last(i_last_) {}
+  __device__ __forceinline__ QueryWalk(int i_first_, int i_last_, int bh0, int start)
+      : i(i_first_), bh(bh0), i_first(i_first_), i_last(i_last_) {
+    if constexpr (kWindow) {
+      const int per = i_last - i_first + 1;
+      bh += start / per;
+      i += start % per;
+    }
+  }
   __device__ __forceinline__ void next() {
     ++i;
     if constexpr (kWindow)
@@ -247,7 +253,16 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   // one head run in the same wave and add into the same dQ rows while those
   // are in L2; within a head the heaviest tile (causal: kt = 0) goes first.
   // Window: bh is the key head, bq0 its group's first query head.
-  const int blk = blockIdx.x;
+  // From split_from on an item is cut into split_parts parts of its query
+  // tiles, a CTA each, whose dK and dV are joined afterwards.
+  int blk = blockIdx.x;
+  int part = -1;
+  if constexpr (kWindow) {
+    if (blk >= p.split_from) {
+      part = (blk - p.split_from) % p.split_parts;
+      blk = p.split_from + (blk - p.split_from) / p.split_parts;
+    }
+  }
   const int bh = blk / p.n_kblk;
   const int kt = blk % p.n_kblk;
   const int k0 = kt * kBlockN;
@@ -255,7 +270,14 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   const int i_first = kWindow || p.causal ? kt : 0;
   // (window <= N <= 2^30, so the sum is an int)
   const int i_last = kWindow ? min(n_qtiles - 1, (k0 + kBlockN - 2 + p.window) / kBlockM) : n_qtiles - 1;
-  const int n_iter = (kWindow ? p.group : 1) * (i_last - i_first + 1);
+  int n_iter = (kWindow ? p.group : 1) * (i_last - i_first + 1);
+  int it0 = 0;  // the part's first
+  if constexpr (kWindow) {
+    if (part >= 0) {
+      it0 = static_cast<int>(static_cast<long long>(n_iter) * part / p.split_parts);
+      n_iter = static_cast<int>(static_cast<long long>(n_iter) * (part + 1) / p.split_parts) - it0;
+    }
+  }
   const int bq0 = kWindow ? bh * p.group : bh;
   using Walk = QueryWalk<kWindow>;
 
@@ -309,7 +331,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         }
       }
       int issued = 0;
-      Walk walk(i_first, i_last, bq0);
+      Walk walk(i_first, i_last, bq0, it0);
       for (int it = 0; it < n_iter; ++it, walk.next()) {
         const int s = it % C::kStages;
         const int use = it / C::kStages;
@@ -445,7 +467,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         return true;
       };
       bool ok = mbar_wait(bar(C::kBarKV), 0, ctl, kSiteKV);
-      if (C::kEarlyS && ok) ok = issue_s(0);
+      if (C::kEarlyS && ok && (!kWindow || n_iter > 0)) ok = issue_s(0);
       for (int it = 0; ok && it < n_iter; ++it) {
         const int s = it % C::kStages;
         const uint32_t q_s = sbase + C::kQOff + s * C::kTileBytes;
@@ -499,7 +521,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       // floats of one query row per reduction
       const int dcol = quarter * 32 + lane;
       const uint32_t t_dqt = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + C::kColDP;
-      Walk walk(i_first, i_last, bq0);
+      Walk walk(i_first, i_last, bq0, it0);
       for (int it = 0; it < n_iter; ++it, walk.next()) {
         bool ok = mbar_wait(bar(C::kBarDQFull), it & 1, ctl, kSiteDQFull);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -533,7 +555,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         }
       }
     } else {
-    Walk walk(i_first, i_last, bq0);
+    Walk walk(i_first, i_last, bq0, it0);
     for (int it = 0; it < n_iter; ++it, walk.next()) {
       const int s = it % C::kStages;
       bool ok = mbar_wait(bar(C::kBarDQFull), it & 1, ctl, kSiteDQFull);
@@ -607,7 +629,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const f32x2 c2 = f2_pack(p.c, p.c);
     bool ok = true;
-    Walk walk(i_first, i_last, bq0);
+    Walk walk(i_first, i_last, bq0, it0);
     for (int it = 0; it < n_iter; ++it, walk.next()) {
       const int s = it % C::kStages;
       const int i = walk.i;
@@ -655,6 +677,15 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         p0 = ex2_mufu(x0);
         p1 = ex2_mufu(x1);
       };
+      // Window: dS is formed from P as computed instead of as rounded for the dV
+      // product: P stays in the registers of S (dP then comes in halves).
+      // The rounding of P would add to dQ and dK as much as dS's own.
+      auto keep_pair = [&](int ch, int e2, float p0, float p1) {
+        if constexpr (kWindow) {
+          sr[ch][2 * e2] = __float_as_uint(p0);
+          sr[ch][2 * e2 + 1] = __float_as_uint(p1);
+        }
+      };
       if (kWindow && diag) {
         // the key sees the query columns [lo, lo + window) of the tile
         const int lo = (kt - i) * kBlockM + kr - wg * 64;
@@ -667,9 +698,10 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           for (int e2 = 0; e2 < 16; ++e2) {
             float p0, p1;
             exp_pair(ch, e2, p0, p1);
-            if (!(seen & (1u << (2 * e2)))) p0 = 0.0f;
-            if (!(seen & (2u << (2 * e2)))) p1 = 0.0f;
+            if (!(seen & (1u << (2 * e2))) || !row_valid) p0 = 0.0f;
+            if (!(seen & (2u << (2 * e2))) || !row_valid) p1 = 0.0f;
             pw[ch * 16 + e2] = pack_bf16x2(p0, p1);
+            keep_pair(ch, e2, p0, p1);
           }
         }
       } else if (diag) {  // uniform: only the diagonal tile pays for the mask
@@ -691,10 +723,12 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           for (int e2 = 0; e2 < 16; ++e2) {
             float p0, p1;
             exp_pair(ch, e2, p0, p1);
+            if (kWindow && !row_valid) p0 = p1 = 0.0f;
             pw[ch * 16 + e2] = pack_bf16x2(p0, p1);
+            keep_pair(ch, e2, p0, p1);
           }
       }
-      if (!row_valid) {
+      if (!kWindow && !row_valid) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) pw[e] = 0u;
       }
@@ -715,25 +749,33 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       ok = mbar_wait(bar(C::kBarDPFull), it & 1, ctl, kSiteDPFull);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
-      uint32_t dr[2][32];
-      tmem_ld32(lane_base + C::kColDP + wg * 64, dr[0]);
-      tmem_ld32(lane_base + C::kColDP + wg * 64 + 32, dr[1]);
-      tmem_ld_wait(dr[0]);
-      reg_fence(dr[1]);
+      uint32_t dr[kWindow ? 1 : 2][32];
+      if constexpr (!kWindow) {
+        tmem_ld32(lane_base + C::kColDP + wg * 64, dr[0]);
+        tmem_ld32(lane_base + C::kColDP + wg * 64 + 32, dr[1]);
+        tmem_ld_wait(dr[0]);
+        reg_fence(dr[1]);
+      }
       uint32_t dsw[32];
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
+        if constexpr (kWindow) {
+          tmem_ld32(lane_base + C::kColDP + wg * 64 + ch * 32, dr[0]);
+          tmem_ld_wait(dr[0]);
+        }
 #pragma unroll
         for (int e2 = 0; e2 < 16; ++e2) {
           float a0, a1;
-          f32x2 dp = f2_pack(__uint_as_float(dr[ch][2 * e2]), __uint_as_float(dr[ch][2 * e2 + 1]));
+          uint32_t (&dc)[32] = dr[kWindow ? 0 : ch];
+          f32x2 dp = f2_pack(__uint_as_float(dc[2 * e2]), __uint_as_float(dc[2 * e2 + 1]));
           if constexpr (C::kRowLse) {
             const float4 d4 = rd4[ch * 8 + (e2 >> 1)];
             dp = f2_add(dp, (e2 & 1) ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y));
           }
-          f2_unpack(f2_mul(dp, f2_pack(__uint_as_float(pw[ch * 16 + e2] << 16),
-                                       __uint_as_float(pw[ch * 16 + e2] & 0xFFFF0000u))),
-                    a0, a1);
+          const f32x2 pp = kWindow ? f2_pack(__uint_as_float(sr[ch][2 * e2]), __uint_as_float(sr[ch][2 * e2 + 1]))
+                                   : f2_pack(__uint_as_float(pw[ch * 16 + e2] << 16),
+                                             __uint_as_float(pw[ch * 16 + e2] & 0xFFFF0000u));
+          f2_unpack(f2_mul(dp, pp), a0, a1);
           dsw[ch * 16 + e2] = pack_bf16x2(a0, a1);
         }
         uint32_t w[16];
@@ -795,12 +837,19 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         tmem_ld_wait(r[0]);
         reg_fence(r[1]);
         if constexpr (kWindow) {
-          // The first tokens also get the rows of the queries whose windows
-          // have left them: their sums are joined in fp32 afterwards.
-          if (p.sink_main != nullptr && kt == 0 && kr < p.sinks) {
-            float4* dst = reinterpret_cast<float4*>(
-                p.sink_main +
-                ((static_cast<size_t>(bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D + h * 64);
+          // Rows that are joined in fp32 afterwards: all of a part's (zeros if
+          // it has no query tile), and the first tokens', which also get the
+          // queries whose windows have left them.
+          if (n_iter == 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[0][e] = r[1][e] = 0u;
+          }
+          const bool sink = p.sink_main != nullptr && kt == 0 && kr < p.sinks;
+          if (part >= 0 || sink) {
+            float* row = part >= 0 ? p.tile_part + ((static_cast<size_t>(static_cast<int>(blockIdx.x) - p.split_from) * 2 +
+                                                     (wg == 0 ? 1 : 0)) * kBlockN + kr) * D
+                                   : p.sink_main + ((static_cast<size_t>(bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D;
+            float4* dst = reinterpret_cast<float4*>(row + h * 64);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const uint32_t* x = &r[c >> 3][(c & 7) * 4];
@@ -821,7 +870,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       }
       fence_proxy_async_smem();
       named_bar_sync(C::kEpiBarrier0 + wg, kBlockM);
-      if (kr == 0) {
+      if (kr == 0 && part < 0) {
         const CUtensorMap* map = wg == 0 ? &p.tm_dv : &p.tm_dk;
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h)
@@ -868,7 +917,8 @@ cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
                                                 : fa_bwd_kernel<D>;
   cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
-  const long long blocks = static_cast<long long>(p.n_kblk) * p.BH;
+  long long blocks = static_cast<long long>(p.n_kblk) * p.BH;
+  if (kWindow) blocks = p.split_from + (blocks - p.split_from) * p.split_parts;
   err = launch_dependent(kernel, dim3(static_cast<unsigned int>(blocks)), dim3(C::kThreads),
                          C::kSmemBytes, stream, p);
   if (err != cudaSuccess) return err;

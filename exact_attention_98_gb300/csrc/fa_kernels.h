@@ -130,6 +130,11 @@ struct BwdParams {
   int sinks;
   int sink_rows;
   float* sink_main;
+  // Items (key tile of a key head) from split_from on are cut into split_parts
+  // parts, whose fp32 dK (unscaled) and dV go to tile_part [part, 2, 128, d].
+  int split_from;
+  int split_parts;
+  float* tile_part;
 };
 
 // What the sliding-window backward does beside its main kernel (fa_window.cu):
@@ -145,6 +150,8 @@ struct WindowParams {
   float* dsum;        // [BHkv * group, N]
   float* dq_acc;      // [BHkv * group, N, d]
   float* sink_part;   // [slots + 1, BHkv, 2 (dK, dV), sink_rows, d]; the last slot is the main kernel's
+  const float* tile_part;  // the main kernel's split items (BwdParams)
+  int split_from, split_parts, n_kblk;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   int N;
@@ -281,7 +288,8 @@ cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream);
 // Before it, where queries see first tokens that their windows have left: D, and
 // those pairs' share of dQ in the accumulator, of dK and dV in sink_part.
 cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream);
-// After it: the first tokens' dK and dV rows from all parts.
+// After it: the first tokens' dK and dV rows, and those of split items, from all
+// their parts.
 cudaError_t launch_window_join(const WindowParams& p, int d, cudaStream_t stream);
 // The same kernel computing dK and dV only (p.tm_dq, p.dq_acc and p.dq_part
 // unused): the deterministic mode's first pass.

@@ -12,8 +12,8 @@
 // m16n8k16 mma.sync, whose operands never leave registers:
 //   S = Q K_s^T, dP = dO V_s^T, P = exp2(c S - LSE log2 e), dS = P (dP - D),
 //   dQ = dS K_s, dK_s += dS^T Q, dV_s += P^T dO
-// (dS without the softmax scale, as in the main kernel).  P and dS are rounded
-// to bf16 for the products, as there.  The lanes of a quad take d in
+// (dS without the softmax scale, as in the main kernel).  dS and the P of the dV
+// product are rounded to bf16, as there.  The lanes of a quad take d in
 // runs of D/4, so that Q, dO and O are read 16 bytes at a time.
 //
 // A key head's queries are cut into parts, each with dK_s and dV_s of its own;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
           const float lse = row < p.N ? p.lse[head_row + row] * p.log2e : 0.0f;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
-            float pe[2], de[2];
+            float pe[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int key = key0 + nt * 8 + 2 * c + e;
@@ -163,9 +163,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
               pe[e] = seen ? ex2_mufu(fmaf(s[nt][2 * r + e], p.c, -lse)) : 0.0f;
             }
             pp[nt][r] = pack_bf16x2(pe[0], pe[1]);
-            de[0] = bf16_lo(pp[nt][r]) * (dp[nt][2 * r] - dsum[r]);
-            de[1] = bf16_hi(pp[nt][r]) * (dp[nt][2 * r + 1] - dsum[r]);
-            dd[nt][r] = pack_bf16x2(de[0], de[1]);
+            dd[nt][r] = pack_bf16x2(pe[0] * (dp[nt][2 * r] - dsum[r]), pe[1] * (dp[nt][2 * r + 1] - dsum[r]));
           }
         }
         // dQ = dS K_s (d in order)
@@ -246,20 +244,46 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
   }
 }
 
-// grid sinks * 2 * BHkv: a first token's row of dK (times the softmax scale) or dV
-// from all its parts; the thread groups take every kGroups-th part.
+// Rows that come in parts.  Blocks below sinks * 2 * BHkv (when there are parts of
+// first tokens): a first token's row of dK (times the softmax scale) or dV;
+// the thread groups take every kGroups-th part.  Blocks from there on: 256 / d
+// rows of a split item's dK or dV, one per thread group.
 template <int D>
 __global__ void __launch_bounds__(256) fa_window_join_kernel(const WindowParams p) {
   constexpr int kGroups = 256 / D;
   __shared__ float part[kGroups][D];
   grid_dependency_wait();
   const int col = threadIdx.x % D, grp = threadIdx.x / D;
+  const int sink_blocks = p.slots > 0 ? p.sinks * 2 * p.BHkv : 0;
+  // element (row, col) of part k of an item, and whether an item is in parts
+  auto tile_row = [&](int item, int k, int which, int row) {
+    return p.tile_part[((static_cast<size_t>((item - p.split_from) * p.split_parts + k) * 2 + which) * kBlockN + row) * D + col];
+  };
+  if (static_cast<int>(blockIdx.x) >= sink_blocks) {
+    const int rest = static_cast<int>(blockIdx.x) - sink_blocks;
+    constexpr int kPerItem = 2 * kBlockN / kGroups;  // blocks of an item
+    const int item = p.split_from + rest / kPerItem;
+    const int at = rest % kPerItem * kGroups + grp;
+    const int which = at / kBlockN, row = at % kBlockN;
+    const int bkv = item / p.n_kblk, key = item % p.n_kblk * kBlockN + row;
+    if (key >= p.N || (p.slots > 0 && key < p.sinks)) return;
+    float x = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < p.split_parts; ++k) x += tile_row(item, k, which, row);
+    __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<size_t>(bkv) * p.N + key) * D + col;
+    *out = __float2bfloat16_rn(which == 0 ? x * p.scale : x);
+    return;
+  }
   const int key = blockIdx.x % p.sinks, which = (blockIdx.x / p.sinks) & 1, bkv = blockIdx.x / p.sinks / 2;
   const size_t stride = static_cast<size_t>(p.BHkv) * 2 * p.sink_rows * D;
   const float* from = p.sink_part + ((static_cast<size_t>(bkv) * 2 + which) * p.sink_rows + key) * D + col;
+  const int item = bkv * p.n_kblk;  // its first key tile
+  const bool split = item >= p.split_from;
   float x = 0.0f;
 #pragma unroll 8
-  for (int s = grp; s <= p.slots; s += kGroups) x += from[s * stride];
+  for (int s = grp; s < p.slots + (split ? 0 : 1); s += kGroups) x += from[s * stride];
+  if (split)
+    for (int k = grp; k < p.split_parts; k += kGroups) x += tile_row(item, k, which, key);
   part[grp][col] = x;
   __syncthreads();
   if (grp != 0) return;
@@ -279,7 +303,9 @@ cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream)
 }
 
 cudaError_t launch_window_join(const WindowParams& p, int d, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned int>(p.sinks) * 2u * static_cast<unsigned int>(p.BHkv));
+  const unsigned int items = static_cast<unsigned int>(p.n_kblk * p.BHkv - p.split_from);
+  const dim3 grid((p.slots > 0 ? static_cast<unsigned int>(p.sinks) * 2u * static_cast<unsigned int>(p.BHkv) : 0u) +
+                  items * (2u * kBlockN / (256u / static_cast<unsigned int>(d))));
   const cudaError_t err = launch_dependent(d == 128 ? fa_window_join_kernel<128> : fa_window_join_kernel<64>, grid,
                                            dim3(256), 0, stream, p);
   return err != cudaSuccess ? err : launched(1);

@@ -301,9 +301,11 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
  * summed over the query heads of the group (in fp32, in an order that does not
  * vary: bit-identical from run to run; dq within the order of its fp32
  * additions).
- *   workspace : fa_bwd_window_workspace_bytes() bytes, 256-byte aligned:
- *               fa_bwd's, then, where queries see first tokens that their
- *               windows have left, the parts of those tokens' dK and dV
+ *   workspace : fa_bwd_window_workspace_bytes() bytes for the current device,
+ *               256-byte aligned: fa_bwd's, then, where queries see first tokens
+ *               that their windows have left, the parts of those tokens' dK
+ *               and dV, then the parts of key tiles whose query tiles are
+ *               split over SMs that a last round of work would leave idle
  */
 size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks);
 int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -481,7 +483,7 @@ int fa_timing_last_ms(int kernel, float* ms);
  * fa_bwd_deterministic three; fa_fwd_fp8 three (two preparation kernels and
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
  * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three,
- * or four where queries see first tokens that their windows have left;
+ * or four where dK and dV rows come in parts (see there);
  * fa_paged_append and fa_paged_read one;
  * fa_fwd_paged two (the forward, then the join of segments that several CTAs
  * shared).
