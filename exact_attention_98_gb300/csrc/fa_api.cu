@@ -819,7 +819,10 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   wp.dv = static_cast<__nv_bfloat16*>(dv);
   wp.N = N;
   wp.BHkv = BHkv;
+  wp.group = p.group;
   wp.scale = scale;
+  wp.dq_acc = dq_acc;
+  wp.dq = static_cast<__nv_bfloat16*>(dq);
   if (sp.slots > 0) {
     wp.q = static_cast<const __nv_bfloat16*>(q);
     wp.k = static_cast<const __nv_bfloat16*>(k);
@@ -828,9 +831,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
     wp.dout = static_cast<const __nv_bfloat16*>(dout);
     wp.lse = lse;
     wp.dsum = dsum;
-    wp.dq_acc = dq_acc;
     wp.sink_part = sink_part;
-    wp.group = p.group;
     wp.window = p.window;
     wp.sinks = p.sinks;
     wp.sink_rows = sp.sink_rows;
@@ -846,8 +847,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   if (timing_record(1, true, s) != cudaSuccess) return FA_ERR_CUDA;
   if (launch_bwd_window(p, d, s) != cudaSuccess) return FA_ERR_CUDA;
   if (timing_record(1, false, s) != cudaSuccess) return FA_ERR_CUDA;
-  if ((sp.slots > 0 || tp.parts > 1) && launch_window_join(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
-  if (launch_bwd_post(dq_acc, dq, rows * d, scale, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_window_post(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
   return FA_OK;
 }
 

@@ -149,6 +149,7 @@ struct WindowParams {
   const float* lse;   // [BHkv * group, N]
   float* dsum;        // [BHkv * group, N]
   float* dq_acc;      // [BHkv * group, N, d]
+  __nv_bfloat16* dq;
   float* sink_part;   // [slots + 1, BHkv, 2 (dK, dV), sink_rows, d]; the last slot is the main kernel's
   const float* tile_part;  // the main kernel's split items (BwdParams)
   int split_from, split_parts, n_kblk;
@@ -165,6 +166,7 @@ struct WindowParams {
   float c;        // scale * log2(e)
   float log2e;
   float scale;
+  int sink_blocks, tile_blocks;  // set by launch_window_post
 };
 
 // Backward by CTA pairs (d = 128): a cluster of two CTAs owns two
@@ -288,9 +290,9 @@ cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream);
 // Before it, where queries see first tokens that their windows have left: D, and
 // those pairs' share of dQ in the accumulator, of dK and dV in sink_part.
 cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream);
-// After it: the first tokens' dK and dV rows, and those of split items, from all
-// their parts.
-cudaError_t launch_window_join(const WindowParams& p, int d, cudaStream_t stream);
+// After it: dQ as bf16, and the first tokens' dK and dV rows and those of split
+// items from all their parts.
+cudaError_t launch_window_post(WindowParams p, int d, cudaStream_t stream);
 // The same kernel computing dK and dV only (p.tm_dq, p.dq_acc and p.dq_part
 // unused): the deterministic mode's first pass.
 cudaError_t launch_bwd_dkdv(const BwdParams& p, int d, cudaStream_t stream);

@@ -17,8 +17,8 @@
 // runs of D/4, so that Q, dO and O are read 16 bytes at a time.
 //
 // A key head's queries are cut into parts, each with dK_s and dV_s of its own;
-// fa_window_join adds the parts and the main kernel's rows in a fixed order, so
-// dK and dV have the same bits from run to run.
+// the kernel after the main one adds the parts and the main kernel's rows in a
+// fixed order, so dK and dV have the same bits from run to run.
 #include "fa_device.cuh"
 #include "fa_kernels.h"
 
@@ -26,12 +26,16 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kKeys = 16;  // keys of a pass
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
 }
 
 // An 8x8 block of 16-bit values (lane (g, c): row g, columns 2c, 2c + 1) transposed.
@@ -46,10 +50,12 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 // grid slots * BHkv.  A warp takes 16 rows of one query head at a time; lane
 // (g, c) their rows g and g + 8, and of each the elements [c D/4, (c+1) D/4).
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const WindowParams p) {
+// NT: tiles of 8 first tokens in a pass over the rows.
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kSteps = D / 16;
-  constexpr int kPitch = D + 8;  // of a key row in shared memory: no bank conflicts
+  constexpr int kKeys = 8 * NT;    // keys of a pass
+  constexpr int kPitch = D + 8;    // of a key row in shared memory: no bank conflicts
   __shared__ __align__(16) __nv_bfloat16 ks[kKeys * kPitch];
   __shared__ __align__(16) __nv_bfloat16 vs[kKeys * kPitch];
   __shared__ __align__(16) float sum[kWarps][kKeys][D];
@@ -60,8 +66,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
 
   const int row_begin = slot * p.slot_rows;
   const int row_end = min(p.N, row_begin + p.slot_rows);
-  for (int kb = 0; kb < p.sink_rows / kKeys; ++kb) {
-    const int key0 = kb * kKeys;
+  for (int key0 = 0; key0 < p.sinks; key0 += kKeys) {
     __syncthreads();  // the pass before has read ks, vs and sum
     for (int i = threadIdx.x; i < kKeys * D / 8; i += 32 * kWarps) {
       const int r = i / (D / 8), col = (i % (D / 8)) * 8;
@@ -75,18 +80,22 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
       *reinterpret_cast<uint4*>(vs + r * kPitch + col) = b;
     }
     __syncthreads();
-    float dk[2 * kSteps][4], dv[2 * kSteps][4];
+    // dK_s^T and dV_s^T: keys 8 nt + 2c + {0, 1} (e & 1) at d(g) + 4 k (+ 2 for e >> 1),
+    // d(g) = (g / 2) D/4 + g % 2
+    float dk[kSteps][NT][4], dv[kSteps][NT][4];
 #pragma unroll
-    for (int j = 0; j < 2 * kSteps; ++j)
+    for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dk[j][e] = dv[j][e] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dk[k][nt][e] = dv[k][nt][e] = 0.0f;
 
     for (int h = 0; h < p.group; ++h) {
       const size_t head_row = (static_cast<size_t>(bkv) * p.group + h) * p.N;
       for (int r0 = row_begin + warp * 16; r0 < row_end; r0 += kWarps * 16) {
         // any pair of these rows with keys of this pass?
         const bool far = min(r0 + 15, p.N - 1) - key0 >= p.window;
-        if (kb > 0 && !far) continue;
+        if (key0 > 0 && !far) continue;
         uint32_t qa[kSteps][4], da[kSteps][4];
         float dsum[2];
 #pragma unroll
@@ -102,7 +111,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
             if (in && far) x = *reinterpret_cast<const uint4*>(p.q + at + 8 * i);
             qa[2 * i][r] = x.x; qa[2 * i][2 + r] = x.y; qa[2 * i + 1][r] = x.z; qa[2 * i + 1][2 + r] = x.w;
             da[2 * i][r] = y.x; da[2 * i][2 + r] = y.y; da[2 * i + 1][r] = y.z; da[2 * i + 1][2 + r] = y.w;
-            if (kb == 0) {
+            if (key0 == 0) {
               uint4 o = make_uint4(0u, 0u, 0u, 0u);
               if (in) o = *reinterpret_cast<const uint4*>(p.o + at + 8 * i);
               const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, yw[4] = {y.x, y.y, y.z, y.w};
@@ -113,12 +122,12 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
               }
             }
           }
-          if (kb == 0) {
+          if (key0 == 0) {
             dsum[r] += __shfl_xor_sync(0xffffffffu, dsum[r], 1);
             dsum[r] += __shfl_xor_sync(0xffffffffu, dsum[r], 2);
             if (in && c == 0) p.dsum[head_row + row] = dsum[r];
           } else {
-            dsum[r] = in ? p.dsum[head_row + row] : 0.0f;  // written by this thread's quad in pass 0
+            dsum[r] = in ? p.dsum[head_row + row] : 0.0f;  // written by this block in its first pass
           }
         }
         float* acc[2];
@@ -134,9 +143,9 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
           continue;
         }
         // S and dP: key key0 + 8 nt + 2c + {0, 1} of rows g (0, 1) and g + 8 (2, 3)
-        float s[2][4], dp[2][4];
+        float s[NT][4], dp[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[nt][e] = dp[nt][e] = 0.0f;
 #pragma unroll
@@ -148,13 +157,13 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
             mma_bf16(dp[nt], da[k], vv.x, vv.y);
           }
         }
-        uint32_t pp[2][2], dd[2][2];  // P and dS as bf16 pairs: [nt][row]
+        uint32_t pp[NT][2], dd[NT][2];  // P and dS as bf16 pairs: [nt][row]
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = r0 + g + 8 * r;
           const float lse = row < p.N ? p.lse[head_row + row] * p.log2e : 0.0f;
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
+          for (int nt = 0; nt < NT; ++nt) {
             float pe[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -166,51 +175,59 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
             dd[nt][r] = pack_bf16x2(pe[0] * (dp[nt][2 * r] - dsum[r]), pe[1] * (dp[nt][2 * r + 1] - dsum[r]));
           }
         }
-        // dQ = dS K_s (d in order)
-        {
-          const uint32_t a[4] = {dd[0][0], dd[0][1], dd[1][0], dd[1][1]};
-          const uint32_t row_s = smem_u32(ks) + ((lane & 15) * kPitch + (lane >> 4) * 8) * 2;
+        // dQ = dS K_s (d in order), 16 columns at a time
 #pragma unroll
-          for (int j = 0; j < 2 * kSteps; j += 2) {
-            uint32_t b[4];
+        for (int j = 0; j < 2 * kSteps; j += 2) {
+          uint32_t b[2 * NT];  // keys 0-7 (and 8-15) of columns 8j.., then of the next 8
+          const uint32_t row_s =
+              smem_u32(ks) + (NT == 2 ? (lane & 15) * kPitch + (lane >> 4) * 8 : (lane & 7) * kPitch + ((lane >> 3) & 1) * 8) * 2;
+          if constexpr (NT == 2)
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
                          : "r"(row_s + j * 16)
                          : "memory");
+          else
+            asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                         : "=r"(b[0]), "=r"(b[1])
+                         : "r"(row_s + j * 16)
+                         : "memory");
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              if (kb > 0) {
-                const float2 y0 = in0 ? *reinterpret_cast<const float2*>(acc[0] + 8 * (j + u)) : make_float2(0.f, 0.f);
-                const float2 y1 = in1 ? *reinterpret_cast<const float2*>(acc[1] + 8 * (j + u)) : make_float2(0.f, 0.f);
-                x[0] = y0.x; x[1] = y0.y; x[2] = y1.x; x[3] = y1.y;
-              }
-              mma_bf16(x, a, b[2 * u], b[2 * u + 1]);
-              if (in0) *reinterpret_cast<float2*>(acc[0] + 8 * (j + u)) = make_float2(x[0], x[1]);
-              if (in1) *reinterpret_cast<float2*>(acc[1] + 8 * (j + u)) = make_float2(x[2], x[3]);
+          for (int u = 0; u < 2; ++u) {
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (key0 > 0) {
+              const float2 y0 = in0 ? *reinterpret_cast<const float2*>(acc[0] + 8 * (j + u)) : make_float2(0.f, 0.f);
+              const float2 y1 = in1 ? *reinterpret_cast<const float2*>(acc[1] + 8 * (j + u)) : make_float2(0.f, 0.f);
+              x[0] = y0.x; x[1] = y0.y; x[2] = y1.x; x[3] = y1.y;
             }
+            if constexpr (NT == 2) {
+              const uint32_t a[4] = {dd[0][0], dd[0][1], dd[1][0], dd[1][1]};
+              mma_bf16(x, a, b[2 * u], b[2 * u + 1]);
+            } else {
+              mma_bf16_k8(x, dd[0][0], dd[0][1], b[u]);
+            }
+            if (in0) *reinterpret_cast<float2*>(acc[0] + 8 * (j + u)) = make_float2(x[0], x[1]);
+            if (in1) *reinterpret_cast<float2*>(acc[1] + 8 * (j + u)) = make_float2(x[2], x[3]);
           }
         }
-        // dK_s += dS^T Q, dV_s += P^T dO: the n-tile of step k, half u holds
-        // d = c' D/4 + 4 k + 2 u + e at its column 2 c' + e
-        {
-          uint32_t at[4], pt[4];
+        // dK_s^T += Q^T dS, dV_s^T += dO^T P: 16 elements of d by 8 keys
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              at[2 * r + nt] = transpose8x8(dd[nt][r]);
-              pt[2 * r + nt] = transpose8x8(pp[nt][r]);
-            }
+          for (int r = 0; r < 2; ++r) {
+            dd[nt][r] = transpose8x8(dd[nt][r]);
+            pp[nt][r] = transpose8x8(pp[nt][r]);
+          }
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < kSteps; ++k) {
+          const uint32_t qt[4] = {transpose8x8(qa[k][0]), transpose8x8(qa[k][2]), transpose8x8(qa[k][1]),
+                                  transpose8x8(qa[k][3])};
+          const uint32_t dt[4] = {transpose8x8(da[k][0]), transpose8x8(da[k][2]), transpose8x8(da[k][1]),
+                                  transpose8x8(da[k][3])};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t q0 = transpose8x8(qa[k][2 * u]), q1 = transpose8x8(qa[k][2 * u + 1]);
-              mma_bf16(dk[2 * k + u], at, q0, q1);
-              const uint32_t d0 = transpose8x8(da[k][2 * u]), d1 = transpose8x8(da[k][2 * u + 1]);
-              mma_bf16(dv[2 * k + u], pt, d0, d1);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(dk[k][nt], qt, dd[nt][0], dd[nt][1]);
+            mma_bf16(dv[k][nt], dt, pp[nt][0], pp[nt][1]);
+          }
         }
       }
     }
@@ -222,13 +239,11 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float* x = which == 0 ? dk[2 * k + u] : dv[2 * k + u];
-            *reinterpret_cast<float2*>(&sum[warp][g + 8 * r][c * (D / 4) + 4 * k + 2 * u]) =
-                make_float2(x[2 * r], x[2 * r + 1]);
-          }
+          for (int e = 0; e < 4; ++e)
+            sum[warp][nt * 8 + 2 * c + (e & 1)][(g >> 1) * (D / 4) + 4 * k + 2 * (e >> 1) + (g & 1)] =
+                which == 0 ? dk[k][nt][e] : dv[k][nt][e];
       __syncthreads();
       float* out = p.sink_part + (((static_cast<size_t>(slot) * p.BHkv + bkv) * 2 + which) * p.sink_rows + key0) * D;
       for (int i = threadIdx.x * 4; i < kKeys * D; i += 32 * kWarps * 4) {
@@ -244,69 +259,108 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const Window
   }
 }
 
-// Rows that come in parts.  Blocks below sinks * 2 * BHkv (when there are parts of
-// first tokens): a first token's row of dK (times the softmax scale) or dV;
-// the thread groups take every kGroups-th part.  Blocks from there on: 256 / d
-// rows of a split item's dK or dV, one per thread group.
+// After the main kernel, three kinds of blocks:
+//   sink_blocks      a first token's row of dK (times the softmax scale) or dV
+//                    from all its parts; the thread groups take every
+//                    kGroups-th part
+//   tile_blocks      16 rows of a split item's dK or dV from its parts
+//   the others       dQ = scale * its accumulator, as bf16, 32 elements a thread
+//                    per step, all loads first
 template <int D>
-__global__ void __launch_bounds__(256) fa_window_join_kernel(const WindowParams p) {
+__global__ void __launch_bounds__(256) fa_window_post_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kGroups = 256 / D;
   __shared__ float part[kGroups][D];
   grid_dependency_wait();
-  const int col = threadIdx.x % D, grp = threadIdx.x / D;
-  const int sink_blocks = p.slots > 0 ? p.sinks * 2 * p.BHkv : 0;
-  // element (row, col) of part k of an item, and whether an item is in parts
-  auto tile_row = [&](int item, int k, int which, int row) {
-    return p.tile_part[((static_cast<size_t>((item - p.split_from) * p.split_parts + k) * 2 + which) * kBlockN + row) * D + col];
-  };
-  if (static_cast<int>(blockIdx.x) >= sink_blocks) {
-    const int rest = static_cast<int>(blockIdx.x) - sink_blocks;
-    constexpr int kPerItem = 2 * kBlockN / kGroups;  // blocks of an item
-    const int item = p.split_from + rest / kPerItem;
-    const int at = rest % kPerItem * kGroups + grp;
-    const int which = at / kBlockN, row = at % kBlockN;
-    const int bkv = item / p.n_kblk, key = item % p.n_kblk * kBlockN + row;
-    if (key >= p.N || (p.slots > 0 && key < p.sinks)) return;
+  int blk = static_cast<int>(blockIdx.x);
+  if (blk < p.sink_blocks) {
+    const int col = threadIdx.x % D, grp = threadIdx.x / D;
+    const int key = blk % p.sinks, which = (blk / p.sinks) & 1, bkv = blk / p.sinks / 2;
+    const size_t stride = static_cast<size_t>(p.BHkv) * 2 * p.sink_rows * D;
+    const float* from = p.sink_part + ((static_cast<size_t>(bkv) * 2 + which) * p.sink_rows + key) * D + col;
+    const int item = bkv * p.n_kblk;  // its first key tile
+    const bool split = item >= p.split_from;
     float x = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < p.split_parts; ++k) x += tile_row(item, k, which, row);
+#pragma unroll 8
+    for (int s = grp; s < p.slots + (split ? 0 : 1); s += kGroups) x += from[s * stride];
+    if (split)
+      for (int k = grp; k < p.split_parts; k += kGroups)
+        x += p.tile_part[((static_cast<size_t>(item - p.split_from) * p.split_parts + k) * 2 + which) * kBlockN * D +
+                         key * D + col];
+    part[grp][col] = x;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) x += part[k][col];
     __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<size_t>(bkv) * p.N + key) * D + col;
     *out = __float2bfloat16_rn(which == 0 ? x * p.scale : x);
     return;
   }
-  const int key = blockIdx.x % p.sinks, which = (blockIdx.x / p.sinks) & 1, bkv = blockIdx.x / p.sinks / 2;
-  const size_t stride = static_cast<size_t>(p.BHkv) * 2 * p.sink_rows * D;
-  const float* from = p.sink_part + ((static_cast<size_t>(bkv) * 2 + which) * p.sink_rows + key) * D + col;
-  const int item = bkv * p.n_kblk;  // its first key tile
-  const bool split = item >= p.split_from;
-  float x = 0.0f;
-#pragma unroll 8
-  for (int s = grp; s < p.slots + (split ? 0 : 1); s += kGroups) x += from[s * stride];
-  if (split)
-    for (int k = grp; k < p.split_parts; k += kGroups) x += tile_row(item, k, which, key);
-  part[grp][col] = x;
-  __syncthreads();
-  if (grp != 0) return;
+  blk -= p.sink_blocks;
+  if (blk < p.tile_blocks) {
+    constexpr int kRows = 16, kPerTile = kBlockN / kRows;
+    const int which = (blk / kPerTile) & 1, rel = blk / kPerTile / 2, row0 = blk % kPerTile * kRows;
+    const int item = p.split_from + rel;
+    const int bkv = item / p.n_kblk, key0 = item % p.n_kblk * kBlockN + row0;
+    const float mul = which == 0 ? p.scale : 1.0f;
+    const float4* from = reinterpret_cast<const float4*>(p.tile_part) +
+                         ((static_cast<size_t>(rel) * p.split_parts * 2 + which) * kBlockN + row0) * (D / 4);
+    __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<size_t>(bkv) * p.N + key0) * D;
+    for (int i = threadIdx.x; i < kRows * D / 4; i += 256) {
+      const int key = key0 + i / (D / 4);
+      if (key >= p.N || (p.sink_blocks > 0 && key < p.sinks)) continue;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < p.split_parts; ++k) {
+        const float4 y = from[static_cast<size_t>(k) * 2 * kBlockN * (D / 4) + i];
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+      }
+      reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(x.x * mul, x.y * mul), pack_bf16x2(x.z * mul, x.w * mul));
+    }
+    return;
+  }
+  blk -= p.tile_blocks;
+  const long long n8 = static_cast<long long>(p.BHkv) * p.group * p.N * (D / 8);
+  const long long stride = static_cast<long long>(gridDim.x - p.sink_blocks - p.tile_blocks) * 256;
+  for (long long i0 = blk * 256LL + threadIdx.x; i0 < n8; i0 += 4 * stride) {
+    float4 a[4], b[4];
 #pragma unroll
-  for (int k = 1; k < kGroups; ++k) x += part[k][col];
-  __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<size_t>(bkv) * p.N + key) * D + col;
-  *out = __float2bfloat16_rn(which == 0 ? x * p.scale : x);
+    for (int u = 0; u < 4; ++u) {
+      const long long i = i0 + u * stride;
+      if (i < n8) {
+        a[u] = reinterpret_cast<const float4*>(p.dq_acc)[2 * i];
+        b[u] = reinterpret_cast<const float4*>(p.dq_acc)[2 * i + 1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const long long i = i0 + u * stride;
+      if (i < n8)
+        reinterpret_cast<uint4*>(p.dq)[i] =
+            make_uint4(pack_bf16x2(a[u].x * p.scale, a[u].y * p.scale), pack_bf16x2(a[u].z * p.scale, a[u].w * p.scale),
+                       pack_bf16x2(b[u].x * p.scale, b[u].y * p.scale), pack_bf16x2(b[u].z * p.scale, b[u].w * p.scale));
+    }
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned int>(p.slots) * static_cast<unsigned int>(p.BHkv));
-  const cudaError_t err = launch_dependent(d == 128 ? fa_window_pre_kernel<128> : fa_window_pre_kernel<64>, grid,
-                                           dim3(32 * kWarps), 0, stream, p);
+  // up to 8 first tokens: half the accumulators, so more warps per SM
+  auto kernel = p.sinks <= 8 ? (d == 128 ? fa_window_pre_kernel<128, 1> : fa_window_pre_kernel<64, 1>)
+                             : (d == 128 ? fa_window_pre_kernel<128, 2> : fa_window_pre_kernel<64, 2>);
+  const cudaError_t err = launch_dependent(kernel, grid, dim3(32 * kWarps), 0, stream, p);
   return err != cudaSuccess ? err : launched(1);
 }
 
-cudaError_t launch_window_join(const WindowParams& p, int d, cudaStream_t stream) {
-  const unsigned int items = static_cast<unsigned int>(p.n_kblk * p.BHkv - p.split_from);
-  const dim3 grid((p.slots > 0 ? static_cast<unsigned int>(p.sinks) * 2u * static_cast<unsigned int>(p.BHkv) : 0u) +
-                  items * (2u * kBlockN / (256u / static_cast<unsigned int>(d))));
-  const cudaError_t err = launch_dependent(d == 128 ? fa_window_join_kernel<128> : fa_window_join_kernel<64>, grid,
+cudaError_t launch_window_post(WindowParams p, int d, cudaStream_t stream) {
+  p.sink_blocks = p.slots > 0 ? p.sinks * 2 * p.BHkv : 0;
+  p.tile_blocks = (p.n_kblk * p.BHkv - p.split_from) * 2 * (kBlockN / 16);
+  const long long n8 = static_cast<long long>(p.BHkv) * p.group * p.N * (d / 8);
+  const long long blocks = (n8 + 255) / 256, cap = 152LL * 16;
+  const dim3 grid(static_cast<unsigned int>(p.sink_blocks) + static_cast<unsigned int>(p.tile_blocks) +
+                  static_cast<unsigned int>(blocks < cap ? blocks : cap));
+  const cudaError_t err = launch_dependent(d == 128 ? fa_window_post_kernel<128> : fa_window_post_kernel<64>, grid,
                                            dim3(256), 0, stream, p);
   return err != cudaSuccess ? err : launched(1);
 }

@@ -482,8 +482,7 @@ int fa_timing_last_ms(int kernel, float* ms);
  * then the merge); fa_bwd three;
  * fa_bwd_deterministic three; fa_fwd_fp8 three (two preparation kernels and
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
- * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three,
- * or four where dK and dV rows come in parts (see there);
+ * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three;
  * fa_paged_append and fa_paged_read one;
  * fa_fwd_paged two (the forward, then the join of segments that several CTAs
  * shared).
