@@ -657,9 +657,9 @@ int check_window(int B, int H, int Hkv, int N, int d, float scale, int window, i
   return FA_OK;
 }
 
-// How fa_window.cu cuts the queries of a key head: about four CTAs per SM of a
-// 152-SM device in all, a part of 64 rows at least, 256 parts at most (the
-// join reads them all).  Nothing when no query's window leaves a first token.
+// How fa_window.cu cuts the queries of a key head: about two CTAs per SM of a
+// 152-SM device in all (what its shared memory allows), a part of 16 rows at
+// least, 256 parts at most (the join reads them all).  Nothing when no query's window leaves a first token.
 struct SinkParts {
   int slots = 0, slot_rows = 0, sink_rows = 0;
   size_t bytes = 0;
@@ -668,10 +668,11 @@ SinkParts sink_parts(int B, int Hkv, int N, int d, int window, int sinks) {
   SinkParts s;
   if (sinks == 0 || N <= window) return s;
   const long long heads = static_cast<long long>(B) * Hkv;
-  long long slots = (608 + heads - 1) / heads;
+  long long slots = 304 / heads;
   if (slots > 256) slots = 256;
+  if (slots < 1) slots = 1;
   const int per = static_cast<int>((N + slots - 1) / slots);
-  s.slot_rows = (per + 63) / 64 * 64;
+  s.slot_rows = (per + 15) / 16 * 16;
   s.slots = (N + s.slot_rows - 1) / s.slot_rows;
   s.sink_rows = (sinks + 15) / 16 * 16;
   s.bytes = round_up(static_cast<size_t>(s.slots + 1) * heads * 2 * s.sink_rows * d * sizeof(float));
@@ -837,6 +838,9 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
     wp.sink_rows = sp.sink_rows;
     wp.slots = sp.slots;
     wp.slot_rows = sp.slot_rows;
+    wp.div_tiles = FastDiv(static_cast<uint32_t>(sp.slot_rows / 16));
+    wp.div_last_tiles = FastDiv(static_cast<uint32_t>((N - (sp.slots - 1) * sp.slot_rows + 15) / 16));
+    wp.status = p.status;
     wp.c = p.c;
     wp.log2e = p.log2e;
     p.sink_main = sink_part + static_cast<size_t>(sp.slots) * BHkv * 2 * sp.sink_rows * d;

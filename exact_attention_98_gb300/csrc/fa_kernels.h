@@ -162,7 +162,9 @@ struct WindowParams {
   int sinks;
   int sink_rows;  // sinks rounded up to 16
   int slots;      // parts that the rows of a key head's queries are cut into
-  int slot_rows;  // rows of a part, a multiple of 64
+  int slot_rows;  // rows of a part, a multiple of 16
+  FastDiv div_tiles, div_last_tiles;  // by the 16-row tiles of a part, of the last part
+  unsigned int* status;
   float c;        // scale * log2(e)
   float log2e;
   float scale;

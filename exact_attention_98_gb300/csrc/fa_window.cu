@@ -27,6 +27,10 @@ namespace {
 
 constexpr int kWarps = 4;
 
+enum : unsigned int {
+  kSiteWindowTile = 0x601,
+};
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -48,26 +52,70 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+template <int D, int NT>
+struct PreCfg {
+  static constexpr int kKeys = 8 * NT;  // keys of a pass
+  static constexpr int kPitch = D + 8;  // of a key row in shared memory: no bank conflicts
+  static constexpr int kStages = 2;
+  static constexpr int kTileBytes = 16 * D * 2;  // 16 rows of Q, dO or O: contiguous
+  static constexpr int kStageBytes = 3 * kTileBytes;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kKOff = kRingBytes;
+  static constexpr int kVOff = kKOff + kKeys * kPitch * 2;
+  static constexpr int kBarOff = kVOff + kKeys * kPitch * 2;
+  static constexpr int kAbortOff = kBarOff + kWarps * kStages * 8;
+  static constexpr int kSmemBytes = kAbortOff + 16;
+  static_assert(kWarps * kKeys * D * 4 <= kRingBytes, "the warps' sums go over the ring");
+};
+
+// Untiled bulk copy global -> shared, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // grid slots * BHkv.  A warp takes 16 rows of one query head at a time; lane
 // (g, c) their rows g and g + 8, and of each the elements [c D/4, (c+1) D/4).
+// The next 16 rows are on their way into the warp's ring meanwhile.
 // NT: tiles of 8 first tokens in a pass over the rows.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid_constant__ WindowParams p) {
+  using C = PreCfg<D, NT>;
   constexpr int kSteps = D / 16;
-  constexpr int kKeys = 8 * NT;    // keys of a pass
-  constexpr int kPitch = D + 8;    // of a key row in shared memory: no bank conflicts
-  __shared__ __align__(16) __nv_bfloat16 ks[kKeys * kPitch];
-  __shared__ __align__(16) __nv_bfloat16 vs[kKeys * kPitch];
-  __shared__ __align__(16) float sum[kWarps][kKeys][D];
+  constexpr int kKeys = C::kKeys, kPitch = C::kPitch;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(smem + C::kKOff);
+  __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(smem + C::kVOff);
+  float (*sum)[kKeys][D] = reinterpret_cast<float (*)[kKeys][D]>(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbortOff);
+  const WaitCtl ctl{abort_flag, p.status};
   const int warp = warp_id(), lane = lane_id();
   const int g = lane >> 2, c = lane & 3;
   const int slot = blockIdx.x % p.slots, bkv = blockIdx.x / p.slots;
+  const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
+  const uint32_t ring_s = smem_u32(ring);
+  const uint32_t bars = smem_u32(smem + C::kBarOff) + warp * C::kStages * 8;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kWarps * C::kStages; ++i) mbar_init(smem_u32(smem + C::kBarOff) + 8 * i, 1);
+    fence_mbar_init();
+  }
   grid_dependency_wait();
 
   const int row_begin = slot * p.slot_rows;
   const int row_end = min(p.N, row_begin + p.slot_rows);
+  // 16-row tiles of the part, of each head of the group in turn
+  const int per_head = (row_end - row_begin + 15) / 16, tiles = per_head * p.group;
+  const FastDiv div_tiles = row_end - row_begin == p.slot_rows ? p.div_tiles : p.div_last_tiles;
+  int stage = 0;          // of the next tile to use
+  uint32_t parity = 0;    // of its barrier
+  int issue_stage = 0;
+  bool ok = true;
   for (int key0 = 0; key0 < p.sinks; key0 += kKeys) {
-    __syncthreads();  // the pass before has read ks, vs and sum
+    fence_proxy_async_smem();  // the sums of the pass before, written over the ring, before the copies into it
+    __syncthreads();  // the pass before has read ks, vs and sum; the barriers are initialised
     for (int i = threadIdx.x; i < kKeys * D / 8; i += 32 * kWarps) {
       const int r = i / (D / 8), col = (i % (D / 8)) * 8;
       uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
@@ -90,30 +138,66 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < 4; ++e) dk[k][nt][e] = dv[k][nt][e] = 0.0f;
 
-    for (int h = 0; h < p.group; ++h) {
-      const size_t head_row = (static_cast<size_t>(bkv) * p.group + h) * p.N;
-      for (int r0 = row_begin + warp * 16; r0 < row_end; r0 += kWarps * 16) {
-        // any pair of these rows with keys of this pass?
-        const bool far = min(r0 + 15, p.N - 1) - key0 >= p.window;
-        if (key0 > 0 && !far) continue;
+    auto first_row = [&](int t) { return row_begin + (t - div_tiles.div(t) * per_head) * 16; };
+    // any pair of the 16 rows from r0 with keys of this pass?
+    auto is_far = [&](int r0) { return min(r0 + 15, p.N - 1) - key0 >= p.window; };
+    // the tile from t on that this pass has to read
+    auto needed = [&](int t) {
+      if (key0 > 0)
+        while (t < tiles && !is_far(first_row(t))) t += kWarps;
+      return t;
+    };
+    auto issue = [&](int t) {
+      if (t >= tiles) return;
+      const int r0 = first_row(t);
+      const uint32_t bytes = static_cast<uint32_t>(min(16, p.N - r0)) * D * 2;
+      const size_t at = ((static_cast<size_t>(bkv) * p.group + div_tiles.div(t)) * p.N + r0) * D;
+      const bool far = is_far(r0);
+      if (lane == 0) {
+        const uint32_t dst = ring_s + issue_stage * C::kStageBytes, bar = bars + 8 * issue_stage;
+        mbar_arrive_expect_tx(bar, bytes * (1u + (far ? 1u : 0u) + (key0 == 0 ? 1u : 0u)));
+        if (far) bulk_load(dst, p.q + at, bytes, bar);
+        bulk_load(dst + C::kTileBytes, p.dout + at, bytes, bar);
+        if (key0 == 0) bulk_load(dst + 2 * C::kTileBytes, p.o + at, bytes, bar);
+      }
+      issue_stage ^= 1;
+    };
+    int ahead = needed(warp);  // the next tile to copy
+    for (int i = 0; i < C::kStages; ++i) {
+      if (ok) issue(ahead);
+      ahead = needed(ahead + kWarps);
+    }
+    {
+      for (int t = needed(warp); t < tiles; t = needed(t + kWarps)) {
+        const int r0 = first_row(t);
+        const size_t head_row = (static_cast<size_t>(bkv) * p.group + div_tiles.div(t)) * p.N;
+        const bool far = is_far(r0);
+        const uint8_t* st = ring + stage * C::kStageBytes;
+        if (ok && !mbar_wait_warp(bars + 8 * stage, parity, ctl, kSiteWindowTile)) {
+          // given up: no more copies; those in flight land before shared memory
+          // is released
+          ok = false;
+          for (int i = 0; i < C::kStages; ++i)
+            mbar_wait_drain(bars + 8 * ((stage + i) % C::kStages), parity ^ (stage + i >= C::kStages ? 1u : 0u));
+        }
         uint32_t qa[kSteps][4], da[kSteps][4];
         float dsum[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = r0 + g + 8 * r;
           const bool in = row < p.N;
-          const size_t at = (head_row + (in ? row : 0)) * D + c * (D / 4);
+          const uint4* at = reinterpret_cast<const uint4*>(st + (g + 8 * r) * (D * 2) + c * (D / 2));
           dsum[r] = 0.0f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-            if (in) y = *reinterpret_cast<const uint4*>(p.dout + at + 8 * i);
-            if (in && far) x = *reinterpret_cast<const uint4*>(p.q + at + 8 * i);
+            if (in) y = at[C::kTileBytes / 16 + i];
+            if (in && far) x = at[i];
             qa[2 * i][r] = x.x; qa[2 * i][2 + r] = x.y; qa[2 * i + 1][r] = x.z; qa[2 * i + 1][2 + r] = x.w;
             da[2 * i][r] = y.x; da[2 * i][2 + r] = y.y; da[2 * i + 1][r] = y.z; da[2 * i + 1][2 + r] = y.w;
             if (key0 == 0) {
               uint4 o = make_uint4(0u, 0u, 0u, 0u);
-              if (in) o = *reinterpret_cast<const uint4*>(p.o + at + 8 * i);
+              if (in) o = at[2 * (C::kTileBytes / 16) + i];
               const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -129,6 +213,13 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
           } else {
             dsum[r] = in ? p.dsum[head_row + row] : 0.0f;  // written by this block in its first pass
           }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (ok) issue(ahead);
+        ahead = needed(ahead + kWarps);
+        if (++stage == C::kStages) {
+          stage = 0;
+          parity ^= 1u;
         }
         float* acc[2];
 #pragma unroll
@@ -232,10 +323,11 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
       }
     }
 
-    // the four warps' dK_s, then dV_s, added in order
+    // the four warps' dK_s, then dV_s, added in order (over the ring: every copy
+    // has been waited for)
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      if (which == 1) __syncthreads();
+      __syncthreads();
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
@@ -349,7 +441,14 @@ cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream)
   // up to 8 first tokens: half the accumulators, so more warps per SM
   auto kernel = p.sinks <= 8 ? (d == 128 ? fa_window_pre_kernel<128, 1> : fa_window_pre_kernel<64, 1>)
                              : (d == 128 ? fa_window_pre_kernel<128, 2> : fa_window_pre_kernel<64, 2>);
-  const cudaError_t err = launch_dependent(kernel, grid, dim3(32 * kWarps), 0, stream, p);
+  const int smem = p.sinks <= 8 ? (d == 128 ? PreCfg<128, 1>::kSmemBytes : PreCfg<64, 1>::kSmemBytes)
+                                : (d == 128 ? PreCfg<128, 2>::kSmemBytes : PreCfg<64, 2>::kSmemBytes);
+  cudaError_t err = p.sinks <= 8 ? (d == 128 ? configure_kernel<fa_window_pre_kernel<128, 1>>(smem)
+                                             : configure_kernel<fa_window_pre_kernel<64, 1>>(smem))
+                                 : (d == 128 ? configure_kernel<fa_window_pre_kernel<128, 2>>(smem)
+                                             : configure_kernel<fa_window_pre_kernel<64, 2>>(smem));
+  if (err != cudaSuccess) return err;
+  err = launch_dependent(kernel, grid, dim3(32 * kWarps), smem, stream, p);
   return err != cudaSuccess ? err : launched(1);
 }
 

@@ -388,8 +388,8 @@ def test_workspace_bytes(fa):
     assert n(1, 4, 2, 0, 64, 9, 1) == 0 and n(1, 4, 3, 300, 64, 9, 1) == 0 and n(1, 4, 2, 300, 64, 9, 129) == 0
     base = fa.fa_bwd_workspace_bytes(1, 4, 300, 64)
     assert n(1, 4, 2, 300, 64, 300, 4) == n(1, 4, 2, 300, 64, 9, 0)  # no query's window leaves a first token
-    # 5 parts of 64 rows and the main kernel's, 2 key heads, dK and dV, 16 rows
-    assert n(1, 4, 2, 300, 64, 9, 4) - n(1, 4, 2, 300, 64, 9, 0) == 6 * 2 * 2 * 16 * 64 * 4
+    # 19 parts of 16 rows and the main kernel's, 2 key heads, dK and dV, 16 rows
+    assert n(1, 4, 2, 300, 64, 9, 4) - n(1, 4, 2, 300, 64, 9, 0) == 20 * 2 * 2 * 16 * 64 * 4
     assert n(1, 4, 2, 300, 64, 9, 0) >= base
 
 
