@@ -93,6 +93,9 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
   const WaitCtl ctl{abort_flag, p.status};
   const int warp = warp_id(), lane = lane_id();
   const int g = lane >> 2, c = lane & 3;
+  // lanes with c >= 2 take their run's 16-byte chunks in pairs exchanged: the four
+  // lanes of a quad, D/2 bytes apart, would meet in the same banks otherwise
+  const int turn = c >> 1;
   const int slot = blockIdx.x % p.slots, bkv = blockIdx.x / p.slots;
   const uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
   const uint32_t ring_s = smem_u32(ring);
@@ -128,8 +131,8 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
       *reinterpret_cast<uint4*>(vs + r * kPitch + col) = b;
     }
     __syncthreads();
-    // dK_s^T and dV_s^T: keys 8 nt + 2c + {0, 1} (e & 1) at d(g) + 4 k (+ 2 for e >> 1),
-    // d(g) = (g / 2) D/4 + g % 2
+    // dK_s^T and dV_s^T: keys 8 nt + 2c + {0, 1} (e & 1) at d(g) + 4 (k ^ 2 (g / 4))
+    // (+ 2 for e >> 1), d(g) = (g / 2) D/4 + g % 2
     float dk[kSteps][NT][4], dv[kSteps][NT][4];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
@@ -191,13 +194,13 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-            if (in) y = at[C::kTileBytes / 16 + i];
-            if (in && far) x = at[i];
+            if (in) y = at[C::kTileBytes / 16 + (i ^ turn)];
+            if (in && far) x = at[i ^ turn];
             qa[2 * i][r] = x.x; qa[2 * i][2 + r] = x.y; qa[2 * i + 1][r] = x.z; qa[2 * i + 1][2 + r] = x.w;
             da[2 * i][r] = y.x; da[2 * i][2 + r] = y.y; da[2 * i + 1][r] = y.z; da[2 * i + 1][2 + r] = y.w;
             if (key0 == 0) {
               uint4 o = make_uint4(0u, 0u, 0u, 0u);
-              if (in) o = at[2 * (C::kTileBytes / 16) + i];
+              if (in) o = at[2 * (C::kTileBytes / 16) + (i ^ turn)];
               const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
           for (int e = 0; e < 4; ++e) s[nt][e] = dp[nt][e] = 0.0f;
 #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
-            const int at = (nt * 8 + g) * kPitch + c * (D / 4) + 4 * k;
+            const int at = (nt * 8 + g) * kPitch + c * (D / 4) + 4 * (k ^ (2 * turn));
             const uint2 kk = *reinterpret_cast<const uint2*>(ks + at);
             const uint2 vv = *reinterpret_cast<const uint2*>(vs + at);
             mma_bf16(s[nt], qa[k], kk.x, kk.y);
@@ -334,7 +337,8 @@ __global__ void __launch_bounds__(32 * kWarps) fa_window_pre_kernel(const __grid
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            sum[warp][nt * 8 + 2 * c + (e & 1)][(g >> 1) * (D / 4) + 4 * k + 2 * (e >> 1) + (g & 1)] =
+            sum[warp][nt * 8 + 2 * c + (e & 1)]
+               [(g >> 1) * (D / 4) + 4 * (k ^ (2 * (g >> 2))) + 2 * (e >> 1) + (g & 1)] =
                 which == 0 ? dk[k][nt][e] : dv[k][nt][e];
       __syncthreads();
       float* out = p.sink_part + (((static_cast<size_t>(slot) * p.BHkv + bkv) * 2 + which) * p.sink_rows + key0) * D;
