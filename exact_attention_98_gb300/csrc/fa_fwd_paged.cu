@@ -51,7 +51,7 @@ __device__ constexpr float kSlack = FP4 ? 8.0f : 2.0f;
 template <int D, bool FP4, int TILES>
 struct PagedCfg {
   static constexpr int kRows = 8 * TILES;            // rows of a block
-  static constexpr int kUnitShift = FP4 ? (TILES == 2 ? 6 : 6) : 4;
+  static constexpr int kUnitShift = FP4 ? 6 : 4;
   static constexpr int kUnit = 1 << kUnitShift;      // positions of a unit
   static constexpr int kLeast = 64 / kUnit;          // units of a warp's piece at least
   static constexpr int kWarps = FP4 ? (TILES == 2 ? 8 : 12) : 8;
@@ -223,24 +223,32 @@ struct Loader {
     }
     const uint32_t dst = ring + stage * C::kStageBytes;
     const uint32_t bar = bars + 8 * stage;
-    // lanes 4 sub + 0..3: of page `sub` of the unit K and V, codes and scales or
-    // 64 columns each
-    const int sub = (lane >> 2) & ((1 << subs_shift) - 1);
+    // 4 bits: a lane per page of the unit, whose block is one copy; a page
+    // longer than the unit: lanes 0-3, its part of K's and V's codes and scales.
+    // bf16: lanes 0-3, K and V, 64 columns each.
+    const bool parts = !FP4 || p.c.page_shift > C::kUnitShift;
+    const int sub = parts ? 0 : lane & ((1 << subs_shift) - 1);
     const unsigned long long from =
         __shfl_sync(0xffffffffu, at, (((32 >> subs_shift) - batch) << subs_shift) + sub);
-    const bool mine = lane < (4 << subs_shift) && from != (FP4 ? 0ull : ~0ull);
+    const bool mine = lane < (parts ? 4 : 1 << subs_shift) && from != (FP4 ? 0ull : ~0ull);
     const unsigned int live = __ballot_sync(0xffffffffu, mine);
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * (C::kStageBytes / 4 >> subs_shift));
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar, __popc(live) * (parts ? C::kStageBytes / 4 : C::kStageBytes >> subs_shift));
     __syncwarp();
     if (mine) {
       const int kv = (lane >> 1) & 1, part = lane & 1;
       if constexpr (FP4) {
-        const uint32_t half = static_cast<uint32_t>(paged_half_bytes(true, 1 << p.c.page_shift, D));
-        // the scales of a row stand behind the page's codes
-        const uint32_t in_page = (first_key + (sub << shift)) & page_mask;
-        const uint32_t src = kv * half + (part ? ((D / 2) << p.c.page_shift) - in_page * (D / 2 - D / 16) : 0u);
-        const uint32_t to = kv * C::kHalf + (part ? C::kUnit * (D / 2) + (sub << shift) * (D / 16) : (sub << shift) * (D / 2));
-        bulk_load(dst + to, reinterpret_cast<const uint8_t*>(from) + src, (part ? D / 16 : D / 2) << shift, bar);
+        if (!parts) {
+          const uint32_t bytes = C::kStageBytes >> subs_shift;
+          bulk_load(dst + sub * bytes, reinterpret_cast<const uint8_t*>(from), bytes, bar);
+        } else {
+          const uint32_t half = static_cast<uint32_t>(paged_half_bytes(true, 1 << p.c.page_shift, D));
+          // the scales of a row stand behind the page's codes
+          const uint32_t in_page = first_key & page_mask;
+          const uint32_t src = kv * half + (part ? ((D / 2) << p.c.page_shift) - in_page * (D / 2 - D / 16) : 0u);
+          bulk_load(dst + kv * C::kHalf + (part ? C::kUnit * (D / 2) : 0),
+                    reinterpret_cast<const uint8_t*>(from) + src, C::kUnit * (part ? D / 16 : D / 2), bar);
+        }
       } else if (part < D / 64) {
         tma_load_3d(dst + kv * C::kHalf + part * (C::kUnit * 128), &p.tm, bar, part * 64, first_key & page_mask,
                     static_cast<int>(from) + kv);
@@ -355,6 +363,10 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
   for (int i = 0; i < C::kStages; ++i) load.next(p, ring_s, bars, lane);
 
   const int g = lane >> 2, c = lane & 3;
+  // 4 bits: a stage holds blocks of sub_keys positions as the cache does (K codes,
+  // K scales, V codes, V scales)
+  const int sub_shift = min(p.c.page_shift, C::kUnitShift);
+  const int sub_half = paged_half_bytes(FP4, 1 << sub_shift, D);
   int stage = 0;
   uint32_t parity = 0;
   bool ok = true;
@@ -465,13 +477,15 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[grp][t][e] = 0.0f;
         if constexpr (FP4) {
+          const uint8_t* k_rows = st + ((grp * 16) >> sub_shift) * 2 * sub_half;
+          const int in_block = (grp * 16) & ((1 << sub_shift) - 1);
           uint32_t codes[2][D / 32];
           uint32_t sc[2][D / 64];  // the scales of this lane's blocks of 16, twice each
 #pragma unroll
           for (int k8 = 0; k8 < 2; ++k8) {
-            const int row = grp * 16 + k8 * 8 + g;
-            const uint8_t* kc = st + row * (D / 2) + c * (D / 8);
-            const uint8_t* ks = st + C::kUnit * (D / 2) + row * (D / 16) + c * (D / 64);
+            const int row = in_block + k8 * 8 + g;
+            const uint8_t* kc = k_rows + row * (D / 2) + c * (D / 8);
+            const uint8_t* ks = k_rows + ((D / 2) << sub_shift) + row * (D / 16) + c * (D / 64);
             if constexpr (D == 128) {
               const uint4 x = *reinterpret_cast<const uint4*>(kc);
               codes[k8][0] = x.x; codes[k8][1] = x.y; codes[k8][2] = x.z; codes[k8][3] = x.w;
@@ -600,8 +614,10 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
           }
         if constexpr (FP4) {
           // rows g, g + 8 of m-tile j are d = g D/8 + 2j, + 1
-          const uint8_t* vc = st + C::kHalf + (grp * 16 + 2 * c) * (D / 2) + g * (D / 16);
-          const uint8_t* vs = st + C::kHalf + C::kUnit * (D / 2) + (grp * 16 + 2 * c) * (D / 16) + (g * D) / 128;
+          const uint8_t* v_rows = st + (((grp * 16) >> sub_shift) * 2 + 1) * sub_half;
+          const int in_block = (grp * 16) & ((1 << sub_shift) - 1);
+          const uint8_t* vc = v_rows + (in_block + 2 * c) * (D / 2) + g * (D / 16);
+          const uint8_t* vs = v_rows + ((D / 2) << sub_shift) + (in_block + 2 * c) * (D / 16) + (g * D) / 128;
           uint32_t sc[2];  // scales of the keys' pairs
 #pragma unroll
           for (int k8 = 0; k8 < 2; ++k8) {

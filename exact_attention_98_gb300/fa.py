@@ -12,6 +12,7 @@ this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -153,7 +154,7 @@ def _stream(stream=None):
     """The cudaStream_t of `stream`, or of the current stream of the current
     device (looked up without building a torch.cuda.Stream, which takes 3 us)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -164,8 +165,8 @@ def _shape(q):
 
 
 def _check_tensor(t, name, dtype, shape, device=None):
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
-            and (device is None or t.device == device) and t.is_contiguous()):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (t.is_cuda if device is None else t.get_device() == device.index)):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -369,7 +370,7 @@ def _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale):
     if not isinstance(pages, torch.Tensor) or not pages.is_cuda:
         raise ValueError("pages must be a CUDA tensor")
     dev = pages.device
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         raise ValueError(f"pages is on {dev}; the library launches on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not pages.is_contiguous():
@@ -403,9 +404,9 @@ def _paged_cache(pages, page_table, seq_lens, d, k_scale, v_scale):
 def _rows(t, name, heads, d, device, rows=None):
     """(rows, row stride, head stride) of a bf16 [rows, heads, d] tensor whose
     rows of d values are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     shape = t.shape
     if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or (
@@ -433,6 +434,11 @@ def fa_paged_read(cache: PagedCache, cu_new, rows, k, v, stream=None) -> None:
 
 def fa_fwd_paged_workspace_bytes(d: int) -> int:
     return lib.fa_fwd_paged_workspace_bytes(d)
+
+
+@functools.lru_cache(maxsize=None)
+def _paged_workspace_bytes(device: int, d: int) -> int:
+    return max(fa_fwd_paged_workspace_bytes(d), 1)
 
 
 def fa_fwd_paged(cache: PagedCache, q, q_row, q_head, o, lse, cu_new, rows, max_new, H, scale, window,
@@ -548,10 +554,11 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
 
 def _empty(stream, device, *shapes_and_types):
     """Uninitialised tensors whose memory belongs to the stream that uses them."""
+    empty = torch.empty
     if stream is not None:
         with torch.cuda.stream(stream):
-            return [torch.empty(s, dtype=t, device=device) for s, t in shapes_and_types]
-    return [torch.empty(s, dtype=t, device=device) for s, t in shapes_and_types]
+            return [empty(s, dtype=t, device=device) for s, t in shapes_and_types]
+    return [empty(s, dtype=t, device=device) for s, t in shapes_and_types]
 
 
 def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
@@ -668,7 +675,7 @@ def paged_forward(q, pages, page_table, seq_lens, cu_new, max_new: int = 1, wind
     _check_tensor(cu_new, "cu_new", torch.int32, (cache.B + 1,), dev)
     o, lse = _empty(stream, dev, ((rows, H, d), torch.bfloat16), ((rows, H), torch.float32))
     if workspace is None:
-        workspace, = _empty(stream, dev, (max(fa_fwd_paged_workspace_bytes(d), 1), torch.uint8))
+        workspace, = _empty(stream, dev, (_paged_workspace_bytes(dev.index, d), torch.uint8))
     fa_fwd_paged(cache, q, q_row, q_head, o, lse, cu_new, rows, max_new, H,
                  default_scale(d) if scale is None else scale, window, sinks, workspace, stream)
     return o, lse
