@@ -281,7 +281,26 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   const int bq0 = kWindow ? bh * p.group : bh;
   using Walk = QueryWalk<kWindow>;
 
-  if (threadIdx.x == 0) {
+  // Window: the loader initialises the barriers and starts the first copies at
+  // once, so that they run beside the CTA's set-up (short windows leave few
+  // query tiles per CTA to make up for it).
+  auto load_kv = [&] {
+    mbar_arrive_expect_tx(bar(C::kBarKV), 2 * C::kTileBytes);
+    for (int h = 0; h < D / 64; ++h) {
+      tma_load_3d(sbase + C::kKOff + h * C::kHalfBytes, &p.tm_k, bar(C::kBarKV), h * 64, k0, bh);
+      tma_load_3d(sbase + C::kVOff + h * C::kHalfBytes, &p.tm_v, bar(C::kBarKV), h * 64, k0, bh);
+    }
+  };
+  auto load_tile = [&](int s, int q0, int head) {
+    mbar_arrive_expect_tx(bar(C::kBarStFull + s), 2 * C::kTileBytes);
+    for (int h = 0; h < D / 64; ++h) {
+      tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_q,
+                  bar(C::kBarStFull + s), h * 64, q0, head);
+      tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_do,
+                  bar(C::kBarStFull + s), h * 64, q0, head);
+    }
+  };
+  if (threadIdx.x == (kWindow ? C::kProducerWarp * 32 : 0)) {
     *abort_flag = 0;
     mbar_init(bar(C::kBarKV), 1);
     for (int s = 0; s < C::kStages; ++s) {
@@ -298,14 +317,24 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
     mbar_init(bar(C::kBarDQEmpty), kBlockM);
     mbar_init(bar(C::kBarMmaDone), 1);
     fence_mbar_init();
+    if constexpr (kWindow) {
+      grid_dependency_wait();
+      load_kv();
+      if (n_iter > 0) {
+        const Walk first(i_first, i_last, bq0, it0);
+        load_tile(0, first.i * kBlockM, first.bh);
+      }
+    }
   }
   // bias operands: A = all ones; the B tiles start at zero and the loader
   // writes only the two hi/lo entries of each row
-  for (int w = threadIdx.x; w < C::kBiasTileBytes / 4; w += C::kThreads)
-    reinterpret_cast<uint32_t*>(smem + C::kOnesOff)[w] = 0x3F803F80u;  // bf16 1.0 pairs
-  for (int w = threadIdx.x; w < C::kStages * 2 * C::kBiasTileBytes / 4; w += C::kThreads)
-    reinterpret_cast<uint32_t*>(smem + C::kBiasOff)[w] = 0u;
-  fence_proxy_async_smem();
+  if constexpr (!kWindow || !C::kRowLse) {
+    for (int w = threadIdx.x; w < C::kBiasTileBytes / 4; w += C::kThreads)
+      reinterpret_cast<uint32_t*>(smem + C::kOnesOff)[w] = 0x3F803F80u;  // bf16 1.0 pairs
+    for (int w = threadIdx.x; w < C::kStages * 2 * C::kBiasTileBytes / 4; w += C::kThreads)
+      reinterpret_cast<uint32_t*>(smem + C::kBiasOff)[w] = 0u;
+    fence_proxy_async_smem();
+  }
   if (warp == C::kMmaWarp) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -324,11 +353,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
         tma_prefetch_desc(&p.tm_do);
-        mbar_arrive_expect_tx(bar(C::kBarKV), 2 * C::kTileBytes);
-        for (int h = 0; h < D / 64; ++h) {
-          tma_load_3d(sbase + C::kKOff + h * C::kHalfBytes, &p.tm_k, bar(C::kBarKV), h * 64, k0, bh);
-          tma_load_3d(sbase + C::kVOff + h * C::kHalfBytes, &p.tm_v, bar(C::kBarKV), h * 64, k0, bh);
-        }
+        if constexpr (!kWindow) load_kv();
       }
       int issued = 0;
       Walk walk(i_first, i_last, bq0, it0);
@@ -340,15 +365,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           if (!__all_sync(0xffffffffu, ok)) break;
         }
         const int q0 = walk.i * kBlockM;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(C::kBarStFull + s), 2 * C::kTileBytes);
-          for (int h = 0; h < D / 64; ++h) {
-            tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_q,
-                        bar(C::kBarStFull + s), h * 64, q0, walk.bh);
-            tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_do,
-                        bar(C::kBarStFull + s), h * 64, q0, walk.bh);
-          }
-        }
+        if (lane == 0 && (!kWindow || it > 0)) load_tile(s, q0, walk.bh);
         if constexpr (C::kRowLse) {
           // fp32 rows -LSE_q log2 e and -D_q (at the start of the stage's
           // bias space); rows past N get -inf (P = 0 there) and D = 0
