@@ -231,11 +231,12 @@ struct QueryWalk {
 };
 
 // The kernel body; fa_bwd_kernel<D> (all five products), fa_bwd_dkdv_kernel<D>
-// (dK and dV only) and fa_bwd_window_kernel<D> below are its entry points.
-// kWindow: a row sees the `window` keys up to itself, and the query heads of a
+// (dK and dV only) and fa_bwd_window_kernel<128> below are its entry points.
+// kWindow (d = 128): a row sees the `window` keys up to itself, and the query heads of a
 // group share a key head, whose dK and dV accumulate over them.
 template <int D, bool kNoDQ, bool kWindow = false>
 __device__ __forceinline__ void bwd_body(const BwdParams& p) {
+  static_assert(!kWindow || D == 128, "d = 64 windows: fa_bwd_window64.cu");
   using C = BwdCfg<D, kNoDQ>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -328,13 +329,11 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   }
   // bias operands: A = all ones; the B tiles start at zero and the loader
   // writes only the two hi/lo entries of each row
-  if constexpr (!kWindow || !C::kRowLse) {
-    for (int w = threadIdx.x; w < C::kBiasTileBytes / 4; w += C::kThreads)
-      reinterpret_cast<uint32_t*>(smem + C::kOnesOff)[w] = 0x3F803F80u;  // bf16 1.0 pairs
-    for (int w = threadIdx.x; w < C::kStages * 2 * C::kBiasTileBytes / 4; w += C::kThreads)
-      reinterpret_cast<uint32_t*>(smem + C::kBiasOff)[w] = 0u;
-    fence_proxy_async_smem();
-  }
+  for (int w = threadIdx.x; w < C::kBiasTileBytes / 4; w += C::kThreads)
+    reinterpret_cast<uint32_t*>(smem + C::kOnesOff)[w] = 0x3F803F80u;  // bf16 1.0 pairs
+  for (int w = threadIdx.x; w < C::kStages * 2 * C::kBiasTileBytes / 4; w += C::kThreads)
+    reinterpret_cast<uint32_t*>(smem + C::kBiasOff)[w] = 0u;
+  fence_proxy_async_smem();
   if (warp == C::kMmaWarp) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -484,7 +483,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         return true;
       };
       bool ok = mbar_wait(bar(C::kBarKV), 0, ctl, kSiteKV);
-      if (C::kEarlyS && ok && (!kWindow || n_iter > 0)) ok = issue_s(0);
+      if (C::kEarlyS && ok) ok = issue_s(0);
       for (int it = 0; ok && it < n_iter; ++it) {
         const int s = it % C::kStages;
         const uint32_t q_s = sbase + C::kQOff + s * C::kTileBytes;
@@ -926,12 +925,21 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   bwd_body<D, false, true>(p);
 }
 
+template <int D, bool kNoDQ, bool kWindow>
+constexpr auto bwd_kernel() -> void (*)(BwdParams) {
+  if constexpr (kWindow) {
+    return fa_bwd_window_kernel<D>;
+  } else if constexpr (kNoDQ) {
+    return fa_bwd_dkdv_kernel<D>;
+  } else {
+    return fa_bwd_kernel<D>;
+  }
+}
+
 template <int D, bool kNoDQ = false, bool kWindow = false>
 cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
   using C = BwdCfg<D, kNoDQ>;
-  constexpr void (*kernel)(BwdParams) = kWindow ? fa_bwd_window_kernel<D>
-                                        : kNoDQ ? fa_bwd_dkdv_kernel<D>
-                                                : fa_bwd_kernel<D>;
+  constexpr auto kernel = bwd_kernel<D, kNoDQ, kWindow>();
   cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   long long blocks = static_cast<long long>(p.n_kblk) * p.BH;
@@ -952,7 +960,7 @@ cudaError_t launch_bwd_main(const BwdParams& p, int d, cudaStream_t stream) {
 
 cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream) {
   if (d == 128) return launch_bwd_d<128, false, true>(p, stream);
-  if (d == 64) return launch_bwd_d<64, false, true>(p, stream);
+  if (d == 64) return launch_bwd_window64(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -289,6 +289,7 @@ cudaError_t launch_bwd_pre(const void* o, const void* dout, float* dsum, float* 
 cudaError_t launch_bwd_main(const BwdParams& p, int d, cudaStream_t stream);
 // The same kernel with a sliding window and shared key heads (p.window, p.group).
 cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream);
+cudaError_t launch_bwd_window64(const BwdParams& p, cudaStream_t stream);  // its d = 64 form (fa_bwd_window64.cu)
 // Before it, where queries see first tokens that their windows have left: D, and
 // those pairs' share of dQ in the accumulator, of dK and dV in sink_part.
 cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream);

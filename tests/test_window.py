@@ -140,6 +140,17 @@ def test_against_plain(B, H, Hkv, N, window, sinks, d):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,N,window,sinks", [
+    (2, 60, 60, 700, 130, 5),    # 720 key tiles: several to a CTA that walks them, few query tiles each
+    (1, 150, 50, 500, 40, 0),    # 200, the last of them split
+    (1, 160, 160, 100, 7, 2),    # 160 of one query tile
+])
+def test_more_key_tiles_than_sms(B, H, Hkv, N, window, sinks, d):
+    check(B, H, Hkv, N, d, window, sinks, seed=H + d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("scale", [0.02, 0.6])
 def test_scales(scale, d):
     """Flat and peaked weights."""
