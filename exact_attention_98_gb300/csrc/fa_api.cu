@@ -809,6 +809,8 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   const TileParts tp = tile_parts(B, H, Hkv, N, d, window);
   p.split_from = tp.from;
   p.split_parts = tp.parts;
+  p.div_kblk = FastDiv(static_cast<uint32_t>(p.n_kblk));
+  p.div_parts = FastDiv(static_cast<uint32_t>(tp.parts));
   p.tile_part = sink_part + sp.bytes / sizeof(float);
 
   WindowParams wp = {};

@@ -135,6 +135,7 @@ struct BwdParams {
   int split_from;
   int split_parts;
   float* tile_part;
+  FastDiv div_kblk, div_parts;  // window: by n_kblk, by split_parts
 };
 
 // What the sliding-window backward does beside its main kernel (fa_window.cu):
