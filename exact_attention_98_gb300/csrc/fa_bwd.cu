@@ -260,8 +260,9 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   int part = -1;
   if constexpr (kWindow) {
     if (blk >= p.split_from) {
-      part = (blk - p.split_from) % p.split_parts;
-      blk = p.split_from + (blk - p.split_from) / p.split_parts;
+      const int i = p.div_parts.div(blk - p.split_from);
+      part = blk - p.split_from - i * p.split_parts;
+      blk = p.split_from + i;
     }
   }
   const int bh = blk / p.n_kblk;
@@ -275,8 +276,9 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   int it0 = 0;  // the part's first
   if constexpr (kWindow) {
     if (part >= 0) {
-      it0 = static_cast<int>(static_cast<long long>(n_iter) * part / p.split_parts);
-      n_iter = static_cast<int>(static_cast<long long>(n_iter) * (part + 1) / p.split_parts) - it0;
+      const int q = p.div_parts.div(n_iter), r = n_iter - q * p.split_parts;
+      it0 = q * part + min(part, r);
+      n_iter = q + (part < r ? 1 : 0);
     }
   }
   const int bq0 = kWindow ? bh * p.group : bh;
@@ -472,6 +474,10 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         }
       };
 
+      // Window: the next S^T early at d = 128 too, over P^T_i, although dP^T_{i+1}
+      // waits for dQ_i in its columns: its few query tiles leave the exponentials
+      // on the chain (same sizes as at the drain: 330 us -> 318).
+      constexpr bool kEarly = C::kEarlyS || kWindow;
       // S^T_i = K Q_i^T and its bias, once stage s of Q_i has landed.
       auto issue_s = [&](int it) -> bool {
         const int s = it % C::kStages;
@@ -483,12 +489,12 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         return true;
       };
       bool ok = mbar_wait(bar(C::kBarKV), 0, ctl, kSiteKV);
-      if (C::kEarlyS && ok) ok = issue_s(0);
+      if (kEarly && ok && n_iter > 0) ok = issue_s(0);
       for (int it = 0; ok && it < n_iter; ++it) {
         const int s = it % C::kStages;
         const uint32_t q_s = sbase + C::kQOff + s * C::kTileBytes;
         const uint32_t do_s = sbase + C::kDOOff + s * C::kTileBytes;
-        if (!C::kEarlyS && !(ok = issue_s(it))) break;
+        if (!kEarly && !(ok = issue_s(it))) break;
         if (!C::kEarlyS && it > 0) {  // dQ_{i-1}^T has left the dP^T columns
           if (!(ok = mbar_wait(bar(C::kBarDQEmpty), (it - 1) & 1, ctl, kSiteDQEmpty))) break;
           tc_fence_after();
@@ -501,7 +507,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         issue_tn(C::kColS, do_s, C::kColDV, it > 0);
         mma_commit(bar(C::kBarDVDone));
         // S^T_{i+1} over P^T_i, which dV_i (issued before it) has read.
-        if (C::kEarlyS && it + 1 < n_iter && !(ok = issue_s(it + 1))) break;
+        if (kEarly && it + 1 < n_iter && !(ok = issue_s(it + 1))) break;
         // dK_i needs dS^T_i in tensor memory only; dQ_i also needs its copy in
         // shared memory, which the compute warps write while dK_i runs.
         if (!(ok = mbar_wait(bar(C::kBarDSTmem), it & 1, ctl, kSiteDSTmem))) break;
@@ -558,7 +564,10 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         mbar_arrive(bar(C::kBarDQEmpty));
         // (The per-key-tile store branch is not taken any more: the
         // deterministic mode computes dQ with its own kernel.  The kernel
-        // measured 1-2% slower without it, so it stays; see BwdParams.)
+        // measured 1-2% slower without it, so it stays; see BwdParams.  The
+        // window kernel: 296 us with it, 338 without, and no pace of the adds
+        // found that makes up for it; B = 2, H = 16, Hkv = 4, N = 8192, window
+        // 1024.)
         if (det) {  // this key tile's contribution, summed later in key-tile order
 #pragma unroll
           for (int qc = 0; qc < kBlockM; ++qc)
@@ -693,33 +702,39 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         p0 = ex2_mufu(x0);
         p1 = ex2_mufu(x1);
       };
-      // Window: dS is formed from P as computed instead of as rounded for the dV
-      // product: P stays in the registers of S (dP then comes in halves).
-      // The rounding of P would add to dQ and dK as much as dS's own.
-      auto keep_pair = [&](int ch, int e2, float p0, float p1) {
-        if constexpr (kWindow) {
-          sr[ch][2 * e2] = __float_as_uint(p0);
-          sr[ch][2 * e2 + 1] = __float_as_uint(p1);
-        }
-      };
-      if (kWindow && diag) {
-        // the key sees the query columns [lo, lo + window) of the tile
-        const int lo = (kt - i) * kBlockM + kr - wg * 64;
-        const int hi = lo + p.window;
-        auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+      // Window: one copy of the exponentials and the mask after it (318 us -> 296:
+      // the roles' code outgrows the instruction caches), and dS is formed from P
+      // as computed instead of as rounded for the dV product: P stays in the
+      // registers of S (dP then comes in halves).  The rounding of P would add to
+      // dQ and dK as much as dS's own.
+      if constexpr (kWindow) {
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          const uint32_t seen = below(hi - ch * 32) & ~below(lo - ch * 32);
+        for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
           for (int e2 = 0; e2 < 16; ++e2) {
             float p0, p1;
             exp_pair(ch, e2, p0, p1);
-            if (!(seen & (1u << (2 * e2))) || !row_valid) p0 = 0.0f;
-            if (!(seen & (2u << (2 * e2))) || !row_valid) p1 = 0.0f;
-            pw[ch * 16 + e2] = pack_bf16x2(p0, p1);
-            keep_pair(ch, e2, p0, p1);
+            sr[ch][2 * e2] = __float_as_uint(p0);
+            sr[ch][2 * e2 + 1] = __float_as_uint(p1);
+          }
+        if (diag || !row_valid) {
+          // the key sees the query columns [lo, lo + window) of the tile
+          const int lo = (kt - i) * kBlockM + kr - wg * 64;
+          const int hi = lo + p.window;
+          auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            const uint32_t seen = row_valid ? below(hi - ch * 32) & ~below(lo - ch * 32) : 0u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen & (1u << e))) sr[ch][e] = 0u;
           }
         }
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+          for (int e2 = 0; e2 < 16; ++e2)
+            pw[ch * 16 + e2] = pack_bf16x2(__uint_as_float(sr[ch][2 * e2]), __uint_as_float(sr[ch][2 * e2 + 1]));
       } else if (diag) {  // uniform: only the diagonal tile pays for the mask
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
@@ -739,9 +754,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           for (int e2 = 0; e2 < 16; ++e2) {
             float p0, p1;
             exp_pair(ch, e2, p0, p1);
-            if (kWindow && !row_valid) p0 = p1 = 0.0f;
             pw[ch * 16 + e2] = pack_bf16x2(p0, p1);
-            keep_pair(ch, e2, p0, p1);
           }
       }
       if (!kWindow && !row_valid) {

@@ -121,31 +121,6 @@ enum : unsigned int {
   kSiteKVFree = 0x21E,
 };
 
-__device__ __forceinline__ uint32_t globaltimer_lo() {
-  uint32_t t;
-  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-  return t;
-}
-
-// mbar_wait in few instructions: a 32-bit clock, and the abort flag holds the
-// site, which the CTA's end records (see above).
-__device__ __forceinline__ bool wait_on(uint32_t b, uint32_t parity, const WaitCtl& ctl, unsigned int site) {
-  static_assert(kWaitLimitNs < 0xffffffffull, "32-bit clock");
-  if (mbar_try_wait(b, parity)) return true;
-  const uint32_t t0 = globaltimer_lo();
-#pragma unroll 1
-  do {
-    if (mbar_try_wait(b, parity)) return true;
-    if (*ctl.abort_flag) return false;
-  } while (globaltimer_lo() - t0 < static_cast<uint32_t>(kWaitLimitNs));
-  *ctl.abort_flag = static_cast<int>(site);
-  return false;
-}
-// The same by a whole converged warp, with a uniform result.
-__device__ __forceinline__ bool wait_on_warp(uint32_t b, uint32_t parity, const WaitCtl& ctl, unsigned int site) {
-  return __all_sync(0xffffffffu, wait_on(b, parity, ctl, site));
-}
-
 // Block `blk` of the list of items: a key tile of a key head (from split_from
 // on a part of its query tiles) and its query tiles i_first..i_last, head by head.
 struct WinItem {
@@ -287,7 +262,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
       int n = 0;
       bool ok = true;
       auto wait = [&](int b, uint32_t parity, unsigned int site) {
-        ok = wait_on(bar(b), parity, ctl, site);
+        ok = mbar_wait_short(bar(b), parity, ctl, site);
         return ok = __all_sync(0xffffffffu, ok);
       };
       int blk = blockIdx.x;
@@ -342,7 +317,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         if (!more) break;
         // the buffers are free once dV and dK of the item before the last have
         // left them
-        if (m > 1 && !(ok = wait_on(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
+        if (m > 1 && !(ok = mbar_wait_short(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
         load_kv(m++, t);
       }
       if (!ok)
@@ -392,22 +367,22 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         const int s = n % C::kStages;
         const int next_m = n >= 0 && last ? m + 1 : m;
         if (n >= 0) {
-          if (!(ok = wait_on_warp(bar(C::kBarPFull), n & 1, ctl, kSitePFull))) break;
-          if (first && m > 0 && !(ok = wait_on_warp(bar(C::kBarAccFree), (m - 1) & 1, ctl, kSiteAccFree))) break;
+          if (!(ok = mbar_wait_short_warp(bar(C::kBarPFull), n & 1, ctl, kSitePFull))) break;
+          if (first && m > 0 && !(ok = mbar_wait_short_warp(bar(C::kBarAccFree), (m - 1) & 1, ctl, kSiteAccFree))) break;
           tc_fence_after();
           issue_tn(C::kColS, sbase + C::kDOOff + s * C::kTileBytes, C::kColDV, !first);
         }
         // the next tile's S^T over P^T, which dV (issued before it) has read
         if (next) {
           const int s1 = (n + 1) % C::kStages;
-          if (last && !(ok = wait_on_warp(bar(C::kBarKV + (next_m & 1)), (next_m / 2) & 1, ctl, kSiteKV))) break;
-          if (!(ok = wait_on_warp(bar(C::kBarStFull + s1), ((n + 1) / C::kStages) & 1, ctl, kSiteStFull))) break;
+          if (last && !(ok = mbar_wait_short_warp(bar(C::kBarKV + (next_m & 1)), (next_m / 2) & 1, ctl, kSiteKV))) break;
+          if (!(ok = mbar_wait_short_warp(bar(C::kBarStFull + s1), ((n + 1) / C::kStages) & 1, ctl, kSiteStFull))) break;
           tc_fence_after();
           issue_nt(k_smem(next_m), sbase + C::kQOff + s1 * C::kTileBytes, C::kColS);
           mma_commit<true>(bar(C::kBarSFull));
         }
         if (n >= 0) {
-          if (!(ok = wait_on_warp(bar(C::kBarDSTmem), n & 1, ctl, kSiteDSTmem))) break;
+          if (!(ok = mbar_wait_short_warp(bar(C::kBarDSTmem), n & 1, ctl, kSiteDSTmem))) break;
           tc_fence_after();
           issue_tn(C::kColDP, sbase + C::kQOff + s * C::kTileBytes, C::kColDK, !first);
           mma_commit<true>(bar(C::kBarStEmpty + s));  // the last to read the stage
@@ -417,8 +392,8 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
           mma_commit<true>(bar(C::kBarDPFull));
         }
         if (n >= 0) {
-          if (!(ok = wait_on_warp(bar(C::kBarDSFull), n & 1, ctl, kSiteDSFull))) break;
-          if (n > 0 && !(ok = wait_on_warp(bar(C::kBarDQEmpty), (n - 1) & 1, ctl, kSiteDQEmpty))) break;
+          if (!(ok = mbar_wait_short_warp(bar(C::kBarDSFull), n & 1, ctl, kSiteDSFull))) break;
+          if (n > 0 && !(ok = mbar_wait_short_warp(bar(C::kBarDQEmpty), (n - 1) & 1, ctl, kSiteDQEmpty))) break;
           tc_fence_after();
           issue_dq(sbase + C::kDsOff, k_smem(m));
           mma_commit<true>(bar(C::kBarDQFull));
@@ -441,7 +416,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         mma_commit<true>(bar(C::kBarMmaDone));
         mbar_wait_drain(bar(C::kBarMmaDone), m & 1);
       } else if (m > 0) {
-        wait_on_warp(bar(C::kBarMmaDone), (m - 1) & 1, ctl, kSiteMmaDone);
+        mbar_wait_short_warp(bar(C::kBarMmaDone), (m - 1) & 1, ctl, kSiteMmaDone);
       }
     }
   } else if (warp >= C::kDrainWarp0) {
@@ -457,7 +432,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     WinItem t;
     for (; ok && next_item(p, blk, stride, total, t); blk += stride) {
       for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
-        ok = wait_on(bar(C::kBarDQFull), n & 1, ctl, kSiteDQFull);
+        ok = mbar_wait_short(bar(C::kBarDQFull), n & 1, ctl, kSiteDQFull);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           // release drain warps already waiting at this tile's barriers below (the
@@ -530,12 +505,12 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         // the diagonal tile, those whose last rows are past some key's window,
         // and all of a key tile with rows past N
         const bool edge = t.i == t.kt || (t.i - t.kt) * kBlockM + kBlockM - 1 >= p.window || last_tile;
-        ok = wait_on(bar(C::kBarSFull), n & 1, ctl, kSiteSFull);
+        ok = mbar_wait_short(bar(C::kBarSFull), n & 1, ctl, kSiteSFull);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         // returns at once (S^T was issued after the stage landed); makes the
         // loader's rows visible
-        ok = wait_on(bar(C::kBarStFull + s), (n / C::kStages) & 1, ctl, kSiteStFull);
+        ok = mbar_wait_short(bar(C::kBarStFull + s), (n / C::kStages) & 1, ctl, kSiteStFull);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         // this warpgroup's 64 queries' -LSE log2 e and -D
         const float4* rl4 = reinterpret_cast<const float4*>(smem + C::kRowsOff + 2 * s * C::kRowBytes) + wg * 16;
@@ -590,7 +565,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
 
         // dS = P (dP - D)^T (unscaled): to tensor memory (for dK) and shared
         // memory (for dQ)
-        ok = wait_on(bar(C::kBarDPFull), n & 1, ctl, kSiteDPFull);
+        ok = mbar_wait_short(bar(C::kBarDPFull), n & 1, ctl, kSiteDPFull);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         uint32_t dsw[32];
@@ -616,7 +591,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         warp_arrive(bar(C::kBarDSTmem));
         // dQ of the tile before has read the buffer
         if (n > 0) {
-          ok = wait_on(bar(C::kBarDQFull), (n - 1) & 1, ctl, kSiteDQFull);
+          ok = mbar_wait_short(bar(C::kBarDQFull), (n - 1) & 1, ctl, kSiteDQFull);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
         // [query half][key row][64 queries], 16-byte chunk index XOR (key row mod 8)
@@ -641,7 +616,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
       else if (p.sink_main != nullptr && t.kt == 0 && kr < p.sinks)
         raw = p.sink_main + ((static_cast<size_t>(t.bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D;
       if (ok && t.n_iter > 0) {
-        ok = wait_on(bar(C::kBarMmaDone), m & 1, ctl, kSiteMmaDone);
+        ok = mbar_wait_short(bar(C::kBarMmaDone), m & 1, ctl, kSiteMmaDone);
         ok = __all_sync(0xffffffffu, ok);
       }
       // the warpgroup goes on, or gives up, together: its warps meet below
@@ -702,7 +677,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) record_status(p.status, kStatusTimeout, static_cast<unsigned int>(*abort_flag));
+  record_abort(ctl);
   if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmemCols);

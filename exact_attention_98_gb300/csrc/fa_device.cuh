@@ -137,6 +137,36 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, co
   return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, ctl, site, limit_ns));
 }
 
+// mbar_wait in few instructions, for kernels whose roles' code outgrows the
+// instruction caches: a 32-bit clock, and the abort flag takes the site, which
+// the CTA records at its end (record_abort, after a __syncthreads).
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
+                                                unsigned int site) {
+  static_assert(kWaitLimitNs < 0xffffffffull, "32-bit clock");
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = globaltimer_lo();
+#pragma unroll 1
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*ctl.abort_flag) return false;
+  } while (globaltimer_lo() - t0 < static_cast<uint32_t>(kWaitLimitNs));
+  *ctl.abort_flag = static_cast<int>(site);
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait_short_warp(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
+                                                     unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, ctl, site));
+}
+__device__ __forceinline__ void record_abort(const WaitCtl& ctl) {
+  if (threadIdx.x == 0 && *ctl.abort_flag)
+    record_status(ctl.status, kStatusTimeout, static_cast<unsigned int>(*ctl.abort_flag));
+}
+
 // Clean-up wait on the give-up path: ignores the abort flag, bounded by
 // kDrainLimitNs, records nothing.  Used to let this CTA's own TMA copies and
 // MMAs finish before it frees tensor memory and exits.
