@@ -377,7 +377,7 @@ struct FwdPagedParams {
 
 // Warps of the paged forward at most, per SM and on the current device (0 on an
 // error), and rows of a block at most: its workspace.
-constexpr int kPagedWorkersPerSm = 16;
+constexpr int kPagedWorkersPerSm = 12;
 constexpr int kPagedRows = 16;
 int fwd_paged_workers();
 // One launch of the forward and one of the join of its split segments.

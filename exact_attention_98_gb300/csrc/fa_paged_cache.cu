@@ -11,7 +11,17 @@
 // rounded to nearest, ties to even.  A block that holds an infinity or a NaN
 // gets the scale NaN: it reads back as NaN.
 //
-// Bound by HBM: every row is read once and written once.
+// Bound by HBM: every row is read once and written once.  A thread takes 16
+// elements (a scale's block), the next row's loads in flight while it works on
+// one; a block takes 4 tokens, so that looking up their places (page table,
+// lengths) is paid once for 4, or 1 where that would leave SMs idle.  Four
+// blocks to an SM keep enough loads in flight.  Measured (K, V and Q, d = 128):
+// bf16, 16384 tokens of 4 key and 16 query heads: 31.4 us, 5.2 TB/s of 6.7 (one
+// token a block 51); 4 bits, 18006 tokens of 8 and 32 heads, with the rows
+// read back: 97 us, 4.1 TB/s (132).  The 4-bit append alone (77 us under a
+// profiler) issues 57% of its slots: the divisions by the scale, each correctly
+// rounded, and the packing take turns with the loads.  Not kept: 2 or 8 tokens a
+// block, a ninth warp that looks the next places up ahead.
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -424,7 +434,8 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
   }
 }
 
-// One token per block while that leaves multiprocessors idle otherwise.
+// One token per block where more would leave multiprocessors idle (a decode step
+// of 8 tokens is 37 us either way, its host calls; for prompts see the top).
 int tokens_per_block(int rows) { return rows >= 152 * 8 * kMaxTokens ? kMaxTokens : 1; }
 
 }  // namespace
