@@ -264,6 +264,33 @@ def test_streams_keep_their_memory():
 
 
 @pytest.mark.gpu
+def test_two_backwards_at_once():
+    """Persistent CTAs of one call beside another's, on streams of their own: each
+    gives what it gives alone, dk and dv bit for bit."""
+    from exact_attention_98_gb300 import fa
+
+    calls = []
+    for d, Hkv in ((64, 16), (128, 4)):
+        q, k, v, do = (t.cuda() for t in inputs(2, 16, Hkv, 1500, d, d))
+        o, lse = fa.window_forward(q, k, v, 400, 3)
+        calls.append((q, k, v, o, lse, do))
+    alone = [fa.window_backward(*c, 400, 3) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        both = []
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                both.append(fa.window_backward(*c, 400, 3))
+        torch.cuda.synchronize()
+        assert fa.fa_last_device_status() == fa.FA_OK, hex(fa.fa_last_device_site())
+        for (dq, dk, dv), ref in zip(both, alone):
+            assert torch.equal(dk, ref[1]) and torch.equal(dv, ref[2])
+            # the order of dq's fp32 additions varies, which can move a rounding to bf16
+            assert (dq.float() - ref[0].float()).abs().max() <= 2 * HALF * ref[0].float().abs().max()
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """Tensors of more than 2^31 elements: the last key head's results are those of that head alone."""
     from exact_attention_98_gb300 import fa
