@@ -51,12 +51,17 @@ enum : unsigned int {
   kSitePagedFull = 0x511,
 };
 
-// A running reference may stay this much (log2 units) below the true maximum
-// before the sums and accumulators are rescaled.  bf16 keeps the dominant
-// weight near 1 (its rounding error reaches O); fp16's spacing is 8 times finer
-// and its range holds 2^8 with room below.
+// A running reference is set kBelow (log2 units) below the maximum at hand, and
+// the sums and accumulators are rescaled once a score is kSlack above that
+// maximum.  bf16 keeps the dominant weight near 1 (its rounding error reaches O)
+// and has exponents enough for the small ones.  fp16's spacing is 8 times finer
+// but ends at 2^-24: with the largest weight at 2^7 to 2^15 a weight is held
+// down to 2^-32 of it, so that a long tail under one dominating position counts
+// in O as it does in the sum (with kBelow = 0, 2^17 positions at 2^-25 were lost).
 template <bool FP4>
 __device__ constexpr float kSlack = FP4 ? 8.0f : 2.0f;
+template <bool FP4>
+__device__ constexpr float kBelow = FP4 ? 7.0f : 0.0f;
 
 template <int D, bool FP4, int TILES>
 struct PagedCfg {
@@ -591,13 +596,14 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             if (mx > lim[t][e]) {
-              const float a = lim[t][e] == -INFINITY ? 0.0f : ex2_mufu(-mx);
-              ref[t][e] += mx;
-              lim[t][e] = kSlack<FP4>;
+              const float up = mx - kBelow<FP4>;
+              const float a = lim[t][e] == -INFINITY ? 0.0f : ex2_mufu(-up);
+              ref[t][e] += up;
+              lim[t][e] = kSlack<FP4> + kBelow<FP4>;
 #pragma unroll
               for (int grp = 0; grp < kGroups; ++grp) {
-                s[grp][t][e] -= mx;
-                s[grp][t][e + 2] -= mx;
+                s[grp][t][e] -= up;
+                s[grp][t][e + 2] -= up;
               }
               l[t][e] *= a;
 #pragma unroll
