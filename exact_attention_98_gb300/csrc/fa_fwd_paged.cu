@@ -205,6 +205,9 @@ struct Loader {
   unsigned long long at;
   int batch;   // units of the batch left, 0: to be loaded
   int stage;   // the next copy's
+  // Parts of a stage that were not copied, 4 bits a stage: bit i the unit's i-th
+  // page (0 where a page holds the whole unit).  The stage keeps what it held there.
+  unsigned int holes;
 
   __device__ __forceinline__ void next(const FwdPagedParams& p, uint32_t ring, uint32_t bars, int lane) {
     if (w.left <= 0) return;
@@ -247,6 +250,8 @@ struct Loader {
         __shfl_sync(0xffffffffu, at, (((32 >> subs_shift) - batch) << subs_shift) + sub);
     const bool mine = lane < (parts ? 4 : 1 << subs_shift) && from != (FP4 ? 0ull : ~0ull);
     const unsigned int live = __ballot_sync(0xffffffffu, mine);
+    const unsigned int hole = parts ? (live == 0u ? 1u : 0u) : ~live & ((1u << (1 << subs_shift)) - 1u);
+    holes = (holes & ~(15u << (4 * stage))) | (hole << (4 * stage));
     if (lane == 0)
       mbar_arrive_expect_tx(bar, __popc(live) * (parts ? C::kStageBytes / 4 : C::kStageBytes >> subs_shift));
     __syncwarp();
@@ -375,6 +380,7 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
   load.batch = 0;
   load.at = 0;
   load.stage = 0;
+  load.holes = 0u;
   for (int i = 0; i < C::kStages; ++i) load.next(p, ring_s, bars, lane);
 
   const int g = lane >> 2, c = lane & 3;
@@ -480,9 +486,10 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
       const int unit_key = (u < w.s.first ? u : u + w.s.skip) * C::kUnit;
       const uint8_t* st = ring + stage * C::kStageBytes;
       const uint32_t st_s = ring_s + stage * C::kStageBytes;
-      // every position visible to every row?
-      const bool edge =
-          unit_key + C::kUnit - 1 > p_lo || (unit_key < p_hi - p.window + 1 && unit_key + C::kUnit > p.sinks);
+      const unsigned int hole = (load.holes >> (4 * stage)) & 15u;
+      // every position there, and visible to every row?
+      const bool edge = hole != 0u || unit_key + C::kUnit - 1 > p_lo ||
+                        (unit_key < p_hi - p.window + 1 && unit_key + C::kUnit > p.sinks);
       // S^T = K Q^T: key unit_key + 16 grp + g (0, 1) or + 8 (2, 3) of pairs 2c, 2c + 1
       float s[kGroups][TILES][4];
 #pragma unroll
@@ -573,6 +580,16 @@ __global__ void __launch_bounds__(32 * PagedCfg<D, FP4, TILES>::kWarps, PagedCfg
               const int q = pos[t][e & 1];
               if (j > q || (j <= q - p.window && j >= p.sinks)) s[grp][t][e] = -INFINITY;
             }
+        // pages outside the cache: no row sees their positions
+#pragma unroll
+        for (int grp = 0; grp < kGroups; ++grp)
+          if ((hole >> ((grp * 16) >> sub_shift)) & 1u) {
+            keep &= ~(15u << (4 * grp));
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[grp][t][e] = -INFINITY;
+          }
       }
       bool over = false;
 #pragma unroll

@@ -403,7 +403,8 @@ int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void
  * included (append first).  The row at position p sees the positions j <= p
  * with p - j < window, and the positions j < sinks (j <= p):
  *   O = softmax(scale q K^T) V over these, LSE as fa_fwd.
- * A row that sees nothing (a sequence of length 0) gets O = 0, LSE = -inf.
+ * Positions on a page outside the cache count as masked (FA_ERR_INVALID_ARG is
+ * recorded).  A row that sees nothing (a sequence of length 0) gets O = 0, LSE = -inf.
  *   q        : in,  bf16 with H heads, strides as fa_paged_append; query head
  *              h reads key head h / (H / Hkv)
  *   o        : out, bf16 [rows, H, d]; lse: out, fp32 [rows, H]; padding rows

@@ -1,0 +1,101 @@
+"""Tables of the paged cache that cannot be followed: what is skipped, what is
+recorded, and what the rows that are left get.  Bounds as in test_paged.py."""
+import numpy as np
+import pytest
+import torch
+
+from paged import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+def q_of(bt, H, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(bt.T, H, bt.d, generator=g).to(torch.bfloat16)
+
+
+def on_gpu(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def status(fa):
+    code = fa.fa_last_device_status()
+    return code, fa.fa_last_device_site() if code != fa.FA_OK else 0
+
+
+def attend_some(q, rows_k, rows_v, length, window, sinks, scale, gone):
+    """64-bit attention of a sequence's last rows q [n, H, d] over its positions but those where `gone`
+    holds: O, LSE, and the bounds' sum p |v| and largest sum |q k| (zeros where nothing is left)."""
+    n, H, d = q.shape
+    Hkv = rows_k.shape[1]
+    o, mag = np.zeros((n, H, d)), np.zeros((n, H, d))
+    lse, dot = np.full((n, H), -np.inf), np.zeros((n, H))
+    for i in range(n):
+        p = length - n + i
+        j = np.arange(max(p + 1, 0))
+        keep = ~gone[j]
+        if window:
+            keep &= (p - j < window) | (j < sinks)
+        j = j[keep]
+        if len(j) == 0:
+            continue
+        for h in range(H):
+            k, v = rows_k[j, h * Hkv // H], rows_v[j, h * Hkv // H]
+            s = scale * (k @ q[i, h])
+            w = np.exp(s - s.max())
+            lse[i, h] = s.max() + np.log(w.sum())
+            w /= w.sum()
+            o[i, h], mag[i, h] = w @ v, w @ np.abs(v)
+            dot[i, h] = scale * (np.abs(k) @ np.abs(q[i, h])).max()
+    return o, lse, mag, dot
+
+
+def check_some(bt, q, o, lse, window, sinks, gone):
+    p_eps = 2.0 ** -8 if bt.fmt == "bf16" else 2.0 ** -11
+    o, lse, q64 = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+    for b, length in enumerate(bt.lens):
+        at = slice(bt.cu_list[b], bt.cu_list[b + 1])
+        ref, l_ref, mag, dot = attend_some(q64[at], bt.rows[0][b], bt.rows[1][b], length, window, sinks,
+                                           bt.fa.default_scale(bt.d), gone[b])
+        s_err = 2.0 ** -17 * dot + 2.0 ** -20
+        bound = mag * (p_eps + 2 * s_err[..., None]) + 2.0 ** -8 * np.abs(ref) * 1.01 + length * 2.0 ** -32 * 6.0
+        assert (np.abs(o[at] - ref) <= bound).all(), (b, np.nanmax(np.abs(o[at] - ref) / bound))
+        empty = np.isinf(l_ref)
+        assert np.array_equal(np.isneginf(lse[at]), empty), b
+        assert (np.abs(lse[at][~empty] - l_ref[~empty]) <= (s_err + 2.0 ** -20 * np.abs(l_ref))[~empty]).all(), b
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("d,page,group,lens,new,window,sinks,bad", [
+    # bad: (sequence, page of the sequence)
+    (64, 16, 2, [200, 150], [1, 1], 0, 0, [(1, 2), (1, 9)]),
+    (128, 16, 12, [333, 50, 90], [2, 1, 1], 0, 0, [(0, 0), (0, 3), (0, 7), (2, 4), (2, 5)]),
+    (128, 32, 4, [700, 260], [1, 3], 200, 5, [(0, 0), (0, 20), (1, 3)]),
+    (64, 64, 1, [900, 64], [1, 1], 0, 0, [(0, 3), (1, 0)]),                 # nothing left of the second
+    (128, 128, 4, [2000, 40], [4, 1], 0, 0, [(0, 0), (0, 15), (1, 0)]),
+    (64, 16, 1, [17], [17], 0, 0, [(0, 0)]),                                # the first rows see nothing
+])
+def test_positions_on_pages_outside_the_cache_are_left_out(fmt, d, page, group, lens, new, window, sinks, bad):
+    """They count as masked, in every row of every call, whatever the kernel's memory held before."""
+    Hkv = 2
+    bt = Batch(fmt, d, page, Hkv, lens, new, seed=sum(lens))
+    fa = bt.fa
+    q = q_of(bt, Hkv * group)
+    other = Batch(fmt, d, page, Hkv, [5000, 300], [1, 1], seed=99)      # leaves rows of its own behind
+    q_other = q_of(other, Hkv * group)
+    gone = [np.zeros(n, bool) for n in lens]
+    for b, i in bad:
+        gone[b][i * page: (i + 1) * page] = True
+    first = None
+    for number in (-1, bt.num_pages, 2 ** 31 - 1, -2 ** 31):
+        table = bt.table.copy()
+        for b, i in bad:
+            table[b, i] = number
+        bt.page_table = on_gpu(table)
+        other.forward(q_other.cuda())
+        assert status(fa) == (fa.FA_OK, 0)
+        o, lse = bt.forward(q.cuda(), window=window, sinks=sinks)
+        assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x503)
+        check_some(bt, q, o, lse, window, sinks, gone)
+        first = (o, lse) if first is None else first
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
