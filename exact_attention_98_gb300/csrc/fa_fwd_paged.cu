@@ -106,9 +106,9 @@ __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool re
   if (report && (bad || extra > 0)) record_status(p.status, kStatusInvalid, kSitePagedRows);
   const long long most = static_cast<long long>(p.c.max_pages) << p.c.page_shift;
   s.len = p.c.seq_lens[b];
-  if (s.len < 0 || s.len > most) {
+  if (s.len < 0 || s.len > most) {  // no telling where its rows are: they see nothing
     if (report) record_status(p.status, kStatusInvalid, kSitePagedLength);
-    s.len = s.len < 0 ? 0 : static_cast<int>(most);
+    s.len = 0;
   }
   s.len = max(0, s.len - extra);
   const int p0 = max(0, s.len - s.n);

@@ -331,8 +331,8 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
  *
  * page_table, seq_lens, cu_new, k_scale and v_scale are read on the device
  * (a captured graph serves whatever they hold at each replay) and so cannot be
- * checked by the call.  The kernels check them: a sequence longer than its
- * pages (or than the rotation's table), a page outside the cache, rows that
+ * checked by the call.  The kernels check them: a position past its sequence's
+ * pages (or the rotation's table), a page outside the cache, rows that
  * do not fit cu_new are skipped, and FA_ERR_INVALID_ARG is recorded in the
  * device status word.  Pages that one call writes must belong to one position
  * of one sequence each; pages that are only read may be shared.
@@ -404,7 +404,8 @@ int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void
  * with p - j < window, and the positions j < sinks (j <= p):
  *   O = softmax(scale q K^T) V over these, LSE as fa_fwd.
  * Positions on a page outside the cache count as masked (FA_ERR_INVALID_ARG is
- * recorded).  A row that sees nothing (a sequence of length 0) gets O = 0, LSE = -inf.
+ * recorded).  A row that sees nothing (a sequence of length 0, or longer than its
+ * pages, which is recorded) gets O = 0, LSE = -inf.
  *   q        : in,  bf16 with H heads, strides as fa_paged_append; query head
  *              h reads key head h / (H / Hkv)
  *   o        : out, bf16 [rows, H, d]; lse: out, fp32 [rows, H]; padding rows

@@ -99,3 +99,40 @@ def test_positions_on_pages_outside_the_cache_are_left_out(fmt, d, page, group, 
         check_some(bt, q, o, lse, window, sinks, gone)
         first = (o, lse) if first is None else first
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 3)])
+def test_a_sequence_longer_than_its_pages_is_empty(fmt, window, sinks):
+    """Its rows see nothing, as one of a negative length: its pages cannot say where they are.  The others
+    are as before.  Append and read go by row: one whose position is past the pages has no place."""
+    bt = Batch(fmt, 64, 16, 1, [40, 64, 33], [1, 2, 1], seed=3, max_pages=4)
+    fa = bt.fa
+    q = q_of(bt, 3)
+    want = bt.forward(q.cuda(), window=window, sinks=sinks)
+    assert status(fa) == (fa.FA_OK, 0)
+    for length in (65, 66, 1000, 2 ** 31 - 1, -1, -2 ** 31):
+        bt.seq_lens = on_gpu([40, length, 33])
+        o, lse = bt.forward(q.cuda(), window=window, sinks=sinks)
+        assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x502)
+        assert (o[1:3] == 0).all() and torch.isneginf(lse[1:3]).all(), length
+        for i in (0, 3):
+            assert torch.equal(o[i], want[0][i]) and torch.equal(lse[i], want[1][i])
+    bt.seq_lens = on_gpu([40, 65, 33])       # new rows at 63, which has a place, and 64
+    x = torch.randn(4, 1, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    before = bt.pages.clone()
+    fa.paged_append(x, x, *bt.tables(), **bt.kw)
+    assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x502)
+    places = [int(bt.table[0, 2]), int(bt.table[1, 3]), int(bt.table[2, 2])]
+    others = [i for i in range(bt.num_pages) if i not in places]
+    assert torch.equal(before[others].view(torch.uint8), bt.pages[others].view(torch.uint8))
+    k, v = fa.paged_read(*bt.tables(), 4, 64, **bt.kw)
+    assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x502)
+    assert (k[2] == 0).all() and (v[2] == 0).all()
+    bt.seq_lens = on_gpu([40, 64, 33])
+    k2, v2 = fa.paged_read(bt.pages, bt.page_table, bt.seq_lens, on_gpu([0, 1, 2, 3]), 3, 64, **bt.kw)
+    assert status(fa) == (fa.FA_OK, 0)
+    for i, j in ((0, 0), (1, 1), (3, 2)):
+        assert torch.equal(k[i], k2[j]) and torch.equal(v[i], v2[j])
+    if fmt == "bf16":
+        assert torch.equal(k[1], x[1]) and torch.equal(v[1], x[1])
