@@ -95,6 +95,11 @@ struct Seq {
   int blocks;       // blocks of rows
 };
 
+// The first position that the window of a sequence's rows reaches.
+__device__ __forceinline__ int seq_first(const FwdPagedParams& p, const Seq& s) {
+  return p.window == INT_MAX ? 0 : max(0, max(0, s.len - s.n) - p.window + 1);
+}
+
 template <class C>
 __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool report) {
   Seq s;
@@ -111,10 +116,8 @@ __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool re
     s.len = 0;
   }
   s.len = max(0, s.len - extra);
-  const int p0 = max(0, s.len - s.n);
-  const int lo = p.window == INT_MAX ? 0 : max(0, p0 - p.window + 1);
   const int end = (s.len + C::kUnit - 1) / C::kUnit;
-  const int win = lo / C::kUnit;
+  const int win = seq_first(p, s) / C::kUnit;
   s.first = min((min(p.sinks, s.len) + C::kUnit - 1) / C::kUnit, win);
   s.skip = win - s.first;
   s.loads = s.n > 0 ? end - s.skip : 0;
@@ -225,7 +228,9 @@ struct Loader {
       const int u = w.unit + (lane >> subs_shift);
       const int key = (u < w.s.first ? u : u + w.s.skip) * C::kUnit + ((lane & ((1 << subs_shift) - 1)) << shift);
       at = FP4 ? 0ull : ~0ull;
-      if (u < w.s.loads && u < w.unit + w.left && key < w.s.len) {
+      // (a page of a unit that no row of the sequence sees may have been given back)
+      const bool seen = key < p.sinks || key + (1 << shift) > seq_first(p, w.s);
+      if (u < w.s.loads && u < w.unit + w.left && key < w.s.len && seen) {
         const int page = p.c.page_table[static_cast<size_t>(w.b) * p.c.max_pages + (key >> p.c.page_shift)];
         if (page < 0 || page >= p.c.num_pages) {
           record_status(p.status, kStatusInvalid, kSitePagedPage);

@@ -418,7 +418,9 @@ int fa_paged_read(const fa_paged_cache* cache, const int* cu_new, int rows, void
  *   workspace: fa_fwd_paged_workspace_bytes() bytes on the current device,
  *              256-byte aligned, contents on entry irrelevant
  * What positions outside every row's sight hold (the rest of a page, too) does
- * not matter, infinities and NaN included; one that some row of the same call
+ * not matter, infinities and NaN included, and the page table's entries of pages
+ * without a position in sight are not looked at: such pages may be given
+ * back as a window moves on.  A position that some row of the same call
  * sees must be finite where another does not see it.
  * The work does not depend on how lengths are spread over sequences; cached
  * rows are read once for every 16 (row, query head of the group) pairs, so

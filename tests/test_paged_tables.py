@@ -136,3 +136,33 @@ def test_a_sequence_longer_than_its_pages_is_empty(fmt, window, sinks):
         assert torch.equal(k[i], k2[j]) and torch.equal(v[i], v2[j])
     if fmt == "bf16":
         assert torch.equal(k[1], x[1]) and torch.equal(v[1], x[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("window,sinks,new", [(40, 4, [1, 1]), (40, 0, [1, 1]), (100, 20, [3, 2]), (1, 1, [1, 1]),
+                                              (130, 64, [17, 1])])
+def test_pages_that_no_row_sees_may_be_freed(fmt, page, window, sinks, new):
+    """A server that gives pages back as the window moves on leaves entries that name no page: nothing is
+    recorded, and the results keep their bits."""
+    lens = [777, 250]
+    bt = Batch(fmt, 128, page, 2, lens, new, seed=page + window, max_pages=60)
+    fa = bt.fa
+    q = q_of(bt, 4)
+    want = bt.forward(q.cuda(), window=window, sinks=sinks)
+    assert status(fa) == (fa.FA_OK, 0)
+    freed = 0
+    for number in (-1, bt.num_pages):
+        table = bt.table.copy()
+        for b, n in enumerate(lens):
+            for i in range(bt.max_pages):
+                lo, hi = i * page, (i + 1) * page       # positions lo .. hi - 1
+                seen = lo < n and (lo < sinks or hi > n - new[b] - window + 1)
+                if not seen:
+                    freed += lo < n
+                    table[b, i] = number
+        bt.page_table = on_gpu(table)
+        o, lse = bt.forward(q.cuda(), window=window, sinks=sinks)
+        assert status(fa) == (fa.FA_OK, 0)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert freed > 0
