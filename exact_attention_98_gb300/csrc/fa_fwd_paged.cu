@@ -93,6 +93,7 @@ struct Seq {
   int units;        // units of a segment: its loads, or 1 without any
   int loads;        // units that hold positions
   int blocks;       // blocks of rows
+  int lo;           // the first position that the window of its rows reaches
 };
 
 // The first position that the window of a sequence's rows reaches.
@@ -117,7 +118,8 @@ __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool re
   }
   s.len = max(0, s.len - extra);
   const int end = (s.len + C::kUnit - 1) / C::kUnit;
-  const int win = seq_first(p, s) / C::kUnit;
+  s.lo = seq_first(p, s);
+  const int win = s.lo / C::kUnit;
   s.first = min((min(p.sinks, s.len) + C::kUnit - 1) / C::kUnit, win);
   s.skip = win - s.first;
   s.loads = s.n > 0 ? end - s.skip : 0;
@@ -229,7 +231,7 @@ struct Loader {
       const int key = (u < w.s.first ? u : u + w.s.skip) * C::kUnit + ((lane & ((1 << subs_shift) - 1)) << shift);
       at = FP4 ? 0ull : ~0ull;
       // (a page of a unit that no row of the sequence sees may have been given back)
-      const bool seen = key < p.sinks || key + (1 << shift) > seq_first(p, w.s);
+      const bool seen = key < p.sinks || key + (1 << shift) > w.s.lo;
       if (u < w.s.loads && u < w.unit + w.left && key < w.s.len && seen) {
         const int page = p.c.page_table[static_cast<size_t>(w.b) * p.c.max_pages + (key >> p.c.page_shift)];
         if (page < 0 || page >= p.c.num_pages) {
