@@ -39,7 +39,7 @@ struct PagedRow {
 
 // Row t belongs to the sequence b with cu[b] <= t < cu[b+1] and holds its
 // position seq_lens[b] - cu[b+1] + t (the rows are the sequence's last).
-__device__ __forceinline__ PagedRow paged_row(const PagedView& c, const int* cu, int t,
+__device__ __forceinline__ PagedRow paged_row(const PagedView& c, const int* cu, int rows, int t,
                                               unsigned int* status) {
   PagedRow r{-1, 0, -1};
   int lo = 0, hi = c.B;  // first b with cu[b+1] > t
@@ -49,7 +49,9 @@ __device__ __forceinline__ PagedRow paged_row(const PagedView& c, const int* cu,
     else lo = mid + 1;
   }
   if (lo == c.B || cu[lo] > t) return r;  // behind the last sequence
-  const long long pos = static_cast<long long>(c.seq_lens[lo]) - cu[lo + 1] + t;
+  const int end = cu[lo + 1];
+  if (cu[lo] < 0 || end > rows) return r;  // a sequence that does not fit the rows: recorded by its caller
+  const long long pos = static_cast<long long>(c.seq_lens[lo]) - end + t;
   if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) {
     record_status(status, kStatusInvalid, kSitePagedLength);
     return r;

@@ -235,6 +235,16 @@ struct Turn {
   }
 };
 
+// Records a sequence whose rows do not lie within the tensors' `rows`, or run
+// backwards.  By the threads of the first block.  (Not inlined, and ahead of the
+// append's first loads: append and read of 14631
+// 4-bit tokens 98.9 us inline behind them, 97.1 without the check, 96.5 so.)
+__device__ __noinline__ void paged_check_rows(const PagedView& c, const int* cu, int rows,
+                                              unsigned int* status) {
+  for (int b = threadIdx.x; b < c.B; b += blockDim.x)
+    if (cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > rows) record_status(status, kStatusInvalid, kSitePagedRows);
+}
+
 // A block of threads takes `tokens` rows of the batch: a thread two chunks of 8
 // elements of every 32nd (d = 128) or 64th (d = 64) row of their heads, Q's first,
 // then K's and V's, the next row's loads ahead of the present one's work.
@@ -243,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) paged_append_kernel(c
   constexpr int kPer = D / 16;  // threads of a row
   constexpr int kSlots = kThreads / kPer;
   grid_dependency_wait();
+  if (blockIdx.x == 0) paged_check_rows(p.c, p.cu, p.rows, p.status);
   __shared__ PagedRow rows[kMaxTokens];
   const int t0 = blockIdx.x * p.tokens;
   const int tokens = min(p.tokens, p.rows - t0);
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) paged_append_kernel(c
   if (q_rows > 0) fetch_q(r);
   else fetch_kv(r);
   if (threadIdx.x < tokens) {
-    PagedRow row = paged_row(p.c, p.cu, t0 + threadIdx.x, p.status);
+    PagedRow row = paged_row(p.c, p.cu, p.rows, t0 + threadIdx.x, p.status);
     if (row.page >= 0 && p.rot > 0 && row.pos >= p.rope_len) {
       record_status(p.status, kStatusInvalid, kSitePagedLength);
       row.page = -1;
@@ -360,11 +371,12 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
   if (threadIdx.x < p.tokens) {
     const int t = t0 + threadIdx.x;
     PagedRow r{-1, 0, -1};
-    if (t < p.rows) r = paged_row(p.c, p.cu, t, p.status);
+    if (t < p.rows) r = paged_row(p.c, p.cu, p.rows, t, p.status);
     rows[threadIdx.x] = r;
     owned[threadIdx.x] = t < p.rows && t >= p.cu[0] && t < p.cu[p.c.B];
   }
   __syncthreads();
+  if (blockIdx.x == 0) paged_check_rows(p.c, p.cu, p.rows, p.status);
   const int i = threadIdx.x % kPer;
   const size_t half_bytes = paged_half_bytes(FP4, 1 << p.c.page_shift, D);
   const int heads = 2 * p.c.Hkv;  // K heads, then V heads

@@ -332,9 +332,9 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
  * page_table, seq_lens, cu_new, k_scale and v_scale are read on the device
  * (a captured graph serves whatever they hold at each replay) and so cannot be
  * checked by the call.  The kernels check them: a position past its sequence's
- * pages (or the rotation's table), a page outside the cache, rows that
- * do not fit cu_new are skipped, and FA_ERR_INVALID_ARG is recorded in the
- * device status word.  Pages that one call writes must belong to one position
+ * pages (or the rotation's table), a page outside the cache, all rows of a
+ * sequence that reach past the tensors' rows, start before them or run backwards
+ * are skipped, and FA_ERR_INVALID_ARG is recorded in the device status word.  Pages that one call writes must belong to one position
  * of one sequence each; pages that are only read may be shared.
  */
 typedef enum {

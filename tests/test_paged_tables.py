@@ -166,3 +166,44 @@ def test_pages_that_no_row_sees_may_be_freed(fmt, page, window, sinks, new):
         assert status(fa) == (fa.FA_OK, 0)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert freed > 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+def test_rows_that_do_not_fit_are_recorded_by_append_and_read(fmt):
+    """A sequence whose rows reach past the tensors, start before them or run backwards: append and read
+    leave it out and say so, as the attention does; what fits keeps its place."""
+    bt = Batch(fmt, 64, 16, 1, [40, 50], [1, 1], seed=23, poison=False)
+    fa = bt.fa
+    x = torch.randn(2, 1, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    before = bt.pages.clone()
+    raw = lambda t: t.view(torch.uint8)  # noqa: E731
+    # offsets, and those of the sequences that are left (none said where a table runs backwards)
+    for cu, left in (([0, 1, 3], [0, 1, 1]), ([0, 1, 2 ** 31 - 1], [0, 1, 1]), ([0, 2, 5], [0, 2, 2]),
+                     ([0, 0, 3], [0, 0, 0]), ([-3, 1, 2], [1, 1, 2]), ([-1, -1, 2], [0, 0, 0]), ([0, 1, -5], None),
+                     ([0, 5, 2], None)):
+        c = on_gpu(cu)
+        bt.pages.copy_(before)
+        fa.paged_append(x, x, bt.pages, bt.page_table, bt.seq_lens, c, q=x, **bt.kw)
+        assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x501), cu
+        got = bt.pages.clone()
+        k, v = fa.paged_read(bt.pages, bt.page_table, bt.seq_lens, c, 2, 64, **bt.kw)
+        assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x501), cu
+        if left is None:
+            continue
+        bt.pages.copy_(before)
+        fa.paged_append(x, x, bt.pages, bt.page_table, bt.seq_lens, on_gpu(left), **bt.kw)
+        want_k, want_v = fa.paged_read(bt.pages, bt.page_table, bt.seq_lens, on_gpu(left), 2, 64, **bt.kw)
+        assert status(fa) == (fa.FA_OK, 0)
+        assert torch.equal(raw(got), raw(bt.pages)), cu
+        for i in range(left[0], left[2]):
+            assert torch.equal(k[i], want_k[i]) and torch.equal(v[i], want_v[i]), cu
+    # more sequences than a block has threads, the last of which does not fit
+    n = 700
+    bt = Batch(fmt, 64, 16, 1, [1] * n, [1] * n, seed=1, poison=False)
+    x = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    c = bt.cu.clone()
+    c[n] += 1
+    fa.paged_append(x, x, bt.pages, bt.page_table, bt.seq_lens, c, **bt.kw)
+    assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x501)
+    fa.paged_read(bt.pages, bt.page_table, bt.seq_lens, c, n, 64, **bt.kw)
+    assert status(fa) == (fa.FA_ERR_INVALID_ARG, 0x501)
