@@ -43,7 +43,8 @@
 // as a rank-1 bias: one more K = 16 MMA adds ones(128 x 16) * b^T onto S^T
 // (and onto dP^T), where column k of b holds the query's value split into
 // bf16 hi + lo parts (about 16 significant bits) in its first two entries and
-// zeros elsewhere.  The compute warps then need no per-query loads at all:
+// zeros elsewhere (window: a third part holds the rest of the fp32 value).
+// The compute warps then need no per-query loads at all:
 // P = exp2(c S'^T) and dS = P dP'^T (the softmax scale comes later).
 //
 // Warp roles (512 threads = four warpgroups):
@@ -393,11 +394,22 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           const size_t gi = static_cast<size_t>(walk.bh) * p.N + q;
           const float vl = (q < p.N) ? -p.lse[gi] * p.inv_scale : -1.0e4f;
           const float vd = (q < p.N) ? -p.dsum[gi] : 0.0f;
-          const int off = (r >> 3) * C::kBiasSbo + (r & 7) * 16;  // K half 0, entries 0 and 1
+          const int off = (r >> 3) * C::kBiasSbo + (r & 7) * 16;  // K half 0, from entry 0
           const float lh = __bfloat162float(__float2bfloat16_rn(vl));
           const float dh = __bfloat162float(__float2bfloat16_rn(vd));
-          *reinterpret_cast<uint32_t*>(bias_lse + off) = pack_bf16x2(lh, vl - lh);
-          *reinterpret_cast<uint32_t*>(bias_d + off) = pack_bf16x2(dh, vd - dh);
+          if constexpr (kWindow) {
+            // what hi + lo leave as a third entry: all 24 bits (two are 2^-18 off, 3%
+            // of P where LSE is 8000)
+            const float lm = __bfloat162float(__float2bfloat16_rn(vl - lh));
+            const float dm = __bfloat162float(__float2bfloat16_rn(vd - dh));
+            *reinterpret_cast<uint2*>(bias_lse + off) =
+                make_uint2(pack_bf16x2(lh, lm), pack_bf16x2(vl - lh - lm, 0.0f));
+            *reinterpret_cast<uint2*>(bias_d + off) =
+                make_uint2(pack_bf16x2(dh, dm), pack_bf16x2(vd - dh - dm, 0.0f));
+          } else {
+            *reinterpret_cast<uint32_t*>(bias_lse + off) = pack_bf16x2(lh, vl - lh);
+            *reinterpret_cast<uint32_t*>(bias_d + off) = pack_bf16x2(dh, vd - dh);
+          }
         }
         fence_proxy_async_smem();
         }
