@@ -657,8 +657,8 @@ int check_window(int B, int H, int Hkv, int N, int d, float scale, int window, i
   return FA_OK;
 }
 
-// How fa_window.cu cuts the queries of a key head: about two CTAs per SM of a
-// 152-SM device in all (what its shared memory allows), a part of 16 rows at
+// How fa_window.cu cuts the queries of a key head: about two CTAs per SM
+// in all (what its shared memory allows), a part of 16 rows at
 // least, 256 parts at most (the join reads them all).  Nothing when no query's window leaves a first token.
 struct SinkParts {
   int slots = 0, slot_rows = 0, sink_rows = 0;
@@ -668,7 +668,8 @@ SinkParts sink_parts(int B, int Hkv, int N, int d, int window, int sinks) {
   SinkParts s;
   if (sinks == 0 || N <= window) return s;
   const long long heads = static_cast<long long>(B) * Hkv;
-  long long slots = 304 / heads;
+  const int sms = sm_count();
+  long long slots = 2 * (sms > 0 ? sms : 152) / heads;  // (without a device: a size for GB300)
   if (slots > 256) slots = 256;
   if (slots < 1) slots = 1;
   const int per = static_cast<int>((N + slots - 1) / slots);

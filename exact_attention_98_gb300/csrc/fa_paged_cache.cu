@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
 
 // One token per block where more would leave multiprocessors idle (a decode step
 // of 8 tokens: 7.8 us, four to a block 8.1; for prompts see the top).
-int tokens_per_block(int rows) { return rows >= 152 * 8 * kMaxTokens ? kMaxTokens : 1; }
+int tokens_per_block(int rows) { return rows >= sm_count() * 8 * kMaxTokens ? kMaxTokens : 1; }
 
 }  // namespace
 

@@ -467,7 +467,7 @@ cudaError_t launch_window_post(WindowParams p, int d, cudaStream_t stream) {
   p.sink_blocks = p.slots > 0 ? p.sinks * 2 * p.BHkv : 0;
   p.tile_blocks = (p.n_kblk * p.BHkv - p.split_from) * 2 * (kBlockN / 16);
   const long long n8 = static_cast<long long>(p.BHkv) * p.group * p.N * (d / 8);
-  const long long blocks = (n8 + 255) / 256, cap = 152LL * 16;
+  const long long blocks = (n8 + 255) / 256, cap = (sm_count() > 0 ? sm_count() : 1) * 16LL;
   const dim3 grid(static_cast<unsigned int>(p.sink_blocks) + static_cast<unsigned int>(p.tile_blocks) +
                   static_cast<unsigned int>(blocks < cap ? blocks : cap));
   const cudaError_t err = launch_dependent(d == 128 ? fa_window_post_kernel<128> : fa_window_post_kernel<64>, grid,
