@@ -16,11 +16,12 @@
 // one; a block takes 4 tokens, so that looking up their places (page table,
 // lengths) is paid once for 4, or 1 where that would leave SMs idle.  Four
 // blocks to an SM keep enough loads in flight.  Measured (K, V and Q, d = 128):
-// bf16, 16384 tokens of 4 key and 16 query heads: 31.4 us, 5.2 TB/s of 6.7 (one
-// token a block 51); 4 bits, 18006 tokens of 8 and 32 heads, with the rows
-// read back: 97 us, 4.1 TB/s (132).  The 4-bit append alone (77 us under a
-// profiler) issues 57% of its slots: the divisions by the scale, each correctly
-// rounded, and the packing take turns with the loads.  Not kept: 2 or 8 tokens a
+// bf16, 13102 tokens of 4 key and 16 query heads: 31.3 us, 5.2 TB/s of 6.7; 4 bits,
+// 14631 tokens of 8 and 32 heads, with the rows read back: 96.5 us, 4.1 TB/s.  The
+// 4-bit append alone (77 us under a profiler) waits for its loads first (5.6
+// cycles per instruction), at 57% of its issue slots, which the divisions by the
+// scale, each correctly rounded, and the packing take; four blocks to an SM leave
+// it 64 registers, of which 20 spill.  Not kept: 2 or 8 tokens a
 // block, a ninth warp that looks the next places up ahead.
 #include "fa_paged.cuh"
 
@@ -446,9 +447,12 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
   }
 }
 
-// One token per block where more would leave multiprocessors idle (a decode step
-// of 8 tokens: 7.8 us, four to a block 8.1; for prompts see the top).
-int tokens_per_block(int rows) { return rows >= sm_count() * 8 * kMaxTokens ? kMaxTokens : 1; }
+// One token per block where more would leave multiprocessors idle, four from two
+// blocks of four to each of them on.  Append of bf16 (4 bits), one token a block
+// against four: 608 rows 8 us against 10 (12 against 14), 1216 rows 12 against 10 (16,
+// 16), 2432 rows 17 against 12 (25 against 21), 13000 rows 57 against 38 (88 against 70).
+// Read: even up to 608 rows, then 10 against 8, 12 against 8 (12 against 10), 32 against 18.
+int tokens_per_block(int rows) { return rows >= sm_count() * 2 * kMaxTokens ? kMaxTokens : 1; }
 
 }  // namespace
 
