@@ -123,7 +123,7 @@ enum : unsigned int {
 
 // Block `blk` of the list of items: a key tile of a key head (from split_from
 // on a part of its query tiles) and its query tiles i_first..i_last, head by head.
-struct WinItem {
+struct KeyItem {
   int bh, kt, k0;  // key head, key tile, its first key
   int part;        // of a split item, else -1
   int i_first, i_last;
@@ -138,8 +138,8 @@ struct WinItem {
   }
 };
 
-__device__ __forceinline__ WinItem win_item(const BwdParams& p, int blk) {
-  WinItem t;
+__device__ __forceinline__ KeyItem key_item(const BwdParams& p, int blk) {
+  KeyItem t;
   t.part = -1;
   int item = blk;
   if (blk >= p.split_from) {
@@ -173,9 +173,9 @@ __device__ __forceinline__ WinItem win_item(const BwdParams& p, int blk) {
 
 // The next block from `blk` on, in steps of `stride`, that has query tiles (a
 // part of a split item may have none); false if there is none.
-__device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stride, int total, WinItem& t) {
+__device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stride, int total, KeyItem& t) {
   for (; blk < total; blk += stride) {
-    t = win_item(p, blk);
+    t = key_item(p, blk);
     if (t.n_iter > 0) return true;
   }
   return false;
@@ -205,13 +205,13 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     if (lane == 0) mbar_arrive(b);
   };
   // m: the CTA's count of items that have query tiles
-  auto load_kv = [&](int m, const WinItem& t) {
+  auto load_kv = [&](int m, const KeyItem& t) {
     const int b = m & 1;
     mbar_arrive_expect_tx(bar(C::kBarKV + b), 2 * C::kTileBytes);
     tma_load_3d(sbase + C::kKOff + b * C::kTileBytes, &p.tm_k, bar(C::kBarKV + b), 0, t.k0, t.bh);
     tma_load_3d(sbase + C::kVOff + b * C::kTileBytes, &p.tm_v, bar(C::kBarKV + b), 0, t.k0, t.bh);
   };
-  auto load_tile = [&](int s, const WinItem& t) {
+  auto load_tile = [&](int s, const KeyItem& t) {
     mbar_arrive_expect_tx(bar(C::kBarStFull + s), 2 * C::kTileBytes);
     tma_load_3d(sbase + C::kQOff + s * C::kTileBytes, &p.tm_q, bar(C::kBarStFull + s), 0, t.i * kBlockM, t.head);
     tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes, &p.tm_do, bar(C::kBarStFull + s), 0, t.i * kBlockM, t.head);
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     mbar_init(bar(C::kBarKVFree), 2);
     fence_mbar_init();
     grid_dependency_wait();
-    WinItem t;
+    KeyItem t;
     int blk = blockIdx.x;
     if (next_item(p, blk, stride, total, t)) {
       load_kv(0, t);
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         return ok = __all_sync(0xffffffffu, ok);
       };
       int blk = blockIdx.x;
-      WinItem t;
+      KeyItem t;
       for (bool more = next_item(p, blk, stride, total, t); ok && more;) {
         for (int it = 0; it < t.n_iter; ++it) {
           const int s = n % C::kStages;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
       // ----------------------------------------------------------- K and V
       bool ok = true;
       int blk = blockIdx.x;
-      WinItem t;
+      KeyItem t;
       bool more = next_item(p, blk, stride, total, t);  // (its copies are on their way)
       int m = 1;
       while (more) {
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
       // Step n issues tile n's dV, dK and dQ and tile n + 1's S^T and dP^T; step -1,
       // the first item's first S^T and dP^T alone.
       int m = 0, blk = blockIdx.x;
-      WinItem t;
+      KeyItem t;
       bool more = next_item(p, blk, stride, total, t);
       int left = 0, next_left = more ? t.n_iter : 0;  // tiles of the item from this step's on; of the next item
       bool first = false;                             // this step's tile is its item's first
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     int n = 0, buf = 0;
     bool ok = true;
     int blk = blockIdx.x;
-    WinItem t;
+    KeyItem t;
     for (; ok && next_item(p, blk, stride, total, t); blk += stride) {
       for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
         ok = mbar_wait_short(bar(C::kBarDQFull), n & 1, ctl, kSiteDQFull);
@@ -494,10 +494,10 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     };
     int n = 0, m = 0;
     bool ok = true;
-    WinItem t_next;
-    if (static_cast<int>(blockIdx.x) < total) t_next = win_item(p, blockIdx.x);
+    KeyItem t_next;
+    if (static_cast<int>(blockIdx.x) < total) t_next = key_item(p, blockIdx.x);
     for (int blk = blockIdx.x; ok && blk < total; blk += stride) {
-      WinItem t = t_next;
+      KeyItem t = t_next;
       const bool row_valid = t.k0 + kr < p.N;
       const bool last_tile = t.k0 + kBlockN > p.N;  // some key rows are past N
       for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(bar(C::kBarDSFull));
       }
-      if (blk + stride < total) t_next = win_item(p, blk + stride);
+      if (blk + stride < total) t_next = key_item(p, blk + stride);
 
       // The item's dV (warpgroup 0) and dK (warpgroup 1, times the softmax scale,
       // which dS left out): a thread holds its key row.

@@ -36,7 +36,8 @@
 // the codes issues 64% of the slots and bounds it beside HBM (units of 32
 // positions: 175 us).  48 sequences, 3 new tokens, a window of 4096: 46 us, 2.5
 // TB/s, of which about 16 are the launches, the tables, the first copies and the
-// join; 12 pairs are two tiles, 249 registers, 8 warps to an SM.  bf16, one
+// join; 12 pairs are two tiles, 253 registers, 8 warps to an SM.  bf16, 32 such
+// sequences, L2 flushed: 389 us, 6.2 TB/s (d = 64: 209, 5.8); one
 // sequence of 4097 positions: 15 us on the GPU, the same fixed cost.
 // kTiles: one where no block has more than 8 pairs (two there: 194 instead of
 // 142 us), else two (one, which reads the rows twice: 60 instead of 46).
@@ -96,11 +97,6 @@ struct Seq {
   int lo;           // the first position that the window of its rows reaches
 };
 
-// The first position that the window of a sequence's rows reaches.
-__device__ __forceinline__ int seq_first(const FwdPagedParams& p, const Seq& s) {
-  return p.window == INT_MAX ? 0 : max(0, max(0, s.len - s.n) - p.window + 1);
-}
-
 template <class C>
 __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool report) {
   Seq s;
@@ -118,7 +114,7 @@ __device__ __forceinline__ Seq paged_seq(const FwdPagedParams& p, int b, bool re
   }
   s.len = max(0, s.len - extra);
   const int end = (s.len + C::kUnit - 1) / C::kUnit;
-  s.lo = seq_first(p, s);
+  s.lo = p.window == INT_MAX ? 0 : max(0, max(0, s.len - s.n) - p.window + 1);
   const int win = s.lo / C::kUnit;
   s.first = min((min(p.sinks, s.len) + C::kUnit - 1) / C::kUnit, win);
   s.skip = win - s.first;
@@ -166,12 +162,6 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-// An 8x8 block of 16-bit values (lane (g, c): row g, columns 2c, 2c + 1) transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
 
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -188,14 +178,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Untiled bulk copy global -> shared, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
 }
 
 // This warp's copies: the units of its piece in order, each into the next stage.

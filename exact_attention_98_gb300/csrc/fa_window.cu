@@ -49,13 +49,6 @@ __device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(b0));
 }
 
-// An 8x8 block of 16-bit values (lane (g, c): row g, columns 2c, 2c + 1) transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -74,14 +67,6 @@ struct PreCfg {
   static constexpr int kSmemBytes = kAbortOff + 16;
   static_assert(kWarps * kKeys * D * 4 <= kRingBytes, "the warps' sums go over the ring");
 };
-
-// Untiled bulk copy global -> shared, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
 
 // grid slots * BHkv.  A warp takes 16 rows of one query head at a time; lane
 // (g, c) their rows g and g + 8, and of each the elements [c D/4, (c+1) D/4).
