@@ -18,7 +18,7 @@
 // blocks to an SM keep enough loads in flight.  Measured (K, V and Q, d = 128):
 // bf16, 13102 tokens of 4 key and 16 query heads: 31.3 us, 5.2 TB/s of 6.7; 4 bits,
 // 14631 tokens of 8 and 32 heads, with the rows read back: 96.5 us, 4.1 TB/s.  The
-// 4-bit append alone (77 us under a profiler) waits for its loads first (5.6
+// 4-bit append alone (75 us under a profiler) waits for its loads first (5.4
 // cycles per instruction), at 57% of its issue slots, which the divisions by the
 // scale, each correctly rounded, and the packing take; four blocks to an SM leave
 // it 64 registers, of which 20 spill.  Not kept: 2 or 8 tokens a
