@@ -35,6 +35,8 @@
  *     kernel in `stream` finishes (programmatic dependent launch); it waits
  *     for that work before touching any buffer.
  *   - Input and output buffers must not overlap.
+ *   - Calls that may run at the same time (on several streams, or replayed by
+ *     several graphs) need workspaces of their own.
  */
 #ifndef FA_H_
 #define FA_H_
