@@ -11,6 +11,7 @@
 #include "fa_device.cuh"
 #include "fa_bwd_dq.h"
 #include "fa_kernels.h"
+#include "fa_packed.cuh"
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -119,6 +120,22 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int N, int BH, int d,
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
             elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of packed sequences (fa_rows), bf16, viewed as (d, rows, heads): box as
+// encode_tile_map.  A single row's or head's stride does not matter.
+bool encode_rows_map(CUtensorMap* map, const fa_rows& t, int rows, int heads, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rows > 1 ? t.row : d) * 2,
+                                 static_cast<cuuint64_t>(heads > 1 ? t.head : d) * 2};
+  const cuuint32_t box[3] = {64, kBlockM, 1};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.data, dims, strides, box, elem_strides,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -857,6 +874,156 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   if (timing_record(1, false, s) != cudaSuccess) return FA_ERR_CUDA;
   if (launch_window_post(wp, d, s) != cudaSuccess) return FA_ERR_CUDA;
   return FA_OK;
+}
+
+namespace {
+
+// A row tensor of packed sequences: alignment, and rows of d elements that do not
+// overlap.
+bool rows_ok(const fa_rows* t, int rows, int heads, int d) {
+  if (!t || !t->data || !aligned16(t->data)) return false;
+  const long long row = rows > 1 ? t->row : 0, head = heads > 1 ? t->head : 0;
+  // (TMA strides are below 2^40 bytes)
+  if (row < 0 || head < 0 || row % 8 != 0 || head % 8 != 0 || row >= 1LL << 38 || head >= 1LL << 38) return false;
+  if ((rows > 1 && row < d) || (heads > 1 && head < d)) return false;
+  if (rows <= 1 || heads <= 1) return true;
+  return row <= head ? (head - d) / row >= rows - 1 : (row - d) / head >= heads - 1;
+}
+
+// As passed to kernels, which multiply strides that may not matter by 0.
+long long row_stride(const fa_rows& t, int rows) { return rows > 1 ? t.row : 0; }
+long long head_stride(const fa_rows& t, int heads) { return heads > 1 ? t.head : 0; }
+
+constexpr int kMaxPacked = 1 << 30;  // rows and sequences
+
+// Checks shared by the calls on packed rows.  Returns FA_OK or the error; *empty:
+// nothing to do.
+int check_packed(const void* plan, int sequences, int rows, int H, int Hkv, int d, float scale, bool* empty) {
+  *empty = false;
+  if (sequences < 0 || rows < 0 || H < 0 || Hkv < 0) return FA_ERR_INVALID_ARG;
+  if (!(isfinite(scale) && scale > 0.0f)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (sequences > kMaxPacked || rows > kMaxPacked) return FA_ERR_UNSUPPORTED;
+  if (sequences == 0 || rows == 0 || H == 0) {
+    *empty = true;
+    return FA_OK;
+  }
+  if (Hkv == 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (!plan || (reinterpret_cast<uintptr_t>(plan) & (kWsAlign - 1)) != 0) return FA_ERR_INVALID_ARG;
+  // work items, and a group's tiles of a sequence, are ints
+  if (packed_tiles(rows, sequences, kBlockM) * H > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+}  // namespace
+
+size_t fa_packed_plan_bytes(int sequences, int rows) {
+  if (sequences < 0 || rows <= 0 || sequences > kMaxPacked || rows > kMaxPacked) return 0;
+  return packed_layout(rows, sequences).bytes;
+}
+
+int fa_packed_plan(const int* cu_seqlens, int sequences, int rows, int causal, void* plan, size_t plan_bytes,
+                   void* stream) {
+  if (sequences < 0 || rows < 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
+  if (sequences > kMaxPacked || rows > kMaxPacked) return FA_ERR_UNSUPPORTED;
+  if (rows == 0) return FA_OK;
+  if (!cu_seqlens || !aligned4(cu_seqlens)) return FA_ERR_INVALID_ARG;
+  if (!plan || plan_bytes < fa_packed_plan_bytes(sequences, rows) ||
+      (reinterpret_cast<uintptr_t>(plan) & (kWsAlign - 1)) != 0)
+    return FA_ERR_WORKSPACE;
+  PackedPlanParams p = {};
+  p.cu = cu_seqlens;
+  p.sequences = sequences;
+  p.rows = rows;
+  p.causal = causal;
+  p.plan = plan;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return launch_packed_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k, const fa_rows* v,
+                  const fa_rows* o, float* lse, int H, int Hkv, int d, float scale, void* stream) {
+  bool empty = false;
+  const int rc = check_packed(plan, sequences, rows, H, Hkv, d, scale, &empty);
+  if (rc != FA_OK || empty) return rc;
+  if (!rows_ok(q, rows, H, d) || !rows_ok(k, rows, Hkv, d) || !rows_ok(v, rows, Hkv, d) || !rows_ok(o, rows, H, d) ||
+      !lse || !aligned4(lse))
+    return FA_ERR_INVALID_ARG;
+  FwdParams p = {};
+  if (!encode_rows_map(&p.tm_q, *q, rows, H, d) || !encode_rows_map(&p.tm_k, *k, rows, Hkv, d) ||
+      !encode_rows_map(&p.tm_v, *v, rows, Hkv, d) || !encode_rows_map(&p.tm_o, *o, rows, H, d))
+    return FA_ERR_CUDA;
+  p.o = o->data;
+  p.o_row = row_stride(*o, rows);
+  p.o_head = head_stride(*o, H);
+  p.lse = lse;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  p.N = rows;
+  p.H = H;
+  p.plan = plan;
+  p.sequences = sequences;
+  p.c = scale * 1.4426950408889634f;
+  p.ln2 = 0.6931471805599453f;
+  p.num_splits = 1;
+  const int group = H / Hkv;
+  p.win_tiles = group % 2 == 0 ? 1 : 2;
+  const int units = p.win_tiles == 1 ? H / 2 : H;
+  // an upper bound: the kernel reads how many there are (its grid is no larger than this)
+  p.n_items = static_cast<int>(packed_tiles(rows, sequences, p.win_tiles * kBlockM) * units);
+  p.div_bh = FastDiv(static_cast<uint32_t>(units));
+  p.div_group = FastDiv(static_cast<uint32_t>(group));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = timing_record(0, true, s);
+  if (err == cudaSuccess) err = launch_fwd(p, d, s);
+  if (err == cudaSuccess) err = timing_record(0, false, s);
+  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_rotate(const fa_rows* q, const fa_rows* q_out, int H, const fa_rows* k, const fa_rows* k_out, int Hkv,
+              const int* positions, int rows, int d, const float* rope, int rope_len, int rot, int interleaved,
+              int backward, void* stream) {
+  if (rows < 0 || H < 0 || Hkv < 0 || rope_len < 0) return FA_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (backward != 0 && backward != 1)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rot < 16 || rot > d || rot % 16 != 0) return FA_ERR_INVALID_ARG;
+  if (rows == 0 || (H == 0 && Hkv == 0)) return FA_OK;
+  if (rows > kMaxPacked || static_cast<long long>(H) + Hkv > (1 << 28) ||
+      (static_cast<long long>(H) + Hkv) * rows > 0x7fffffffLL)
+    return FA_ERR_UNSUPPORTED;
+  if (!positions || !aligned4(positions) || !rope || !aligned16(rope)) return FA_ERR_INVALID_ARG;
+  if (H > 0 && (!rows_ok(q, rows, H, d) || !rows_ok(q_out, rows, H, d))) return FA_ERR_INVALID_ARG;
+  if (Hkv > 0 && (!rows_ok(k, rows, Hkv, d) || !rows_ok(k_out, rows, Hkv, d))) return FA_ERR_INVALID_ARG;
+  RotateParams p = {};
+  if (H > 0) {
+    p.q = static_cast<const __nv_bfloat16*>(q->data);
+    p.q_out = static_cast<__nv_bfloat16*>(q_out->data);
+    p.q_row = row_stride(*q, rows);
+    p.q_head = head_stride(*q, H);
+    p.qo_row = row_stride(*q_out, rows);
+    p.qo_head = head_stride(*q_out, H);
+  }
+  if (Hkv > 0) {
+    p.k = static_cast<const __nv_bfloat16*>(k->data);
+    p.k_out = static_cast<__nv_bfloat16*>(k_out->data);
+    p.k_row = row_stride(*k, rows);
+    p.k_head = head_stride(*k, Hkv);
+    p.ko_row = row_stride(*k_out, rows);
+    p.ko_head = head_stride(*k_out, Hkv);
+  }
+  p.H = H;
+  p.Hkv = Hkv;
+  p.positions = positions;
+  p.rows = rows;
+  p.rope = rope;
+  p.rope_len = rope_len;
+  p.rot = rot;
+  p.interleaved = interleaved;
+  p.backward = backward;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return launch_rotate(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_paged_block_bytes(int format, int page_size, int d) {

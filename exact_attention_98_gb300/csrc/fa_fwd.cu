@@ -48,6 +48,7 @@
 // it may read and rescale O_t.
 #include "fa_device.cuh"
 #include "fa_kernels.h"
+#include "fa_packed.cuh"
 
 namespace fa {
 namespace {
@@ -59,7 +60,9 @@ namespace {
 // tcgen05 MMA (cta_group::2): each CTA keeps its own two query tiles, S, P and
 // O, and loads half of every K tile (64 of its keys) and half of every V tile
 // (64 of its d columns); bf16, d = 128 only.
-template <int D, bool FP8 = false, bool PAIR = false>
+// PACKED: packed sequences (PackItem); warp 10 clears the rows of V that a
+// sequence's last key tile holds past its end.
+template <int D, bool FP8 = false, bool PAIR = false, bool PACKED = false>
 struct FwdCfg {
   static_assert(D == 64 || D == 128, "head dim");
   static_assert(!FP8 || D == 128, "FP8 forward: d = 128");
@@ -72,6 +75,7 @@ struct FwdCfg {
                 "register split exceeds the launch allocation");
   static constexpr int kProducerWarp = 8;
   static constexpr int kMmaWarp = 9;
+  static constexpr int kTrimWarp = 10;  // PACKED
   static constexpr int kTileBytes = kBlockM * D * (FP8 ? 1 : 2);  // one Q, K or V tile
   static constexpr int kHalfBytes = kBlockM * 64 * 2;  // one 64-column bf16 swizzle block
   static_assert(FP8 || kTileBytes == (D / 64) * kHalfBytes, "bf16 tile = its swizzle blocks");
@@ -91,7 +95,8 @@ struct FwdCfg {
   static constexpr int kStageOff = kRingOff + kSlots * kSlotBytes + kRingPad;
   static constexpr int kBarOff = kStageOff + (kStageO ? 2 * kStageBytes : 0);
   // barriers: q_full, q_empty, full[kSlots], empty[kSlots], s_full[2],
-  // p_full[2], o_full[2], mma_done
+  // p_full[2], o_full[2], mma_done; PACKED: trim[kSlots], a V tile that warp 10
+  // has to clear rows of has landed
   static constexpr int kBarQFull = 0;
   static constexpr int kBarQEmpty = 1;
   static constexpr int kBarFull = 2;
@@ -100,7 +105,8 @@ struct FwdCfg {
   static constexpr int kBarPFull = kBarSFull + 2;
   static constexpr int kBarOFull = kBarPFull + 2;
   static constexpr int kBarMmaDone = kBarOFull + 2;
-  static constexpr int kNumBars = kBarMmaDone + 1;
+  static constexpr int kBarTrim = kBarMmaDone + 1;
+  static constexpr int kNumBars = kBarTrim + (PACKED ? kSlots : 0);
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kAbortOff = kTmemSlotOff + 4;
   static constexpr int kSmemUsed = kAbortOff + 4;
@@ -121,6 +127,7 @@ enum : unsigned int {
   kSiteSFull = 0x106,
   kSiteOFull = 0x107,
   kSiteQEmpty = 0x108,
+  kSiteTrim = 0x109,
 };
 
 // Blocks: two 128-row query tiles of one (batch, head) (four for a CTA
@@ -153,7 +160,7 @@ struct FwdItem {
   __device__ __forceinline__ int q_head(int) const { return bh; }
   __device__ __forceinline__ int q_row(int t) const { return q0 + t * kBlockM; }
   __device__ __forceinline__ int kv_head() const { return bh; }
-  __device__ __forceinline__ int key_tile(int j) const { return kb + j; }
+  __device__ __forceinline__ int key_row(int j) const { return (kb + j) * kBlockN; }
 };
 
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int w, int n_ktiles) {
@@ -221,7 +228,7 @@ struct WinItem {
   __device__ __forceinline__ int q_head(int t) const { return t ? head1 : head0; }
   __device__ __forceinline__ int q_row(int t) const { return t ? row1 : row0; }
   __device__ __forceinline__ int kv_head() const { return kv; }
-  __device__ __forceinline__ int key_tile(int j) const { return j < first ? j : j + skip; }
+  __device__ __forceinline__ int key_row(int j) const { return (j < first ? j : j + skip) * kBlockN; }
 };
 
 __device__ __forceinline__ WinItem win_item(const FwdParams& p, int w) {
@@ -248,6 +255,64 @@ __device__ __forceinline__ WinItem win_item(const FwdParams& p, int w) {
   return it;
 }
 
+// Packed work item: two 128-row query tiles of one sequence that walk its key
+// tiles, all or up to the diagonal.  As for windows they are one query tile of two
+// heads of a group where the group is even, otherwise two neighbouring tiles of one head.
+struct PackItem {
+  int head0, head1;  // query heads of the two tiles
+  int row0, row1;    // their first rows within the sequence
+  int kv;            // key head
+  int start, len;    // the sequence's rows
+  int nkv0, nkv1;    // key tiles that each query tile sees (0: no such tile)
+  int nmax;
+  static constexpr int part = -1;
+  __device__ __forceinline__ int nkv(int t) const { return t ? nkv1 : nkv0; }
+  __device__ __forceinline__ int q_head(int t) const { return t ? head1 : head0; }
+  __device__ __forceinline__ int row(int t) const { return t ? row1 : row0; }
+  __device__ __forceinline__ int q_row(int t) const { return start + row(t); }
+  __device__ __forceinline__ int kv_head() const { return kv; }
+  __device__ __forceinline__ int key_row(int j) const { return start + j * kBlockN; }
+  // key tile j reaches past the sequence's end
+  __device__ __forceinline__ bool ragged(int j) const { return (j + 1) * kBlockN > len; }
+};
+
+__device__ __forceinline__ PackItem pack_item(const FwdParams& p, int w) {
+  const PackedLayout l = packed_layout(p.N, p.sequences);
+  const uint8_t* plan = static_cast<const uint8_t*>(p.plan);
+  const bool causal = reinterpret_cast<const PackedHead*>(plan)->causal != 0;
+  const int entry = p.div_bh.div(w), unit = w - entry * static_cast<int>(p.div_bh.d);
+  const int4 e = reinterpret_cast<const int4*>(plan + (p.win_tiles == 1 ? l.tiles : l.blocks))[entry];
+  PackItem it;
+  it.start = e.x;
+  it.len = e.y;
+  it.row0 = e.z * p.win_tiles * kBlockM;
+  if (p.win_tiles == 1) {
+    it.head0 = 2 * unit;
+    it.head1 = 2 * unit + 1;
+    it.row1 = it.row0;
+  } else {
+    it.head0 = it.head1 = unit;
+    it.row1 = it.row0 + kBlockM;
+  }
+  it.kv = p.div_group.div(it.head0);
+  const int tiles = (it.len + kBlockN - 1) / kBlockN;
+  it.nkv0 = causal ? it.row0 / kBlockN + 1 : tiles;
+  it.nkv1 = it.row1 >= it.len ? 0 : causal ? it.row1 / kBlockN + 1 : tiles;
+  it.nmax = max(it.nkv0, it.nkv1);
+  return it;
+}
+
+// Work items of a packed call: 0 when the plan is not one for its rows
+// (recorded).
+__device__ __forceinline__ int pack_items(const FwdParams& p) {
+  const PackedHead& h = *static_cast<const PackedHead*>(p.plan);
+  if (!packed_fits(h, p.N, p.sequences)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kPackedInvalid, kSitePackedPlan);
+    return 0;
+  }
+  return (p.win_tiles == 1 ? h.n_tiles : h.n_blocks) * static_cast<int>(p.div_bh.d);
+}
+
 // The r-th item of this CTA (of this pair): persistent CTAs (pairs) walk the
 // item list in rounds of G = gridDim.x (pairs: gridDim.x / 2), alternating
 // direction (0..G-1, then G-1..0), so that with the heaviest items first
@@ -263,10 +328,11 @@ __device__ __forceinline__ int fwd_item_index(int r) {
 // at positions 0 .. POLY-1 are evaluated by the polynomial on the FMA pipe
 // (exp2_poly2 for a pair, exp2_poly for a lone one), the rest by MUFU ex2.
 // WINDOW: sliding window with first tokens and shared key heads (win_item).
-template <int D, int POLY, bool FP8, bool PAIR = false, bool WINDOW = false>
-__global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
+// PACKED: packed sequences and shared key heads (pack_item).
+template <int D, int POLY, bool FP8, bool PAIR = false, bool WINDOW = false, bool PACKED = false>
+__global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
-  using C = FwdCfg<D, FP8, PAIR>;
+  using C = FwdCfg<D, FP8, PAIR, PACKED>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
@@ -284,6 +350,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
   auto item_of = [&](int wi) {
     if constexpr (PAIR) return pair_item(p, wi, n_ktiles);
     else if constexpr (WINDOW) return win_item(p, wi);
+    else if constexpr (PACKED) return pack_item(p, wi);
     else return fwd_item(p, wi, n_ktiles);
   };
 
@@ -302,6 +369,8 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       mbar_init(bar(C::kBarOFull + t), 1);
     }
     mbar_init(bar(C::kBarMmaDone), 1);
+    if constexpr (PACKED)
+      for (int s = 0; s < C::kSlots; ++s) mbar_init(bar(C::kBarTrim + s), 1);
     fence_mbar_init();
   }
   if (warp == C::kMmaWarp) {
@@ -317,6 +386,9 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   // Q, K, V and the outputs may belong to the stream's earlier work
   grid_dependency_wait();
+  int n_packed = 0;
+  if constexpr (PACKED) n_packed = pack_items(p);
+  auto n_items = [&] { return PACKED ? n_packed : p.n_items; };
 
   if (warp >= 8) {
    regs_set<C::kOtherRegs, C::kLaunchRegs>();
@@ -338,7 +410,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       bool ok = true;
       for (int round = 0; ok; ++round) {
         const int wi = fwd_item_index<PAIR>(round);
-        if (wi >= p.n_items) break;
+        if (wi >= n_items()) break;
         const FwdItem item = pair_item(p, wi, n_ktiles);
         if (item.nmax == 0) continue;
         if (q_items > 0 && !(ok = mbar_wait(bar(C::kBarQEmpty), (q_items - 1) & 1, ctl, kSiteQEmpty)))
@@ -392,7 +464,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       bool ok = true;
       for (int round = 0; ok; ++round) {
         const int wi = fwd_item_index(round);
-        if (wi >= p.n_items) break;
+        if (wi >= n_items()) break;
         const auto item = item_of(wi);
         if (item.nmax == 0) continue;  // a key range past every row's keys
         if (q_items > 0 && !(ok = mbar_wait(bar(C::kBarQEmpty), (q_items - 1) & 1, ctl, kSiteQEmpty)))
@@ -417,17 +489,21 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
           const CUtensorMap* map = (idx & 1) ? &p.tm_v : &p.tm_k;
           const int j = idx >> 1;
           const uint32_t dst = sbase + C::kRingOff + slot * C::kTileBytes;
-          mbar_arrive_expect_tx(bar(C::kBarFull + slot), C::kTileBytes);
+          // packed: the last V tile goes by the trim warp where it is ragged
+          int full = C::kBarFull + slot;
+          if constexpr (PACKED)
+            if ((idx & 1) && item.ragged(j)) full = C::kBarTrim + slot;
+          mbar_arrive_expect_tx(bar(full), C::kTileBytes);
           if constexpr (FP8) {
             // K: [key][d] rows; V^T: [d][key] rows (keys along x)
             if (idx & 1)
-              tma_load_3d(dst, map, bar(C::kBarFull + slot), item.key_tile(j) * kBlockN, 0, item.kv_head());
+              tma_load_3d(dst, map, bar(C::kBarFull + slot), item.key_row(j), 0, item.kv_head());
             else
-              tma_load_3d(dst, map, bar(C::kBarFull + slot), 0, item.key_tile(j) * kBlockN, item.kv_head());
+              tma_load_3d(dst, map, bar(C::kBarFull + slot), 0, item.key_row(j), item.kv_head());
           } else {
             for (int h = 0; h < D / 64; ++h)
-              tma_load_3d(dst + h * C::kHalfBytes, map, bar(C::kBarFull + slot), h * 64,
-                          item.key_tile(j) * kBlockN, item.kv_head());
+              tma_load_3d(dst + h * C::kHalfBytes, map, bar(full), h * 64,
+                          item.key_row(j), item.kv_head());
           }
           issued = gidx + 1;
         }
@@ -437,6 +513,33 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       if (items_loaded > 0) mbar_wait_drain(bar(C::kBarQFull), (items_loaded - 1) & 1);
       for (int idx = max(0, issued - C::kSlots); idx < issued; ++idx)
         mbar_wait_drain(bar(C::kBarFull + idx % C::kSlots), (idx / C::kSlots) & 1);
+    }
+  } else if (PACKED && warp == C::kTrimWarp) {
+    // ---------------------------------------------------------------- trim
+    // Rows of V past the sequence's end are another's, or padding, whatever they
+    // hold; their weights are 0, and so have they to be.
+    if constexpr (PACKED) {
+      int base = 0;
+      uint32_t parity = 0;  // of each slot's trim barrier
+      for (int round = 0;; ++round) {
+        const int wi = fwd_item_index(round);
+        if (wi >= n_items()) break;
+        const PackItem item = pack_item(p, wi);
+        if (item.ragged(item.nmax - 1)) {
+          const int slot = (base + 2 * item.nmax - 1) % C::kSlots;
+          if (!mbar_wait_warp(bar(C::kBarTrim + slot), (parity >> slot) & 1u, ctl, kSiteTrim)) break;
+          parity ^= 1u << slot;
+          const int row0 = item.len - (item.nmax - 1) * kBlockN;
+          for (int h = 0; h < D / 64; ++h)
+            for (int i = row0 * 8 + lane; i < kBlockN * 8; i += 32)
+              *reinterpret_cast<uint4*>(smem + C::kRingOff + slot * C::kTileBytes + h * C::kHalfBytes + i * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarFull + slot));
+        }
+        base += 2 * item.nmax;
+      }
     }
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------- MMA issue
@@ -546,7 +649,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       int np0 = 0, np1 = 0;
       for (int round = 0; ok; ++round) {
         const int wi = fwd_item_index<PAIR>(round);
-        if (wi >= p.n_items) break;
+        if (wi >= n_items()) break;
         const auto item = item_of(wi);
         if (item.nmax == 0) continue;
         ok = wait(bar(C::kBarQFull), (q_items++) & 1, kSiteQFull);
@@ -622,7 +725,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
     bool ok = true;
     for (int round = 0; ok; ++round) {
       const int wi = fwd_item_index<PAIR>(round);
-      if (wi >= p.n_items) break;
+      if (wi >= n_items()) break;
       // Key tiles of this warpgroup's query tile in the item's range, the
       // range's first key tile, the index of this warpgroup's query tile
       // (its diagonal key tile) and the item's head, first row and partial
@@ -638,14 +741,19 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
         iv[1] = itm.first;
         iv[2] = itm.skip;
         iv[3] = itm.q_row(t) / kBlockN;
+      } else if constexpr (PACKED) {
+        // columns that a row keeps of the last tile, less those its own place adds
+        const bool causal = static_cast<const PackedHead*>(p.plan)->causal != 0;
+        iv[0] = itm.nkv(t);
+        iv[1] = causal ? row + 1 : itm.len - (itm.nkv(t) - 1) * kBlockN;
       } else {
         iv[0] = itm.nkv0;
         iv[1] = itm.nkv1;
         iv[2] = itm.kb;
         iv[3] = (itm.q0 + tile_row0) / kBlockN;
       }
-      if (iv[WINDOW ? 0 : t] == 0) {
-        if constexpr (WINDOW) continue;
+      if (iv[WINDOW || PACKED ? 0 : t] == 0) {
+        if constexpr (WINDOW || PACKED) continue;
         // Split mode: an empty key range still leaves its partial result
         // for the merge (weight exp(-inf) = 0).
         else {
@@ -671,14 +779,16 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
       // row sum of exp2(x - m_used): four f32x2 accumulators (eight partial sums)
       f32x2 l2[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f),
                      f2_pack(0.0f, 0.0f)};
-      for (int j = 0, nk = iv[WINDOW ? 0 : t]; j < nk; ++j) {
+      for (int j = 0, nk = iv[WINDOW || PACKED ? 0 : t]; j < nk; ++j) {
         // The key tile and whether it needs a mask, from the small local array
         // before the wait for S, so that the loads' latency hides in it.
-        const int jabs = WINDOW ? (j < iv[1] ? j : j + iv[2]) : iv[2] + j;  // key tile index
+        const int jabs = WINDOW ? (j < iv[1] ? j : j + iv[2]) : PACKED ? j : iv[2] + j;  // key tile index
         // causal: the diagonal tile (pair mode: and the tile after it, which
         // the earlier CTA of the pair masks whole)
         // window: also the tiles that the window of the tile's last row leaves
+        // packed: the diagonal tile or the one with the sequence's end, the last
         const bool edge = WINDOW ? jabs >= iv[3] || jabs * kBlockN < (iv[3] + 1) * kBlockM - p.window
+                          : PACKED ? j == nk - 1
                                  : (p.causal && (PAIR ? jabs >= iv[3] : jabs == iv[3])) ||
                                        (ragged && jabs == n_ktiles - 1);
         ok = mbar_wait(bar(C::kBarSFull + t), phase & 1u, ctl, kSiteSFull);
@@ -714,9 +824,14 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
         } else if (edge) {
           // the row keeps its first `lim` columns: keys below N and, causal,
           // not after the query
-          const int kbase = jabs * kBlockN;
-          int lim = p.N - kbase;
-          if (p.causal) lim = min(lim, iv[3] * kBlockN + row - kbase + 1);
+          int lim;
+          if constexpr (PACKED) {
+            lim = iv[1];
+          } else {
+            const int kbase = jabs * kBlockN;
+            lim = p.N - kbase;
+            if (p.causal) lim = min(lim, iv[3] * kBlockN + row - kbase + 1);
+          }
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
@@ -861,7 +976,20 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
           const int qrow0 = PAIR ? item.q_row(0) + tile_row0 : item.q_row(t);
           const int qpos = qrow0 + row;
           const int part = item.part;
-          const bool in_range = qpos < p.N;
+          bool in_range = qpos < p.N;
+          bool staged = C::kStageO && part < 0;
+          size_t lse_at = static_cast<size_t>(bh) * p.N + qpos;
+          __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + lse_at * D;
+          bool o32 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+          if constexpr (PACKED) {
+            // the rows behind a sequence's end are not its own: a bulk store for
+            // whole tiles only
+            in_range = item.row(t) + row < item.len;
+            staged = item.row(t) + kBlockM <= item.len;
+            lse_at = static_cast<size_t>(qpos) * p.H + bh;
+            orow = static_cast<__nv_bfloat16*>(p.o) + qpos * p.o_row + bh * p.o_head;
+            o32 = o32 && p.o_row % 16 == 0 && p.o_head % 16 == 0;
+          }
           float inv_l = 1.0f / l;
           float lse_row = m_used * p.ln2 + logf(l);
           if constexpr (FP8) {  // P carried a factor 64, V the head's scale
@@ -869,7 +997,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
             inv_l *= va > 0.0f ? va * (1.0f / 448.0f) : 1.0f;
             lse_row -= 6.0f * p.ln2;
           }
-          if (C::kStageO && part < 0) {
+          if (staged) {
             // The whole O row in one batch of loads, normalised and packed;
             // then per 64 columns: staged in this warpgroup's buffer (a 128B-
             // swizzle box: row r at r * 128 bytes, 16-byte chunk c at
@@ -908,14 +1036,11 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
                 bulk_commit();
               }
             }
-            if (in_range) p.lse[static_cast<size_t>(bh) * p.N + qpos] = lse_row;
+            if (in_range) p.lse[lse_at] = lse_row;
           } else if (part < 0) {
-            __nv_bfloat16* orow =
-                static_cast<__nv_bfloat16*>(p.o) + (static_cast<size_t>(bh) * p.N + qpos) * D;
             // The whole O row in one batch of loads (pair mode: 32 columns at
             // a time, registers are short there), then 32-byte stores where O
             // allows them (a row is 2d bytes, so every row keeps O's alignment).
-            const bool o32 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
             constexpr int kBatch = PAIR ? 1 : D / 32;
             uint32_t r[kBatch][32];
 #pragma unroll(PAIR ? 1 : D / 32)
@@ -945,7 +1070,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
                 }
               }
             }
-            if (in_range) p.lse[static_cast<size_t>(bh) * p.N + qpos] = lse_row;
+            if (in_range) p.lse[lse_at] = lse_row;
           } else {
             // Split mode: this key range's O (normalised over the range) and
             // LSE in fp32, for the merge.
@@ -990,10 +1115,10 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR>::kThreads, 1)
   }
 }
 
-template <int D, int POLY, bool FP8 = false, bool WINDOW = false>
+template <int D, int POLY, bool FP8 = false, bool WINDOW = false, bool PACKED = false>
 cudaError_t launch_fwd_dp(const FwdParams& p, cudaStream_t stream) {
-  using C = FwdCfg<D, FP8>;
-  constexpr auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW>;
+  using C = FwdCfg<D, FP8, false, PACKED>;
+  constexpr auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW, PACKED>;
   cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM (the kernel holds all of tensor memory),
@@ -1059,6 +1184,10 @@ cudaError_t launch_fwd_d(const FwdParams& p, cudaStream_t stream) {
 
 cudaError_t launch_fwd(const FwdParams& p, int d, cudaStream_t stream) {
   if (p.pair) return (d == 128 && !p.fp8) ? launch_fwd_pair(p, stream) : cudaErrorInvalidValue;
+  if (p.plan)
+    return d == 128  ? launch_fwd_dp<128, 0, false, false, true>(p, stream)
+           : d == 64 ? launch_fwd_dp<64, 0, false, false, true>(p, stream)
+                     : cudaErrorInvalidValue;
   if (p.window > 0)
     return d == 128  ? launch_fwd_dp<128, 0, false, true>(p, stream)
            : d == 64 ? launch_fwd_dp<64, 0, false, true>(p, stream)

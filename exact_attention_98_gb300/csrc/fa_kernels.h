@@ -81,6 +81,15 @@ struct FwdParams {
   int sinks;
   int win_tiles;
   FastDiv div_group;
+  // Packed sequences (plan != null; bf16, no split): the rows of all sequences
+  // follow one another, N is their number, and tm_q, tm_k, tm_v and tm_o have one
+  // slice per head.  A work item is entry i / units of the plan's list: two
+  // query tiles of one head (win_tiles = 2: blocks), or one of two heads (tiles);
+  // div_bh's divisor is units.
+  const void* plan;
+  int sequences;
+  int H;                     // of lse [N, H]
+  long long o_row, o_head;   // strides of o in elements
 };
 
 // Default share of the forward's exponentials evaluated by the polynomial on
@@ -304,6 +313,38 @@ cudaError_t launch_bwd_dkdv(const BwdParams& p, int d, cudaStream_t stream);
 // kernels leave out of dS).
 cudaError_t launch_bwd_post(const float* dq_acc, void* dq, long long elems, float mul,
                             cudaStream_t stream);
+
+// A plan of packed sequences (fa_packed.cuh).
+struct PackedPlanParams {
+  const int* cu;  // [sequences + 1]
+  int sequences;
+  int rows;
+  int causal;
+  void* plan;
+  int buckets, list_blocks;  // set by the launcher
+  unsigned int* status;
+};
+cudaError_t launch_packed_plan(PackedPlanParams p, cudaStream_t stream);
+
+// Rotation of Q and K rows (fa_rotate.cu).
+struct RotateParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  long long q_row, q_head, k_row, k_head, qo_row, qo_head, ko_row, ko_head;  // strides in elements
+  int H, Hkv;
+  const int* positions;  // [rows]
+  int rows;
+  const float* rope;  // [rope_len, rot]: rot/2 cosines, then rot/2 sines
+  int rope_len;
+  int rot;
+  int interleaved;
+  int backward;  // -sin for sin
+  FastDiv div_chunks;  // set by the launcher
+  unsigned int* status;
+};
+cudaError_t launch_rotate(RotateParams p, int d, cudaStream_t stream);
 
 // The paged key/value cache as the kernels see it (fa_paged_cache in fa.h).
 struct PagedView {

@@ -51,6 +51,11 @@ class PagedCache(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
+class Rows(ctypes.Structure):
+    """fa_rows of include/fa.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -122,6 +127,15 @@ def _load() -> ctypes.CDLL:
     lib.fa_fwd_paged_workspace_bytes.restype = sz
     lib.fa_fwd_paged.argtypes = [cache, vp, ll, ll, vp, vp, vp, i, i, i, f, i, i, vp, sz, vp]
     lib.fa_fwd_paged.restype = i
+    rows = ctypes.POINTER(Rows)
+    lib.fa_packed_plan_bytes.argtypes = [i, i]
+    lib.fa_packed_plan_bytes.restype = sz
+    lib.fa_packed_plan.argtypes = [vp, i, i, i, vp, sz, vp]
+    lib.fa_packed_plan.restype = i
+    lib.fa_fwd_packed.argtypes = [vp, i, i, rows, rows, rows, rows, vp, i, i, i, f, vp]
+    lib.fa_fwd_packed.restype = i
+    lib.fa_rotate.argtypes = [rows, rows, i, rows, rows, i, vp, i, i, vp, i, i, i, i, vp]
+    lib.fa_rotate.restype = i
     lib.fa_launch_count.argtypes = []
     lib.fa_launch_count.restype = ctypes.c_ulonglong
     return lib
@@ -449,6 +463,28 @@ def fa_fwd_paged(cache: PagedCache, q, q_row, q_head, o, lse, cu_new, rows, max_
                             ws_bytes, _stream(stream)), "fa_fwd_paged")
 
 
+def fa_packed_plan_bytes(sequences: int, rows: int) -> int:
+    return int(lib.fa_packed_plan_bytes(sequences, rows))
+
+
+def fa_packed_plan(cu_seqlens, sequences, rows, causal, plan, stream=None) -> None:
+    ws_ptr, ws_bytes = _workspace(plan, cu_seqlens.device)
+    _check(lib.fa_packed_plan(_ptr(cu_seqlens), sequences, rows, int(bool(causal)), ws_ptr, ws_bytes,
+                              _stream(stream)), "fa_packed_plan")
+
+
+def fa_fwd_packed(plan, sequences, rows, q: Rows, k: Rows, v: Rows, o: Rows, lse, H, Hkv, d, scale,
+                  stream=None) -> None:
+    _check(lib.fa_fwd_packed(_ptr(plan), sequences, rows, q, k, v, o, _ptr(lse), H, Hkv, d, float(scale),
+                             _stream(stream)), "fa_fwd_packed")
+
+
+def fa_rotate(q: Rows, q_out: Rows, H, k: Rows, k_out: Rows, Hkv, positions, rows, d, rope, rope_len, rot,
+              interleaved, backward, stream=None) -> None:
+    _check(lib.fa_rotate(q, q_out, H, k, k_out, Hkv, _ptr(positions), rows, d, _ptr(rope), rope_len, rot,
+                         int(bool(interleaved)), int(bool(backward)), _stream(stream)), "fa_rotate")
+
+
 def fa_last_device_status(stream=None) -> int:
     return int(lib.fa_last_device_status(_stream(stream)))
 
@@ -679,3 +715,129 @@ def paged_forward(q, pages, page_table, seq_lens, cu_new, max_new: int = 1, wind
     fa_fwd_paged(cache, q, q_row, q_head, o, lse, cu_new, rows, max_new, H,
                  default_scale(d) if scale is None else scale, window, sinks, workspace, stream)
     return o, lse
+
+
+# --- packed sequences ----------------------------------------------------------------
+
+
+class PackedPlan:
+    """A plan of packed sequences (packed_plan): `plan`, its device memory;
+    `rows`, `sequences`, `causal`, which it was made with; `positions`, int32
+    [rows], each row's position in its sequence (-1: padding)."""
+
+    __slots__ = ("plan", "rows", "sequences", "causal", "positions")
+
+    def __init__(self, plan, rows: int, sequences: int, causal: bool):
+        self.plan, self.rows, self.sequences, self.causal = plan, rows, sequences, causal
+        self.positions = plan[_POSITIONS: _POSITIONS + 4 * rows].view(torch.int32)
+
+
+_POSITIONS = 256  # FA_PACKED_POSITIONS
+
+
+def _current_device(t, name):
+    """t's device, which has to be the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.device
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {dev}; the library launches on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def packed_plan(cu_seqlens, rows: int, causal: bool = True, out: PackedPlan | None = None,
+                stream=None) -> PackedPlan:
+    """Plan of a batch of packed sequences, for packed_forward and
+    packed_backward of all its layers: sequence b holds the rows cu_seqlens[b] ..
+    cu_seqlens[b+1]-1 (int32 [sequences + 1], on the device) of tensors of `rows` rows.
+    causal: a row sees its sequence's rows up to itself, otherwise all of them.
+    out: a plan of as many rows and sequences to make anew (in a captured graph,
+    say) and return."""
+    dev = _current_device(cu_seqlens, "cu_seqlens")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("expected cu_seqlens [sequences + 1]")
+    sequences, rows = cu_seqlens.numel() - 1, int(rows)
+    _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, (sequences + 1,), dev)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    if out is None:
+        n = max(fa_packed_plan_bytes(sequences, rows), _POSITIONS + 4 * rows)
+        plan, = _empty(stream, dev, (n, torch.uint8))
+    else:
+        if (out.rows, out.sequences) != (rows, sequences) or out.plan.device != dev:
+            raise ValueError(f"out is a plan of {out.rows} rows and {out.sequences} sequences on {out.plan.device}, "
+                             f"expected {rows} and {sequences} on {dev}")
+        plan = out.plan
+    fa_packed_plan(cu_seqlens, sequences, rows, causal, plan, stream)
+    if out is None:
+        return PackedPlan(plan, rows, sequences, bool(causal))
+    out.causal = bool(causal)
+    return out
+
+
+def _packed_rows(t, name, rows, heads, d, device) -> Rows:
+    """The row tensor t [rows, heads, d]."""
+    n, row, head = _rows(t, name, heads, d, device, rows)
+    return Rows(t.data_ptr(), row, head)
+
+
+def _packed_heads(q, k, plan):
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("expected q [rows, H, d]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("expected k [rows, Hkv, d]")
+    if not isinstance(plan, PackedPlan):
+        raise ValueError("plan must be a PackedPlan (packed_plan)")
+    if plan.plan.device != _current_device(q, "q"):
+        raise ValueError(f"plan is on {plan.plan.device}, expected {q.device}")
+    return plan.rows, q.shape[1], k.shape[1], q.shape[2]
+
+
+def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=None, stream=None):
+    """Attention within each packed sequence of `plan` (see packed_plan): q
+    [rows, H, d], k and v [rows, Hkv, d] (H a multiple of Hkv; row and head strides
+    that are multiples of 8) -> (o [rows, H, d], lse [rows, H]).  out: where o is
+    written, strides as q.  Padding rows of the results are not written."""
+    rows, H, Hkv, d = _packed_heads(q, k, plan)
+    dev = q.device
+    shapes = ((rows, H), torch.float32), ((rows, H, d), torch.bfloat16)
+    if out is None:
+        lse, out = _empty(stream, dev, *shapes)
+    else:
+        lse, = _empty(stream, dev, shapes[0])
+    fa_fwd_packed(plan.plan, plan.sequences, rows, _packed_rows(q, "q", rows, H, d, dev),
+                  _packed_rows(k, "k", rows, Hkv, d, dev), _packed_rows(v, "v", rows, Hkv, d, dev),
+                  _packed_rows(out, "out", rows, H, d, dev), lse, H, Hkv, d,
+                  default_scale(d) if scale is None else scale, stream)
+    return out, lse
+
+
+def rotate(q, k, positions, rope, interleaved: bool = False, backward: bool = False, out=None, stream=None):
+    """q [rows, H, d] and k [rows, Hkv, d] (either may be None) rotated by their rows'
+    positions, int32 [rows] (a plan's `positions`, or any), with the table `rope` [length, rot]
+    (see rope_table): (q', k').  backward: the transpose, which takes the gradients
+    of q' and k' to those of q and k.  out: (q', k') to write to; each may be q or k
+    itself.  Rows of negative position are not written."""
+    some = k if q is None else q
+    if not isinstance(some, torch.Tensor) or some.dim() != 3:
+        raise ValueError("expected q [rows, H, d] or k [rows, Hkv, d]")
+    dev = _current_device(some, "k" if q is None else "q")
+    rows, _, d = some.shape
+    _check_tensor(positions, "positions", torch.int32, (rows,), dev)
+    if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+        raise ValueError("rope must be [length, rot]")
+    rope_len, rot = rope.shape
+    _check_tensor(rope, "rope", torch.float32, (rope_len, rot), dev)
+    heads = [0 if x is None else x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 3 else None for x in (q, k)]
+    if out is None:
+        new = iter(_empty(stream, dev, *[((rows, h, d), torch.bfloat16) for x, h in zip((q, k), heads) if x is not None]))
+        out = tuple(None if x is None else next(new) for x in (q, k))
+    args = []
+    for x, y, h, name in zip((q, k), out, heads, "qk"):
+        if (x is None) != (y is None):
+            raise ValueError(f"{name} and its place in out must both be given")
+        args += [None, None, 0] if x is None or h == 0 else [
+            _packed_rows(x, name, rows, h, d, dev), _packed_rows(y, f"out ({name})", rows, h, d, dev), h]
+    fa_rotate(*args, positions, rows, d, rope, rope_len, rot, interleaved, backward, stream)
+    return out

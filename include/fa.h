@@ -316,6 +316,92 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
                   void* stream);
 
 /*
+ * Packed sequences: the rows of several sequences of different lengths, one after
+ * another in one tensor, without padding between them.  Sequence b holds the rows
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1; rows before the first and from the last
+ * one's end on are padding: they are not looked at, and outputs keep there what
+ * they held.
+ *
+ * A row tensor has `heads` rows of d bf16 values per token, at
+ * data + token * row + head * head (strides in elements, multiples of 8; data
+ * 16-byte aligned), so rows that a fused projection leaves, or views of a fused
+ * gradient, need no copy.  Rows of different tokens or heads do not overlap (no
+ * stride of 0; strides of a single token or head do not matter).
+ */
+typedef struct {
+  void* data;
+  long long row;  /* from a token to the next */
+  long long head; /* from a head to the next */
+} fa_rows;
+
+/*
+ * A plan of packed sequences: the tiles of all sequences, those of most work
+ * first, and each row's position in its sequence, in device memory that the
+ * caller owns.  It is made from cu_seqlens by one kernel, once for a batch, and read
+ * by every fa_fwd_packed and fa_bwd_packed on rows of this batch (any number of
+ * heads, any layer).  cu_seqlens is not needed afterwards.
+ *   cu_seqlens : in,  int [sequences + 1], read on the device: a captured graph
+ *                serves whatever it holds at each replay
+ *   rows       : rows of the tensors; 0 <= cu_seqlens[0] <= ... <=
+ *                cu_seqlens[sequences] <= rows.  The kernel checks this: offsets
+ *                that do not run forwards within the rows give a plan of no
+ *                sequence, and FA_ERR_INVALID_ARG is recorded in the device
+ *                status word.
+ *   causal     : 1 = a row sees its sequence's rows up to itself, 0 = all of
+ *                them, in every call with this plan
+ *   plan       : out, fa_packed_plan_bytes() bytes, 256-byte aligned.  The rows'
+ *                positions are at FA_PACKED_POSITIONS bytes into it: int [rows],
+ *                -1 for padding (fa_rotate's `positions`).
+ * At most 2^30 rows and 2^30 sequences (FA_ERR_UNSUPPORTED); empty sequences are
+ * allowed.
+ */
+#define FA_PACKED_POSITIONS 256
+size_t fa_packed_plan_bytes(int sequences, int rows);
+int fa_packed_plan(const int* cu_seqlens, int sequences, int rows, int causal, void* plan,
+                   size_t plan_bytes, void* stream);
+
+/*
+ * Attention within each of several packed sequences, key/value heads shared by groups of
+ * query heads (query head h reads key head h / (H / Hkv)):
+ *   O = softmax(scale q K^T) V over the rows that a row sees, LSE as fa_fwd.
+ *   plan            : of these rows (fa_packed_plan); a kernel that meets another one
+ *                     computes nothing and records FA_ERR_INVALID_ARG
+ *   sequences, rows : as the plan was made with
+ *   q, o            : in, out: row tensors of H heads; k, v: of Hkv heads, H a
+ *                     multiple of Hkv
+ *   lse             : out, fp32 [rows, H]
+ *   d               : 64 or 128
+ * K and V have to be finite in the rows of a sequence that hold a row's later keys
+ * (a masked pair's weight is an exact 0, and 0 times an infinity or a NaN is not);
+ * what other sequences and padding rows hold does not matter.
+ */
+int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k,
+                  const fa_rows* v, const fa_rows* o, float* lse, int H, int Hkv, int d, float scale,
+                  void* stream);
+
+/*
+ * Rotates Q and K rows by their positions (before fa_fwd_packed), or turns their
+ * gradients back (after fa_bwd_packed).
+ *   q, q_out  : in, out: row tensors of H heads, or both NULL (H = 0)
+ *   k, k_out  : the same of Hkv heads
+ *               An output may be its own input (the same data and strides), and may
+ *               not overlap it otherwise.
+ *   positions : in, int [rows]; a row of negative position is left as it was
+ *   rope      : in, fp32 [rope_len, rot]: row p holds cos of the rot/2 angles of
+ *               position p, then their sines (any pair of factors: a table for
+ *               long contexts may be scaled).  A position past the table:
+ *               the row is left as it was and FA_ERR_INVALID_ARG is recorded.
+ *   rot       : elements of a row that are rotated, a multiple of 16 from 16 to d; the
+ *               others are copied
+ *   interleaved, and the arithmetic: as fa_paged_append
+ *   backward  : 0 = rotate; 1 = the transpose, x_a = x'_a cos + x'_b sin, x_b =
+ *               x'_b cos - x'_a sin: the gradient of x from that of x'
+ */
+int fa_rotate(const fa_rows* q, const fa_rows* q_out, int H, const fa_rows* k, const fa_rows* k_out,
+              int Hkv, const int* positions, int rows, int d, const float* rope, int rope_len, int rot,
+              int interleaved, int backward, void* stream);
+
+/*
  * A paged key/value cache.  The cache is an array of num_pages * Hkv blocks;
  * block (page, head) holds page_size consecutive positions of one key head of
  * one sequence: their K rows, then their V rows.
@@ -436,8 +522,8 @@ int fa_fwd_paged(const fa_paged_cache* cache, const void* q, long long q_row, lo
 /*
  * Synchronises `stream`, then returns and clears the device status word:
  * FA_OK, or FA_ERR_TIMEOUT when a kernel gave up on a bounded wait since the
- * last call, or FA_ERR_INVALID_ARG when a kernel of the paged cache met tables
- * that it could not follow, or FA_ERR_CUDA when the synchronisation itself failed.
+ * last call, or FA_ERR_INVALID_ARG when a kernel of the paged cache or of packed
+ * sequences met tables that it could not follow, or FA_ERR_CUDA when the synchronisation itself failed.
  */
 int fa_last_device_status(void* stream);
 
@@ -489,7 +575,8 @@ int fa_timing_last_ms(int kernel, float* ms);
  * fa_bwd_deterministic three; fa_fwd_fp8 three (two preparation kernels and
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
  * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three;
- * fa_paged_append and fa_paged_read one;
+ * fa_paged_append and fa_paged_read one; fa_packed_plan, fa_fwd_packed and
+ * fa_rotate one;
  * fa_fwd_paged two (the forward, then the join of segments that several CTAs
  * shared).
  */
