@@ -981,6 +981,94 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+size_t fa_bwd_packed_workspace_bytes(int sequences, int rows, int H, int Hkv, int d) {
+  bool empty = false;
+  // (any aligned address stands for the plan)
+  if (check_packed(reinterpret_cast<const void*>(kWsAlign), sequences, rows, H, Hkv, d, 1.0f, &empty) != FA_OK || empty)
+    return 0;
+  const size_t n = static_cast<size_t>(rows) * H;
+  return n > 0x7fffffffu ? 0 : 2 * round_up(n * sizeof(float)) + round_up(n * d * sizeof(float));
+}
+
+int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k, const fa_rows* v,
+                  const fa_rows* o, const float* lse, const fa_rows* dout, const fa_rows* dq, const fa_rows* dk,
+                  const fa_rows* dv, int H, int Hkv, int d, float scale, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  bool empty = false;
+  const int rc = check_packed(plan, sequences, rows, H, Hkv, d, scale, &empty);
+  if (rc != FA_OK || empty) return rc;
+  const size_t n = static_cast<size_t>(rows) * H;  // 32-bit row indices
+  if (n > 0x7fffffffu) return FA_ERR_UNSUPPORTED;
+  for (const fa_rows* t : {q, o, dout, dq})
+    if (!rows_ok(t, rows, H, d)) return FA_ERR_INVALID_ARG;
+  for (const fa_rows* t : {k, v, dk, dv})
+    if (!rows_ok(t, rows, Hkv, d)) return FA_ERR_INVALID_ARG;
+  if (!lse || !aligned4(lse)) return FA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < fa_bwd_packed_workspace_bytes(sequences, rows, H, Hkv, d) ||
+      (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0)
+    return FA_ERR_WORKSPACE;
+  char* w = static_cast<char*>(workspace);
+  float* dsum = reinterpret_cast<float*>(w);
+  float* lse_heads = reinterpret_cast<float*>(w + round_up(n * sizeof(float)));
+  float* dq_acc = reinterpret_cast<float*>(w + 2 * round_up(n * sizeof(float)));
+
+  BwdParams p = {};
+  if (!encode_rows_map(&p.tm_q, *q, rows, H, d) || !encode_rows_map(&p.tm_k, *k, rows, Hkv, d) ||
+      !encode_rows_map(&p.tm_v, *v, rows, Hkv, d) || !encode_rows_map(&p.tm_do, *dout, rows, H, d) ||
+      !encode_rows_map(&p.tm_dk, *dk, rows, Hkv, d) || !encode_rows_map(&p.tm_dv, *dv, rows, Hkv, d) ||
+      !encode_dq_map(&p.tm_dq, dq_acc, rows, H, d))
+    return FA_ERR_CUDA;
+  p.lse = lse_heads;
+  p.dsum = dsum;
+  p.dq_acc = dq_acc;
+  p.dk = dk->data;
+  p.dv = dv->data;
+  p.dk_row = row_stride(*dk, rows);
+  p.dk_head = head_stride(*dk, Hkv);
+  p.dv_row = row_stride(*dv, rows);
+  p.dv_head = head_stride(*dv, Hkv);
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  p.N = rows;
+  p.BH = Hkv;
+  p.n_kblk = static_cast<int>(packed_tiles(rows, sequences, kBlockN));  // an upper bound
+  p.c = scale * 1.4426950408889634f;
+  p.scale = scale;
+  p.inv_scale = 1.0f / scale;
+  p.log2e = 1.4426950408889634f;
+  p.group = H / Hkv;
+  p.plan = plan;
+  p.sequences = sequences;
+  p.div_kv = FastDiv(static_cast<uint32_t>(Hkv));
+
+  PackedBwdParams r = {};
+  r.plan = plan;
+  r.sequences = sequences;
+  r.rows = rows;
+  r.H = H;
+  r.o = static_cast<const __nv_bfloat16*>(o->data);
+  r.dout = static_cast<const __nv_bfloat16*>(dout->data);
+  r.o_row = row_stride(*o, rows);
+  r.o_head = head_stride(*o, H);
+  r.do_row = row_stride(*dout, rows);
+  r.do_head = head_stride(*dout, H);
+  r.lse = lse;
+  r.lse_heads = lse_heads;
+  r.dsum = dsum;
+  r.dq_acc = dq_acc;
+  r.dq = static_cast<__nv_bfloat16*>(dq->data);
+  r.dq_row = row_stride(*dq, rows);
+  r.dq_head = head_stride(*dq, H);
+  r.scale = scale;
+  r.div_h = FastDiv(static_cast<uint32_t>(H));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (launch_packed_pre(r, d, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (timing_record(1, true, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_bwd_packed(p, d, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (timing_record(1, false, s) != cudaSuccess) return FA_ERR_CUDA;
+  return launch_packed_post(r, d, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 int fa_rotate(const fa_rows* q, const fa_rows* q_out, int H, const fa_rows* k, const fa_rows* k_out, int Hkv,
               const int* positions, int rows, int d, const float* rope, int rope_len, int rot, int interleaved,
               int backward, void* stream) {

@@ -66,11 +66,12 @@
 // (compute 144, drain 144, load/MMA 80).
 #include "fa_device.cuh"
 #include "fa_kernels.h"
+#include "fa_packed.cuh"
 
 namespace fa {
 namespace {
 
-template <int D, bool kNoDQ = false>
+template <int D, bool kNoDQ = false, bool kPacked = false>
 struct BwdCfg {
   static_assert(D == 64 || D == 128, "head dim");
   // kNoDQ: dK and dV only (the deterministic mode's first pass; dQ comes
@@ -90,6 +91,7 @@ struct BwdCfg {
   static constexpr int kDrainWarp0 = 8;
   static constexpr int kProducerWarp = 12;
   static constexpr int kMmaWarp = 13;
+  static constexpr int kTrimWarp = 14;  // packed: clears rows past a sequence's end
   static constexpr int kTileBytes = kBlockM * D * 2;
   static constexpr int kHalfBytes = kBlockM * 64 * 2;
   // Q_i/dO_i stages: two at d = 128 (all shared memory allows), three at
@@ -155,7 +157,11 @@ struct BwdCfg {
   static constexpr int kBarDQFull = kBarDSFull + 1;
   static constexpr int kBarDQEmpty = kBarDQFull + 1;
   static constexpr int kBarMmaDone = kBarDQEmpty + 1;
-  static constexpr int kNumBars = kBarMmaDone + 1;
+  // packed: K and V, or a stage's Q and dO, that the trim warp has to clear rows
+  // of have landed
+  static constexpr int kBarTrimKV = kBarMmaDone + 1;
+  static constexpr int kBarTrim = kBarTrimKV + 1;
+  static constexpr int kNumBars = kPacked ? kBarTrim + kStages : kBarMmaDone + 1;
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kAbortOff = kTmemSlotOff + 4;
   static constexpr int kSmemBytes = kAbortOff + 4 + 1024;
@@ -204,18 +210,19 @@ enum : unsigned int {
   kSiteDQEmpty = 0x20A,
   kSiteMmaDone = 0x20B,
   kSiteDSTmem = 0x20C,
+  kSiteTrim = 0x20D,
 };
 
 // The query tiles of a CTA in the order its roles walk them: tiles i_first.. of
-// the one head; window: of each query head of the group in turn, the tiles
-// i_first..i_last whose windows reach the key tile.
-template <bool kWindow>
+// the one head; grouped (windows, packed sequences): of each query head of the group in
+// turn, the tiles i_first..i_last that see the key tile.
+template <bool kGrouped>
 struct QueryWalk {
   int i, bh;
   int i_first, i_last;
   __device__ __forceinline__ QueryWalk(int i_first_, int i_last_, int bh0, int start)
       : i(i_first_), bh(bh0), i_first(i_first_), i_last(i_last_) {
-    if constexpr (kWindow) {
+    if constexpr (kGrouped) {
       const int per = i_last - i_first + 1;
       bh += start / per;
       i += start % per;
@@ -223,7 +230,7 @@ struct QueryWalk {
   }
   __device__ __forceinline__ void next() {
     ++i;
-    if constexpr (kWindow)
+    if constexpr (kGrouped)
       if (i > i_last) {
         i = i_first;
         ++bh;
@@ -232,13 +239,17 @@ struct QueryWalk {
 };
 
 // The kernel body; fa_bwd_kernel<D> (all five products), fa_bwd_dkdv_kernel<D>
-// (dK and dV only) and fa_bwd_window_kernel<128> below are its entry points.
+// (dK and dV only), fa_bwd_window_kernel<128> and fa_bwd_packed_kernel<128> below are
+// its entry points.
 // kWindow (d = 128): a row sees the `window` keys up to itself, and the query heads of a
 // group share a key head, whose dK and dV accumulate over them.
-template <int D, bool kNoDQ, bool kWindow = false>
+// kPacked (d = 128): shared key heads as well; a CTA's key tile is an entry of
+// the plan's list, its query tiles those of the same sequence.
+template <int D, bool kNoDQ, bool kWindow = false, bool kPacked = false>
 __device__ __forceinline__ void bwd_body(const BwdParams& p) {
-  static_assert(!kWindow || D == 128, "d = 64 windows: fa_bwd_window64.cu");
-  using C = BwdCfg<D, kNoDQ>;
+  constexpr bool kGrouped = kWindow || kPacked;
+  static_assert(!kGrouped || D == 128, "d = 64: fa_bwd_window64.cu");
+  using C = BwdCfg<D, kNoDQ, kPacked>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
@@ -266,14 +277,23 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       blk = p.split_from + i;
     }
   }
-  const int bh = blk / p.n_kblk;
-  const int kt = blk % p.n_kblk;
+  // Packed: the heads of a sequence in turn, the key tiles of each.  The plan is
+  // earlier work of the stream.
+  PackedItem item{0, p.N, 0, 0, p.causal != 0};
+  if constexpr (kPacked) {
+    grid_dependency_wait();
+    if (!packed_item(p, blk, item)) return;
+  }
+  const int row0 = kPacked ? item.start : 0;  // of the sequence
+  const int len = kPacked ? item.len : p.N;
+  const int bh = kPacked ? item.kv : blk / p.n_kblk;
+  const int kt = kPacked ? item.kt : blk % p.n_kblk;
   const int k0 = kt * kBlockN;
-  const int n_qtiles = (p.N + kBlockM - 1) / kBlockM;
-  const int i_first = kWindow || p.causal ? kt : 0;
+  const int n_qtiles = (len + kBlockM - 1) / kBlockM;
+  const int i_first = kWindow || (kPacked ? item.causal : p.causal != 0) ? kt : 0;
   // (window <= N <= 2^30, so the sum is an int)
   const int i_last = kWindow ? min(n_qtiles - 1, (k0 + kBlockN - 2 + p.window) / kBlockM) : n_qtiles - 1;
-  int n_iter = (kWindow ? p.group : 1) * (i_last - i_first + 1);
+  int n_iter = (kGrouped ? p.group : 1) * (i_last - i_first + 1);
   int it0 = 0;  // the part's first
   if constexpr (kWindow) {
     if (part >= 0) {
@@ -282,29 +302,32 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       n_iter = q + (part < r ? 1 : 0);
     }
   }
-  const int bq0 = kWindow ? bh * p.group : bh;
-  using Walk = QueryWalk<kWindow>;
+  const int bq0 = kGrouped ? bh * p.group : bh;
+  using Walk = QueryWalk<kGrouped>;
 
-  // Window: the loader initialises the barriers and starts the first copies at
+  // Grouped: the loader initialises the barriers and starts the first copies at
   // once, so that they run beside the CTA's set-up (short windows leave few
   // query tiles per CTA to make up for it).
+  // Packed: a tile with rows past the sequence's end goes by the trim warp.
   auto load_kv = [&] {
-    mbar_arrive_expect_tx(bar(C::kBarKV), 2 * C::kTileBytes);
+    const uint32_t full = bar(kPacked && k0 + kBlockN > len ? C::kBarTrimKV : C::kBarKV);
+    mbar_arrive_expect_tx(full, 2 * C::kTileBytes);
     for (int h = 0; h < D / 64; ++h) {
-      tma_load_3d(sbase + C::kKOff + h * C::kHalfBytes, &p.tm_k, bar(C::kBarKV), h * 64, k0, bh);
-      tma_load_3d(sbase + C::kVOff + h * C::kHalfBytes, &p.tm_v, bar(C::kBarKV), h * 64, k0, bh);
+      tma_load_3d(sbase + C::kKOff + h * C::kHalfBytes, &p.tm_k, full, h * 64, row0 + k0, bh);
+      tma_load_3d(sbase + C::kVOff + h * C::kHalfBytes, &p.tm_v, full, h * 64, row0 + k0, bh);
     }
   };
   auto load_tile = [&](int s, int q0, int head) {
-    mbar_arrive_expect_tx(bar(C::kBarStFull + s), 2 * C::kTileBytes);
+    const uint32_t full = bar((kPacked && q0 + kBlockM > len ? C::kBarTrim : C::kBarStFull) + s);
+    mbar_arrive_expect_tx(full, 2 * C::kTileBytes);
     for (int h = 0; h < D / 64; ++h) {
-      tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_q,
-                  bar(C::kBarStFull + s), h * 64, q0, head);
-      tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_do,
-                  bar(C::kBarStFull + s), h * 64, q0, head);
+      tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_q, full, h * 64, row0 + q0,
+                  head);
+      tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes + h * C::kHalfBytes, &p.tm_do, full, h * 64, row0 + q0,
+                  head);
     }
   };
-  if (threadIdx.x == (kWindow ? C::kProducerWarp * 32 : 0)) {
+  if (threadIdx.x == (kGrouped ? C::kProducerWarp * 32 : 0)) {
     *abort_flag = 0;
     mbar_init(bar(C::kBarKV), 1);
     for (int s = 0; s < C::kStages; ++s) {
@@ -320,8 +343,12 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
     mbar_init(bar(C::kBarDQFull), 1);
     mbar_init(bar(C::kBarDQEmpty), kBlockM);
     mbar_init(bar(C::kBarMmaDone), 1);
+    if constexpr (kPacked) {
+      mbar_init(bar(C::kBarTrimKV), 1);
+      for (int s = 0; s < C::kStages; ++s) mbar_init(bar(C::kBarTrim + s), 1);
+    }
     fence_mbar_init();
-    if constexpr (kWindow) {
+    if constexpr (kGrouped) {
       grid_dependency_wait();
       load_kv();
       if (n_iter > 0) {
@@ -355,7 +382,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
         tma_prefetch_desc(&p.tm_do);
-        if constexpr (!kWindow) load_kv();
+        if constexpr (!kGrouped) load_kv();
       }
       int issued = 0;
       Walk walk(i_first, i_last, bq0, it0);
@@ -367,7 +394,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           if (!__all_sync(0xffffffffu, ok)) break;
         }
         const int q0 = walk.i * kBlockM;
-        if (lane == 0 && (!kWindow || it > 0)) load_tile(s, q0, walk.bh);
+        if (lane == 0 && (!kGrouped || it > 0)) load_tile(s, q0, walk.bh);
         if constexpr (C::kRowLse) {
           // fp32 rows -LSE_q log2 e and -D_q (at the start of the stage's
           // bias space); rows past N get -inf (P = 0 there) and D = 0
@@ -391,13 +418,13 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         for (int r4 = 0; r4 < 4; ++r4) {
           const int r = r4 * 32 + lane;
           const int q = q0 + r;
-          const size_t gi = static_cast<size_t>(walk.bh) * p.N + q;
-          const float vl = (q < p.N) ? -p.lse[gi] * p.inv_scale : -1.0e4f;
-          const float vd = (q < p.N) ? -p.dsum[gi] : 0.0f;
+          const size_t gi = static_cast<size_t>(walk.bh) * p.N + row0 + q;
+          const float vl = (q < len) ? -p.lse[gi] * p.inv_scale : -1.0e4f;
+          const float vd = (q < len) ? -p.dsum[gi] : 0.0f;
           const int off = (r >> 3) * C::kBiasSbo + (r & 7) * 16;  // K half 0, from entry 0
           const float lh = __bfloat162float(__float2bfloat16_rn(vl));
           const float dh = __bfloat162float(__float2bfloat16_rn(vd));
-          if constexpr (kWindow) {
+          if constexpr (kGrouped) {
             // what hi + lo leave as a third entry: all 24 bits (two are 2^-18 off, 3%
             // of P where LSE is 8000)
             const float lm = __bfloat162float(__float2bfloat16_rn(vl - lh));
@@ -421,6 +448,41 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         mbar_wait_drain(bar(C::kBarKV), 0);
         for (int it = max(0, issued - C::kStages); it < issued; ++it)
           mbar_wait_drain(bar(C::kBarStFull + it % C::kStages), (it / C::kStages) & 1);
+      }
+    } else if (kPacked && warp == C::kTrimWarp) {
+      // ----------------------------------------------------------- trim
+      // Rows past the sequence's end are another's, or padding, whatever they
+      // hold: as zeros they add nothing to any product.
+      if constexpr (kPacked) {
+        auto clear = [&](int off, int from) {
+          for (int h = 0; h < D / 64; ++h)
+            for (int i = from * 8 + lane; i < kBlockM * 8; i += 32)
+              *reinterpret_cast<uint4*>(smem + off + h * C::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        };
+        bool ok = true;
+        if (k0 + kBlockN > len) {
+          ok = mbar_wait_warp(bar(C::kBarTrimKV), 0, ctl, kSiteTrim);
+          if (ok) {
+            clear(C::kKOff, len - k0);
+            clear(C::kVOff, len - k0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarKV));
+          }
+        }
+        uint32_t parity = 0;  // of each stage's trim barrier
+        Walk walk(i_first, i_last, bq0, it0);
+        for (int it = 0; ok && it < n_iter; ++it, walk.next()) {
+          const int s = it % C::kStages, from = len - walk.i * kBlockM;
+          if (from >= kBlockM) continue;
+          if (!(ok = mbar_wait_warp(bar(C::kBarTrim + s), (parity >> s) & 1u, ctl, kSiteTrim))) break;
+          parity ^= 1u << s;
+          clear(C::kQOff + s * C::kTileBytes, from);
+          clear(C::kDOOff + s * C::kTileBytes, from);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarStFull + s));
+        }
       }
     } else if (warp == C::kMmaWarp && lane == 0) {
       // ----------------------------------------------------------- MMA issue
@@ -486,10 +548,10 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         }
       };
 
-      // Window: the next S^T early at d = 128 too, over P^T_i, although dP^T_{i+1}
+      // Grouped: the next S^T early at d = 128 too, over P^T_i, although dP^T_{i+1}
       // waits for dQ_i in its columns: its few query tiles leave the exponentials
       // on the chain (same sizes as at the drain: 330 us -> 318).
-      constexpr bool kEarly = C::kEarlyS || kWindow;
+      constexpr bool kEarly = C::kEarlyS || kGrouped;
       // S^T_i = K Q_i^T and its bias, once stage s of Q_i has landed.
       auto issue_s = [&](int it) -> bool {
         const int s = it % C::kStages;
@@ -563,7 +625,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         const int q0 = walk.i * kBlockM;
         const bool det = p.dq_part != nullptr;
         float* acc = det ? p.dq_part + (static_cast<size_t>(kt * p.BH + bh) * p.N + q0) * D + dcol
-                         : p.dq_acc + (static_cast<size_t>(walk.bh) * p.N + q0) * D + dcol;
+                         : p.dq_acc + (static_cast<size_t>(walk.bh) * p.N + row0 + q0) * D + dcol;
         uint32_t r[4][32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) tmem_ld32(t_dqt + b * 32, r[b]);
@@ -583,11 +645,11 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         if (det) {  // this key tile's contribution, summed later in key-tile order
 #pragma unroll
           for (int qc = 0; qc < kBlockM; ++qc)
-            if (q0 + qc < p.N) acc[static_cast<size_t>(qc) * D] = __uint_as_float(r[qc >> 5][qc & 31]);
+            if (q0 + qc < len) acc[static_cast<size_t>(qc) * D] = __uint_as_float(r[qc >> 5][qc & 31]);
         } else {
 #pragma unroll
           for (int qc = 0; qc < kBlockM; ++qc)
-            if (q0 + qc < p.N)
+            if (q0 + qc < len)
               atomicAdd(acc + static_cast<size_t>(qc) * D, __uint_as_float(r[qc >> 5][qc & 31]));
         }
       }
@@ -662,7 +724,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
     const int quarter = warp & 3;
     const int kr = quarter * 32 + lane;  // key row within the tile
     const int kpos = k0 + kr;
-    const bool row_valid = kpos < p.N;
+    const bool row_valid = kpos < len;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const f32x2 c2 = f2_pack(p.c, p.c);
     bool ok = true;
@@ -672,7 +734,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       const int i = walk.i;
       // window: also the tiles whose last rows are past some key's window
       const bool diag = kWindow ? i == kt || (i - kt) * kBlockM + kBlockM - 1 >= p.window
-                                : p.causal && i == kt;
+                                : (kPacked ? item.causal : p.causal != 0) && i == kt;
       // S^T_i complete implies Q_i landed: the compute warps read no stage data
       ok = mbar_wait(bar(C::kBarSFull), it & 1, ctl, kSiteSFull);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -714,12 +776,12 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
         p0 = ex2_mufu(x0);
         p1 = ex2_mufu(x1);
       };
-      // Window: one copy of the exponentials and the mask after it (318 us -> 296:
+      // Grouped: one copy of the exponentials and the mask after it (318 us -> 296:
       // the roles' code outgrows the instruction caches), and dS is formed from P
       // as computed instead of as rounded for the dV product: P stays in the
       // registers of S (dP then comes in halves).  The rounding of P would add to
       // dQ and dK as much as dS's own.
-      if constexpr (kWindow) {
+      if constexpr (kGrouped) {
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
@@ -731,8 +793,9 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           }
         if (diag || !row_valid) {
           // the key sees the query columns [lo, lo + window) of the tile
-          const int lo = (kt - i) * kBlockM + kr - wg * 64;
-          const int hi = lo + p.window;
+          // (packed: [lo, ...), from 0 where nothing is masked but the sequence's end)
+          const int lo = kPacked && !diag ? 0 : (kt - i) * kBlockM + kr - wg * 64;
+          const int hi = kPacked ? 64 : lo + p.window;
           auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
@@ -769,7 +832,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
             pw[ch * 16 + e2] = pack_bf16x2(p0, p1);
           }
       }
-      if (!kWindow && !row_valid) {
+      if (!kGrouped && !row_valid) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) pw[e] = 0u;
       }
@@ -790,8 +853,8 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       ok = mbar_wait(bar(C::kBarDPFull), it & 1, ctl, kSiteDPFull);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
-      uint32_t dr[kWindow ? 1 : 2][32];
-      if constexpr (!kWindow) {
+      uint32_t dr[kGrouped ? 1 : 2][32];
+      if constexpr (!kGrouped) {
         tmem_ld32(lane_base + C::kColDP + wg * 64, dr[0]);
         tmem_ld32(lane_base + C::kColDP + wg * 64 + 32, dr[1]);
         tmem_ld_wait(dr[0]);
@@ -800,20 +863,20 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       uint32_t dsw[32];
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
-        if constexpr (kWindow) {
+        if constexpr (kGrouped) {
           tmem_ld32(lane_base + C::kColDP + wg * 64 + ch * 32, dr[0]);
           tmem_ld_wait(dr[0]);
         }
 #pragma unroll
         for (int e2 = 0; e2 < 16; ++e2) {
           float a0, a1;
-          uint32_t (&dc)[32] = dr[kWindow ? 0 : ch];
+          uint32_t (&dc)[32] = dr[kGrouped ? 0 : ch];
           f32x2 dp = f2_pack(__uint_as_float(dc[2 * e2]), __uint_as_float(dc[2 * e2 + 1]));
           if constexpr (C::kRowLse) {
             const float4 d4 = rd4[ch * 8 + (e2 >> 1)];
             dp = f2_add(dp, (e2 & 1) ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y));
           }
-          const f32x2 pp = kWindow ? f2_pack(__uint_as_float(sr[ch][2 * e2]), __uint_as_float(sr[ch][2 * e2 + 1]))
+          const f32x2 pp = kGrouped ? f2_pack(__uint_as_float(sr[ch][2 * e2]), __uint_as_float(sr[ch][2 * e2 + 1]))
                                    : f2_pack(__uint_as_float(pw[ch * 16 + e2] << 16),
                                              __uint_as_float(pw[ch * 16 + e2] & 0xFFFF0000u));
           f2_unpack(f2_mul(dp, pp), a0, a1);
@@ -870,6 +933,9 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       const float mul = wg == 0 ? 1.0f : p.scale;
       const int stage_off = C::kEpiStageOff + wg * C::kEpiStageStride;
       uint8_t* stage = smem + stage_off + kr * 128;
+      // packed: the rows behind a sequence's end are not its own, so a bulk store
+      // is for whole tiles only
+      const bool rows = kPacked && k0 + kBlockN > len;
 #pragma unroll 1
       for (int h = 0; h < D / 64; ++h) {
         uint32_t r[2][32];
@@ -899,6 +965,22 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
             }
           }
         }
+        if constexpr (kPacked) {
+          if (rows && row_valid) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(wg == 0 ? p.dv : p.dk) +
+                                 (row0 + kpos) * (wg == 0 ? p.dv_row : p.dk_row) +
+                                 bh * (wg == 0 ? p.dv_head : p.dk_head) + h * 64;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint32_t* x = &r[c >> 2][(c & 3) * 8];
+              reinterpret_cast<uint4*>(out)[c] =
+                  make_uint4(pack_bf16x2(__uint_as_float(x[0]) * mul, __uint_as_float(x[1]) * mul),
+                             pack_bf16x2(__uint_as_float(x[2]) * mul, __uint_as_float(x[3]) * mul),
+                             pack_bf16x2(__uint_as_float(x[4]) * mul, __uint_as_float(x[5]) * mul),
+                             pack_bf16x2(__uint_as_float(x[6]) * mul, __uint_as_float(x[7]) * mul));
+            }
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint32_t* x = &r[c >> 2][(c & 3) * 8];
@@ -911,11 +993,11 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       }
       fence_proxy_async_smem();
       named_bar_sync(C::kEpiBarrier0 + wg, kBlockM);
-      if (kr == 0 && part < 0) {
+      if (kr == 0 && part < 0 && !rows) {
         const CUtensorMap* map = wg == 0 ? &p.tm_dv : &p.tm_dk;
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h)
-          tma_store_3d(map, sbase + stage_off + h * C::kEpiBoxBytes, h * 64, k0, bh);
+          tma_store_3d(map, sbase + stage_off + h * C::kEpiBoxBytes, h * 64, row0 + k0, bh);
         bulk_commit();
         // The CTA may end once the stores have read shared memory; the
         // grid's completion covers their writes.
@@ -950,9 +1032,17 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   bwd_body<D, false, true>(p);
 }
 
-template <int D, bool kNoDQ, bool kWindow>
+template <int D>
+__global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
+    fa_bwd_packed_kernel(const __grid_constant__ BwdParams p) {
+  bwd_body<D, false, false, true>(p);
+}
+
+template <int D, bool kNoDQ, bool kWindow, bool kPacked>
 constexpr auto bwd_kernel() -> void (*)(BwdParams) {
-  if constexpr (kWindow) {
+  if constexpr (kPacked) {
+    return fa_bwd_packed_kernel<D>;
+  } else if constexpr (kWindow) {
     return fa_bwd_window_kernel<D>;
   } else if constexpr (kNoDQ) {
     return fa_bwd_dkdv_kernel<D>;
@@ -961,10 +1051,10 @@ constexpr auto bwd_kernel() -> void (*)(BwdParams) {
   }
 }
 
-template <int D, bool kNoDQ = false, bool kWindow = false>
+template <int D, bool kNoDQ = false, bool kWindow = false, bool kPacked = false>
 cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
-  using C = BwdCfg<D, kNoDQ>;
-  constexpr auto kernel = bwd_kernel<D, kNoDQ, kWindow>();
+  using C = BwdCfg<D, kNoDQ, kPacked>;
+  constexpr auto kernel = bwd_kernel<D, kNoDQ, kWindow, kPacked>();
   cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   long long blocks = static_cast<long long>(p.n_kblk) * p.BH;
@@ -986,6 +1076,12 @@ cudaError_t launch_bwd_main(const BwdParams& p, int d, cudaStream_t stream) {
 cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream) {
   if (d == 128) return launch_bwd_d<128, false, true>(p, stream);
   if (d == 64) return launch_bwd_window64(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_bwd_packed(const BwdParams& p, int d, cudaStream_t stream) {
+  if (d == 128) return launch_bwd_d<128, false, false, true>(p, stream);
+  if (d == 64) return launch_bwd_packed64(p, stream);
   return cudaErrorInvalidValue;
 }
 

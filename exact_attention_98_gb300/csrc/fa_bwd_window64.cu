@@ -36,12 +36,14 @@
 // that rounding would add to dQ and dK as much as dS's own.
 #include "fa_device.cuh"
 #include "fa_kernels.h"
+#include "fa_packed.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int D = 64;
 
+template <bool kPacked>
 struct WinCfg {
   static constexpr int kThreads = 512;
   static constexpr int kLaunchRegs = 128;
@@ -55,6 +57,7 @@ struct WinCfg {
   static constexpr int kProducerWarp = 12;
   static constexpr int kMmaWarp = 13;
   static constexpr int kKVWarp = 14;  // loads K and V (the producer runs tiles ahead of them)
+  static constexpr int kTrimWarp = 15;  // packed: clears rows past a sequence's end
   static constexpr int kTileBytes = kBlockM * D * 2;
   static constexpr int kHalfBytes = kBlockM * 64 * 2;
   static constexpr int kStages = 3;
@@ -86,7 +89,11 @@ struct WinCfg {
   static constexpr int kBarMmaDone = kBarDQEmpty + 1;  // an item's products are complete
   static constexpr int kBarAccFree = kBarMmaDone + 1;  // its dV and dK have left tensor memory
   static constexpr int kBarKVFree = kBarAccFree + 1;   // its dV and dK have left K's and V's buffer
-  static constexpr int kNumBars = kBarKVFree + 1;
+  // packed: K and V in buffer m % 2, or a stage's Q and dO, that the trim warp has
+  // to clear rows of have landed
+  static constexpr int kBarTrimKV = kBarKVFree + 1;
+  static constexpr int kBarTrim = kBarTrimKV + 2;
+  static constexpr int kNumBars = kPacked ? kBarTrim + kStages : kBarKVFree + 1;
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kAbortOff = kTmemSlotOff + 4;
   static constexpr int kSmemBytes = kAbortOff + 4 + 1024;
@@ -119,12 +126,16 @@ enum : unsigned int {
   kSiteDSTmem = 0x21C,
   kSiteAccFree = 0x21D,
   kSiteKVFree = 0x21E,
+  kSiteTrim = 0x21F,
 };
 
 // Block `blk` of the list of items: a key tile of a key head (from split_from
 // on a part of its query tiles) and its query tiles i_first..i_last, head by head.
+template <bool kPacked>
 struct KeyItem {
   int bh, kt, k0;  // key head, key tile, its first key
+  int start, len;  // packed: rows of the sequence
+  bool causal;
   int part;        // of a split item, else -1
   int i_first, i_last;
   int n_iter;      // query tiles (all heads')
@@ -136,11 +147,31 @@ struct KeyItem {
       ++head;
     }
   }
+  // the first row and the rows of what the tiles are counted in: the
+  // sequence, or all
+  __device__ __forceinline__ int row0() const { return kPacked ? start : 0; }
+  __device__ __forceinline__ int rows(const BwdParams& p) const { return kPacked ? len : p.N; }
 };
 
-__device__ __forceinline__ KeyItem key_item(const BwdParams& p, int blk) {
-  KeyItem t;
+template <bool kPacked>
+__device__ __forceinline__ KeyItem<kPacked> key_item(const BwdParams& p, int blk) {
+  KeyItem<kPacked> t;
   t.part = -1;
+  if constexpr (kPacked) {
+    const PackedItem item = packed_item_at(p, blk);
+    t.start = item.start;
+    t.len = item.len;
+    t.causal = item.causal;
+    t.bh = item.kv;
+    t.kt = item.kt;
+    t.k0 = t.kt * kBlockN;
+    t.i_first = t.causal ? t.kt : 0;
+    t.i_last = (t.len + kBlockM - 1) / kBlockM - 1;
+    t.n_iter = p.group * (t.i_last - t.i_first + 1);
+    t.head = t.bh * p.group;
+    t.i = t.i_first;
+    return t;
+  }
   int item = blk;
   if (blk >= p.split_from) {
     const int i = p.div_parts.div(blk - p.split_from);
@@ -173,17 +204,22 @@ __device__ __forceinline__ KeyItem key_item(const BwdParams& p, int blk) {
 
 // The next block from `blk` on, in steps of `stride`, that has query tiles (a
 // part of a split item may have none); false if there is none.
-__device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stride, int total, KeyItem& t) {
+template <bool kPacked>
+__device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stride, int total, KeyItem<kPacked>& t) {
   for (; blk < total; blk += stride) {
-    t = key_item(p, blk);
+    t = key_item<kPacked>(p, blk);
     if (t.n_iter > 0) return true;
   }
   return false;
 }
 
-__global__ void __launch_bounds__(WinCfg::kThreads, 1)
+// kPacked: items come from a plan of packed sequences; the tiles' rows are
+// a sequence's, the masks the diagonal (if causal) and the sequence's end.
+template <bool kPacked>
+__global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     fa_bwd_window64_kernel(const __grid_constant__ BwdParams p) {
-  using C = WinCfg;
+  using C = WinCfg<kPacked>;
+  using KeyItem = KeyItem<kPacked>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
@@ -194,7 +230,13 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
   const WaitCtl ctl{abort_flag, p.status};
   const int warp = warp_id();
   const int lane = lane_id();
-  const int total = p.split_from + (p.n_kblk * p.BH - p.split_from) * p.split_parts;
+  int total = 0;
+  if constexpr (kPacked) {
+    grid_dependency_wait();  // the plan is earlier work of the stream
+    total = packed_items(p);
+  } else {
+    total = p.split_from + (p.n_kblk * p.BH - p.split_from) * p.split_parts;
+  }
   const int stride = static_cast<int>(gridDim.x);
 
   // One arrival for the warp's lanes, each of which has made its own fence: lanes
@@ -207,14 +249,17 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
   // m: the CTA's count of items that have query tiles
   auto load_kv = [&](int m, const KeyItem& t) {
     const int b = m & 1;
-    mbar_arrive_expect_tx(bar(C::kBarKV + b), 2 * C::kTileBytes);
-    tma_load_3d(sbase + C::kKOff + b * C::kTileBytes, &p.tm_k, bar(C::kBarKV + b), 0, t.k0, t.bh);
-    tma_load_3d(sbase + C::kVOff + b * C::kTileBytes, &p.tm_v, bar(C::kBarKV + b), 0, t.k0, t.bh);
+    const uint32_t full = bar((kPacked && t.k0 + kBlockN > t.len ? C::kBarTrimKV : C::kBarKV) + b);
+    mbar_arrive_expect_tx(full, 2 * C::kTileBytes);
+    tma_load_3d(sbase + C::kKOff + b * C::kTileBytes, &p.tm_k, full, 0, t.row0() + t.k0, t.bh);
+    tma_load_3d(sbase + C::kVOff + b * C::kTileBytes, &p.tm_v, full, 0, t.row0() + t.k0, t.bh);
   };
   auto load_tile = [&](int s, const KeyItem& t) {
-    mbar_arrive_expect_tx(bar(C::kBarStFull + s), 2 * C::kTileBytes);
-    tma_load_3d(sbase + C::kQOff + s * C::kTileBytes, &p.tm_q, bar(C::kBarStFull + s), 0, t.i * kBlockM, t.head);
-    tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes, &p.tm_do, bar(C::kBarStFull + s), 0, t.i * kBlockM, t.head);
+    const int q0 = t.i * kBlockM;
+    const uint32_t full = bar((kPacked && q0 + kBlockM > t.len ? C::kBarTrim : C::kBarStFull) + s);
+    mbar_arrive_expect_tx(full, 2 * C::kTileBytes);
+    tma_load_3d(sbase + C::kQOff + s * C::kTileBytes, &p.tm_q, full, 0, t.row0() + q0, t.head);
+    tma_load_3d(sbase + C::kDOOff + s * C::kTileBytes, &p.tm_do, full, 0, t.row0() + q0, t.head);
   };
 
   // the loader's thread initialises the barriers and starts the first item's
@@ -237,6 +282,8 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     mbar_init(bar(C::kBarMmaDone), 1);
     mbar_init(bar(C::kBarAccFree), C::kComputeWarps);
     mbar_init(bar(C::kBarKVFree), 2);
+    if constexpr (kPacked)
+      for (int b = 0; b < 2 + C::kStages; ++b) mbar_init(bar(C::kBarTrimKV + b), 1);
     fence_mbar_init();
     grid_dependency_wait();
     KeyItem t;
@@ -273,13 +320,13 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
           // fp32 rows -LSE_q log2 e and -D_q; rows past N get -inf (P = 0 there)
           // and D = 0.  Read before the wait for the stage.
           const int q0 = t.i * kBlockM;
-          const size_t head_row = static_cast<size_t>(t.head) * p.N;
+          const size_t head_row = static_cast<size_t>(t.head) * p.N + t.row0();
           float nl[4], nd[4];
 #pragma unroll
           for (int r4 = 0; r4 < 4; ++r4) {
             const int q = q0 + r4 * 32 + lane;
-            nl[r4] = (q < p.N) ? -p.lse[head_row + q] * p.log2e : -INFINITY;
-            nd[r4] = (q < p.N) ? -p.dsum[head_row + q] : 0.0f;
+            nl[r4] = (q < t.rows(p)) ? -p.lse[head_row + q] * p.log2e : -INFINITY;
+            nd[r4] = (q < t.rows(p)) ? -p.dsum[head_row + q] : 0.0f;
           }
           if (n >= C::kStages && !wait(C::kBarStEmpty + s, (n / C::kStages - 1) & 1, kSiteStEmpty)) break;
           if (lane == 0 && n > 0) load_tile(s, t);  // (the very first is on its way)
@@ -322,6 +369,48 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
       }
       if (!ok)
         for (int k = m - 2; k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
+    } else if (kPacked && warp == C::kTrimWarp) {
+      // ----------------------------------------------------------- trim
+      // Rows past the sequence's end are another's, or padding, whatever they
+      // hold: as zeros they add nothing to any product.
+      if constexpr (kPacked) {
+        auto clear = [&](int off, int from) {
+          for (int i = from * 8 + lane; i < kBlockM * 8; i += 32)
+            *reinterpret_cast<uint4*>(smem + off + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto give = [&](int b) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(b));
+        };
+        uint32_t parity = 0;  // of the trim barriers
+        auto wait = [&](int b) {
+          const int i = b - C::kBarTrimKV;
+          const bool ok = mbar_wait_short_warp(bar(b), (parity >> i) & 1u, ctl, kSiteTrim);
+          parity ^= 1u << i;
+          return ok;
+        };
+        int n = 0, m = 0;
+        bool ok = true;
+        int blk = blockIdx.x;
+        KeyItem t;
+        for (; ok && next_item(p, blk, stride, total, t); blk += stride, ++m) {
+          if (t.k0 + kBlockN > t.len) {
+            if (!(ok = wait(C::kBarTrimKV + (m & 1)))) break;
+            clear(C::kKOff + (m & 1) * C::kTileBytes, t.len - t.k0);
+            clear(C::kVOff + (m & 1) * C::kTileBytes, t.len - t.k0);
+            give(C::kBarKV + (m & 1));
+          }
+          for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
+            const int s = n % C::kStages, from = t.len - t.i * kBlockM;
+            if (from >= kBlockM) continue;
+            if (!(ok = wait(C::kBarTrim + s))) break;
+            clear(C::kQOff + s * C::kTileBytes, from);
+            clear(C::kDOOff + s * C::kTileBytes, from);
+            give(C::kBarStFull + s);
+          }
+        }
+      }
     } else if (warp == C::kMmaWarp) {
       // ----------------------------------------------------------- MMA issue
       // warp-uniform code (see fa_device.cuh): operand arithmetic in uniform
@@ -451,6 +540,13 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         reg_fence16(r[3]);
         tc_fence_before();
         warp_arrive(bar(C::kBarDQEmpty));
+        // packed: rows past the sequence's end add zeros to whatever follows it
+        if (kPacked && q0 + qr >= t.len) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[c][e] = 0u;
+        }
         // The fp32 dQ tile goes out in chunks of 16 columns (64-byte swizzled rows)
         // through a ring of buffers; the TMA adds them into the accumulator.
 #pragma unroll
@@ -466,7 +562,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
           // issued: the buffer written after the barrier is free.
           named_bar_sync(C::kDrainBarrier, kBlockM);
           if (leader) {
-            tma_reduce_add_3d(&p.tm_dq, smem_u32(chunk), c * C::kDqCols, q0, t.head);
+            tma_reduce_add_3d(&p.tm_dq, smem_u32(chunk), c * C::kDqCols, t.row0() + q0, t.head);
             bulk_commit();
             bulk_wait_read<1>();
           }
@@ -495,16 +591,17 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
     int n = 0, m = 0;
     bool ok = true;
     KeyItem t_next;
-    if (static_cast<int>(blockIdx.x) < total) t_next = key_item(p, blockIdx.x);
+    if (static_cast<int>(blockIdx.x) < total) t_next = key_item<kPacked>(p, blockIdx.x);
     for (int blk = blockIdx.x; ok && blk < total; blk += stride) {
       KeyItem t = t_next;
-      const bool row_valid = t.k0 + kr < p.N;
-      const bool last_tile = t.k0 + kBlockN > p.N;  // some key rows are past N
+      const bool row_valid = t.k0 + kr < t.rows(p);
+      const bool last_tile = t.k0 + kBlockN > t.rows(p);  // some key rows are past the last
       for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
         const int s = n % C::kStages;
         // the diagonal tile, those whose last rows are past some key's window,
         // and all of a key tile with rows past N
-        const bool edge = t.i == t.kt || (t.i - t.kt) * kBlockM + kBlockM - 1 >= p.window || last_tile;
+        const bool edge = kPacked ? (t.causal && t.i == t.kt) || last_tile
+                                  : t.i == t.kt || (t.i - t.kt) * kBlockM + kBlockM - 1 >= p.window || last_tile;
         ok = mbar_wait_short(bar(C::kBarSFull), n & 1, ctl, kSiteSFull);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
@@ -539,8 +636,9 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
           }
         if (edge) {
           // the key sees the query columns [lo, lo + window) of the tile
-          const int lo = (t.kt - t.i) * kBlockM + kr - wg * 64;
-          const int hi = lo + p.window;
+          // (packed: [lo, ...) if causal, all otherwise)
+          const int lo = kPacked && !t.causal ? 0 : (t.kt - t.i) * kBlockM + kr - wg * 64;
+          const int hi = kPacked ? 64 : lo + p.window;
           auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
@@ -603,7 +701,7 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(bar(C::kBarDSFull));
       }
-      if (blk + stride < total) t_next = key_item(p, blk + stride);
+      if (blk + stride < total) t_next = key_item<kPacked>(p, blk + stride);
 
       // The item's dV (warpgroup 0) and dK (warpgroup 1, times the softmax scale,
       // which dS left out): a thread holds its key row.
@@ -611,7 +709,9 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
       // of a part's (zeros if it has no query tile), and the first tokens', which
       // also get the queries whose windows have left them.
       float* raw = nullptr;
-      if (t.part >= 0)
+      if (kPacked)
+        raw = nullptr;
+      else if (t.part >= 0)
         raw = p.tile_part + ((static_cast<size_t>(blk - p.split_from) * 2 + (wg == 0 ? 1 : 0)) * kBlockN + kr) * D;
       else if (p.sink_main != nullptr && t.kt == 0 && kr < p.sinks)
         raw = p.sink_main + ((static_cast<size_t>(t.bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D;
@@ -662,8 +762,19 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
         }
         fence_proxy_async_smem();
         named_bar_sync(C::kEpiBarrier0 + wg, kBlockM);
-        if (kr == 0) {
-          tma_store_3d(wg == 0 ? &p.tm_dv : &p.tm_dk, sbase + off, 0, t.k0, t.bh);
+        if (kPacked && last_tile) {
+          // the rows behind a sequence's end are not its own: each thread its row
+          if (row_valid) {
+            uint4* out = reinterpret_cast<uint4*>(
+                static_cast<__nv_bfloat16*>(wg == 0 ? p.dv : p.dk) +
+                (t.start + t.k0 + kr) * (wg == 0 ? p.dv_row : p.dk_row) + t.bh * (wg == 0 ? p.dv_head : p.dk_head));
+#pragma unroll
+            for (int c = 0; c < 8; ++c) out[c] = *reinterpret_cast<const uint4*>(row + ((c ^ (kr & 7)) << 4));
+          }
+          // (the buffer is read before its next load)
+          named_bar_sync(C::kEpiBarrier0 + wg, kBlockM);
+        } else if (kr == 0) {
+          tma_store_3d(wg == 0 ? &p.tm_dv : &p.tm_dk, sbase + off, 0, t.row0() + t.k0, t.bh);
           bulk_commit();
         }
       }
@@ -686,17 +797,31 @@ __global__ void __launch_bounds__(WinCfg::kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_bwd_window64(const BwdParams& p, cudaStream_t stream) {
-  using C = WinCfg;
-  cudaError_t err = configure_kernel<fa_bwd_window64_kernel>(C::kSmemBytes, C::kLaunchRegs);
+namespace {
+
+// `total`: the items, or (packed) more than there are
+template <bool kPacked>
+cudaError_t launch(const BwdParams& p, int total, cudaStream_t stream) {
+  using C = WinCfg<kPacked>;
+  constexpr auto kernel = fa_bwd_window64_kernel<kPacked>;
+  cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int total = p.split_from + (p.n_kblk * p.BH - p.split_from) * p.split_parts;
-  err = launch_dependent(fa_bwd_window64_kernel, dim3(static_cast<unsigned int>(total < sms ? total : sms)),
+  err = launch_dependent(kernel, dim3(static_cast<unsigned int>(total < sms ? total : sms)),
                          dim3(C::kThreads), C::kSmemBytes, stream, p);
   if (err != cudaSuccess) return err;
   return launched(1);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_window64(const BwdParams& p, cudaStream_t stream) {
+  return launch<false>(p, p.split_from + (p.n_kblk * p.BH - p.split_from) * p.split_parts, stream);
+}
+
+cudaError_t launch_bwd_packed64(const BwdParams& p, cudaStream_t stream) {
+  return launch<true>(p, p.n_kblk * p.BH, stream);
 }
 
 }  // namespace fa

@@ -145,6 +145,13 @@ struct BwdParams {
   int split_parts;
   float* tile_part;
   FastDiv div_kblk, div_parts;  // window: by n_kblk, by split_parts
+  // Packed sequences (the packed kernels only): items come from the plan, N is the
+  // rows of all sequences, BH the key heads, and `group` query heads share one;
+  // lse and dsum are [query heads, N] as elsewhere.
+  const void* plan;
+  int sequences;
+  long long dk_row, dk_head, dv_row, dv_head;  // strides in elements
+  FastDiv div_kv;  // by BH
 };
 
 // What the sliding-window backward does beside its main kernel (fa_window.cu):
@@ -300,6 +307,9 @@ cudaError_t launch_bwd_main(const BwdParams& p, int d, cudaStream_t stream);
 // The same kernel with a sliding window and shared key heads (p.window, p.group).
 cudaError_t launch_bwd_window(const BwdParams& p, int d, cudaStream_t stream);
 cudaError_t launch_bwd_window64(const BwdParams& p, cudaStream_t stream);  // its d = 64 form (fa_bwd_window64.cu)
+// The same kernels over packed sequences (p.plan, p.group).
+cudaError_t launch_bwd_packed(const BwdParams& p, int d, cudaStream_t stream);
+cudaError_t launch_bwd_packed64(const BwdParams& p, cudaStream_t stream);
 // Before it, where queries see first tokens that their windows have left: D, and
 // those pairs' share of dQ in the accumulator, of dK and dV in sink_part.
 cudaError_t launch_window_pre(const WindowParams& p, int d, cudaStream_t stream);
@@ -325,6 +335,28 @@ struct PackedPlanParams {
   unsigned int* status;
 };
 cudaError_t launch_packed_plan(PackedPlanParams p, cudaStream_t stream);
+
+// What the packed backward does beside its main kernel (fa_packed.cu): before it D,
+// LSE by heads and the zeroed dQ accumulator, after it dQ as bf16.
+struct PackedBwdParams {
+  const void* plan;
+  int sequences;
+  int rows;
+  int H;
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* dout;
+  long long o_row, o_head, do_row, do_head;  // strides in elements
+  const float* lse;   // [rows, H]
+  float* lse_heads;   // [H, rows]
+  float* dsum;        // [H, rows]
+  float* dq_acc;      // [H, rows, d]
+  __nv_bfloat16* dq;
+  long long dq_row, dq_head;
+  float scale;
+  FastDiv div_h;      // by H
+};
+cudaError_t launch_packed_pre(const PackedBwdParams& p, int d, cudaStream_t stream);
+cudaError_t launch_packed_post(const PackedBwdParams& p, int d, cudaStream_t stream);
 
 // Rotation of Q and K rows (fa_rotate.cu).
 struct RotateParams {

@@ -151,7 +151,112 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
   }
 }
 
+// Before the backward's main kernel: D = rowsum(dO * O) and LSE by heads, where the
+// main kernel reads a head's rows one after another, and the zeroed dQ
+// accumulator.  16 bytes of a row to a lane.  Rows of no sequence are left out.
+// After it: dQ = scale * accumulator -> bf16.  Both are bound by HBM.
+constexpr int kRowThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) fa_packed_pre_kernel(const __grid_constant__ PackedBwdParams p) {
+  constexpr int kLanes = D / 8;
+  grid_dependency_wait();
+  const PackedHead& head = *static_cast<const PackedHead*>(p.plan);
+  if (!packed_fits(head, p.rows, p.sequences)) return;  // (the main kernel records it)
+  const int col = static_cast<int>(threadIdx.x) % kLanes * 8;
+  const long long n = static_cast<long long>(head.end - head.begin) * p.H;
+  // (whole warps leave the loop together: a warp's rows are neighbours)
+  for (long long i0 = blockIdx.x * static_cast<long long>(kRowThreads / kLanes); i0 < n;
+       i0 += static_cast<long long>(gridDim.x) * (kRowThreads / kLanes)) {
+    const long long i = i0 + threadIdx.x / kLanes;
+    float acc = 0.0f;
+    size_t at = 0;
+    long long row = 0;
+    int h = 0;
+    if (i < n) {
+      const uint32_t t = p.div_h.div(static_cast<uint32_t>(i));
+      row = head.begin + static_cast<long long>(t);
+      h = static_cast<int>(static_cast<uint32_t>(i) - t * p.div_h.d);
+      at = static_cast<size_t>(h) * p.rows + row;
+      const uint4 a = *reinterpret_cast<const uint4*>(p.o + row * p.o_row + h * p.o_head + col);
+      const uint4 b = *reinterpret_cast<const uint4*>(p.dout + row * p.do_row + h * p.do_head + col);
+      const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
+      const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 x = __bfloat1622float2(a2[c]), y = __bfloat1622float2(b2[c]);
+        acc = fmaf(x.x, y.x, acc);
+        acc = fmaf(x.y, y.y, acc);
+      }
+      float4* z = reinterpret_cast<float4*>(p.dq_acc + at * D + col);
+      z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (i < n && col == 0) {
+      p.dsum[at] = acc;
+      p.lse_heads[at] = p.lse[row * p.H + h];
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) fa_packed_post_kernel(const __grid_constant__ PackedBwdParams p) {
+  constexpr int kLanes = D / 8, kRows = kRowThreads / kLanes, kUnroll = 4;
+  grid_dependency_wait();
+  const PackedHead& head = *static_cast<const PackedHead*>(p.plan);
+  if (!packed_fits(head, p.rows, p.sequences)) return;
+  const int col = static_cast<int>(threadIdx.x) % kLanes * 8;
+  const long long n = static_cast<long long>(head.end - head.begin) * p.H;
+  for (long long i0 = blockIdx.x * static_cast<long long>(kRows * kUnroll) + threadIdx.x / kLanes; i0 < n;
+       i0 += static_cast<long long>(gridDim.x) * (kRows * kUnroll)) {
+    float4 a[kUnroll], b[kUnroll];
+    __nv_bfloat16* to[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long i = i0 + u * kRows;
+      to[u] = nullptr;
+      if (i < n) {
+        const uint32_t t = p.div_h.div(static_cast<uint32_t>(i));
+        const long long row = head.begin + static_cast<long long>(t);
+        const int h = static_cast<int>(static_cast<uint32_t>(i) - t * p.div_h.d);
+        const float4* from = reinterpret_cast<const float4*>(p.dq_acc + (static_cast<size_t>(h) * p.rows + row) * D + col);
+        a[u] = from[0];
+        b[u] = from[1];
+        to[u] = p.dq + row * p.dq_row + h * p.dq_head + col;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (to[u] != nullptr)
+        *reinterpret_cast<uint4*>(to[u]) =
+            make_uint4(pack_bf16x2(a[u].x * p.scale, a[u].y * p.scale), pack_bf16x2(a[u].z * p.scale, a[u].w * p.scale),
+                       pack_bf16x2(b[u].x * p.scale, b[u].y * p.scale), pack_bf16x2(b[u].z * p.scale, b[u].w * p.scale));
+  }
+}
+
+// Blocks for n rows of a head: as many as are resident at once, at most.
+dim3 row_grid(long long n, int per_block) {
+  const long long blocks = (n + per_block - 1) / per_block, cap = 8LL * (sm_count() > 0 ? sm_count() : 1);
+  return dim3(static_cast<unsigned int>(blocks < cap ? blocks : cap));
+}
+
 }  // namespace
+
+cudaError_t launch_packed_pre(const PackedBwdParams& p, int d, cudaStream_t stream) {
+  const cudaError_t err = launch_dependent(d == 128 ? fa_packed_pre_kernel<128> : fa_packed_pre_kernel<64>,
+                                           row_grid(static_cast<long long>(p.rows) * p.H, kRowThreads / (d / 8)),
+                                           dim3(kRowThreads), 0, stream, p);
+  return err != cudaSuccess ? err : launched(1);
+}
+
+cudaError_t launch_packed_post(const PackedBwdParams& p, int d, cudaStream_t stream) {
+  const cudaError_t err = launch_dependent(d == 128 ? fa_packed_post_kernel<128> : fa_packed_post_kernel<64>,
+                                           row_grid(static_cast<long long>(p.rows) * p.H, 4 * kRowThreads / (d / 8)),
+                                           dim3(kRowThreads), 0, stream, p);
+  return err != cudaSuccess ? err : launched(1);
+}
 
 cudaError_t launch_packed_plan(PackedPlanParams p, cudaStream_t stream) {
   // the last bucket that a sequence of all the rows reaches

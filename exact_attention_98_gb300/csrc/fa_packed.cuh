@@ -65,4 +65,44 @@ __device__ __forceinline__ bool packed_fits(const PackedHead& h, int rows, int s
   return h.magic == kPackedMagic && h.rows == rows && h.sequences == sequences;
 }
 
+// Work item of the backward: a key tile of a key head.  Item i belongs to the
+// sequence of entry i / Hkv of seq_tiles; within a sequence the heads come one
+// after another, the key tiles of each in order (causal: those of most work first), so
+// that CTAs that run at the same time add to the same rows of dQ.
+struct PackedItem {
+  int start, len;  // rows of the sequence
+  int kt;          // key tile
+  int kv;          // key head
+  bool causal;
+};
+
+// Items of a backward call: 0 when the plan is not one for its rows (recorded).
+__device__ __forceinline__ int packed_items(const BwdParams& p) {
+  const PackedHead& h = *static_cast<const PackedHead*>(p.plan);
+  if (!packed_fits(h, p.N, p.sequences)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kPackedInvalid, kSitePackedPlan);
+    return 0;
+  }
+  return h.n_tiles * p.BH;
+}
+
+// Item i (< packed_items) of a backward call.
+__device__ __forceinline__ PackedItem packed_item_at(const BwdParams& p, int i) {
+  const uint8_t* plan = static_cast<const uint8_t*>(p.plan);
+  const int4 e = reinterpret_cast<const int4*>(plan + packed_layout(p.N, p.sequences).seq_tiles)[p.div_kv.div(i)];
+  PackedItem it;
+  it.start = e.x;
+  it.len = e.y;
+  const int tiles = (e.y + kBlockN - 1) / kBlockN, at = i - e.w * p.BH;
+  it.kv = at / tiles;
+  it.kt = at - it.kv * tiles;
+  it.causal = reinterpret_cast<const PackedHead*>(plan)->causal != 0;
+  return it;
+}
+__device__ __forceinline__ bool packed_item(const BwdParams& p, int i, PackedItem& it) {
+  if (i >= packed_items(p)) return false;
+  it = packed_item_at(p, i);
+  return true;
+}
+
 }  // namespace fa

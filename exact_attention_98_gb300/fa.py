@@ -134,6 +134,11 @@ def _load() -> ctypes.CDLL:
     lib.fa_packed_plan.restype = i
     lib.fa_fwd_packed.argtypes = [vp, i, i, rows, rows, rows, rows, vp, i, i, i, f, vp]
     lib.fa_fwd_packed.restype = i
+    lib.fa_bwd_packed_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.fa_bwd_packed_workspace_bytes.restype = sz
+    lib.fa_bwd_packed.argtypes = [vp, i, i, rows, rows, rows, rows, vp, rows, rows, rows, rows, i, i, i, f, vp, sz,
+                                  vp]
+    lib.fa_bwd_packed.restype = i
     lib.fa_rotate.argtypes = [rows, rows, i, rows, rows, i, vp, i, i, vp, i, i, i, i, vp]
     lib.fa_rotate.restype = i
     lib.fa_launch_count.argtypes = []
@@ -479,6 +484,17 @@ def fa_fwd_packed(plan, sequences, rows, q: Rows, k: Rows, v: Rows, o: Rows, lse
                              _stream(stream)), "fa_fwd_packed")
 
 
+def fa_bwd_packed_workspace_bytes(sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib.fa_bwd_packed_workspace_bytes(sequences, rows, H, Hkv, d))
+
+
+def fa_bwd_packed(plan, sequences, rows, q: Rows, k: Rows, v: Rows, o: Rows, lse, dout: Rows, dq: Rows,
+                  dk: Rows, dv: Rows, H, Hkv, d, scale, workspace, stream=None) -> None:
+    ws_ptr, ws_bytes = _workspace(workspace, plan.device)
+    _check(lib.fa_bwd_packed(_ptr(plan), sequences, rows, q, k, v, o, _ptr(lse), dout, dq, dk, dv, H, Hkv, d,
+                             float(scale), ws_ptr, ws_bytes, _stream(stream)), "fa_bwd_packed")
+
+
 def fa_rotate(q: Rows, q_out: Rows, H, k: Rows, k_out: Rows, Hkv, positions, rows, d, rope, rope_len, rot,
               interleaved, backward, stream=None) -> None:
     _check(lib.fa_rotate(q, q_out, H, k, k_out, Hkv, _ptr(positions), rows, d, _ptr(rope), rope_len, rot,
@@ -811,6 +827,28 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
                   _packed_rows(out, "out", rows, H, d, dev), lse, H, Hkv, d,
                   default_scale(d) if scale is None else scale, stream)
     return out, lse
+
+
+def packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float | None = None, out=None,
+                    workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of packed_forward, shaped as q, k and v; dk and dv are
+    summed over the query heads that share a key head.  out: (dq, dk, dv) to write
+    to, strides as q (parts of a fused projection's gradient, say).  Padding rows of the results are
+    not written."""
+    rows, H, Hkv, d = _packed_heads(q, k, plan)
+    dev = q.device
+    if out is None:
+        out = _empty(stream, dev, *[((rows, h, d), torch.bfloat16) for h in (H, Hkv, Hkv)])
+    dq, dk, dv = out
+    if workspace is None:
+        n = fa_bwd_packed_workspace_bytes(plan.sequences, rows, H, Hkv, d)
+        workspace, = _empty(stream, dev, (max(n, 1), torch.uint8))
+    _check_tensor(lse, "lse", torch.float32, (rows, H), dev)
+    of_q = [_packed_rows(t, name, rows, H, d, dev) for t, name in ((q, "q"), (o, "o"), (dout, "dout"), (dq, "dq"))]
+    of_k = [_packed_rows(t, name, rows, Hkv, d, dev) for t, name in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv"))]
+    fa_bwd_packed(plan.plan, plan.sequences, rows, of_q[0], of_k[0], of_k[1], of_q[1], lse, of_q[2], of_q[3], of_k[2],
+                  of_k[3], H, Hkv, d, default_scale(d) if scale is None else scale, workspace, stream)
+    return dq, dk, dv
 
 
 def rotate(q, k, positions, rope, interleaved: bool = False, backward: bool = False, out=None, stream=None):

@@ -380,6 +380,25 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
                   void* stream);
 
 /*
+ * Backward of fa_fwd_packed, as fa_bwd: gradients of sum(O * dO); dk and dv
+ * are summed over the query heads of the group (in fp32, in an order that does not
+ * vary: bit-identical from run to run; dq within the order of its fp32 additions).
+ *   o, lse     : in,  the forward's outputs
+ *   dout, dq   : in, out: row tensors of H heads; dk, dv: out, of Hkv heads
+ *   workspace  : fa_bwd_packed_workspace_bytes() bytes, 256-byte aligned, contents
+ *                on entry irrelevant: fp32 D and LSE by heads, and the dQ
+ *                accumulator.  0 for empty or unsupported shapes.
+ * What rows of the other sequences and padding rows hold does not matter; a
+ * sequence's own rows have to be finite, all of them.  rows * H up to 2^31 - 1
+ * (FA_ERR_UNSUPPORTED).
+ */
+size_t fa_bwd_packed_workspace_bytes(int sequences, int rows, int H, int Hkv, int d);
+int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k,
+                  const fa_rows* v, const fa_rows* o, const float* lse, const fa_rows* dout,
+                  const fa_rows* dq, const fa_rows* dk, const fa_rows* dv, int H, int Hkv, int d,
+                  float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Rotates Q and K rows by their positions (before fa_fwd_packed), or turns their
  * gradients back (after fa_bwd_packed).
  *   q, q_out  : in, out: row tensors of H heads, or both NULL (H = 0)
@@ -576,7 +595,7 @@ int fa_timing_last_ms(int kernel, float* ms);
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
  * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three;
  * fa_paged_append and fa_paged_read one; fa_packed_plan, fa_fwd_packed and
- * fa_rotate one;
+ * fa_rotate one, fa_bwd_packed three;
  * fa_fwd_paged two (the forward, then the join of segments that several CTAs
  * shared).
  */
