@@ -11,6 +11,7 @@ this module raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import math
@@ -127,7 +128,7 @@ def _load() -> ctypes.CDLL:
     lib.fa_fwd_paged_workspace_bytes.restype = sz
     lib.fa_fwd_paged.argtypes = [cache, vp, ll, ll, vp, vp, vp, i, i, i, f, i, i, vp, sz, vp]
     lib.fa_fwd_paged.restype = i
-    rows = ctypes.POINTER(Rows)
+    rows = vp  # of an fa_rows: byref(Rows), or an address (_RowBlock)
     lib.fa_packed_plan_bytes.argtypes = [i, i]
     lib.fa_packed_plan_bytes.restype = sz
     lib.fa_packed_plan.argtypes = [vp, i, i, i, vp, sz, vp]
@@ -478,8 +479,8 @@ def fa_packed_plan(cu_seqlens, sequences, rows, causal, plan, stream=None) -> No
                               _stream(stream)), "fa_packed_plan")
 
 
-def fa_fwd_packed(plan, sequences, rows, q: Rows, k: Rows, v: Rows, o: Rows, lse, H, Hkv, d, scale,
-                  stream=None) -> None:
+def fa_fwd_packed(plan, sequences, rows, q, k, v, o, lse, H, Hkv, d, scale, stream=None) -> None:
+    """q, k, v, o: an fa_rows each, as byref(Rows(...)) or its address (None: null)."""
     _check(lib.fa_fwd_packed(_ptr(plan), sequences, rows, q, k, v, o, _ptr(lse), H, Hkv, d, float(scale),
                              _stream(stream)), "fa_fwd_packed")
 
@@ -488,15 +489,17 @@ def fa_bwd_packed_workspace_bytes(sequences: int, rows: int, H: int, Hkv: int, d
     return int(lib.fa_bwd_packed_workspace_bytes(sequences, rows, H, Hkv, d))
 
 
-def fa_bwd_packed(plan, sequences, rows, q: Rows, k: Rows, v: Rows, o: Rows, lse, dout: Rows, dq: Rows,
-                  dk: Rows, dv: Rows, H, Hkv, d, scale, workspace, stream=None) -> None:
+def fa_bwd_packed(plan, sequences, rows, q, k, v, o, lse, dout, dq, dk, dv, H, Hkv, d, scale, workspace,
+                  stream=None) -> None:
+    """Row tensors as fa_fwd_packed."""
     ws_ptr, ws_bytes = _workspace(workspace, plan.device)
     _check(lib.fa_bwd_packed(_ptr(plan), sequences, rows, q, k, v, o, _ptr(lse), dout, dq, dk, dv, H, Hkv, d,
                              float(scale), ws_ptr, ws_bytes, _stream(stream)), "fa_bwd_packed")
 
 
-def fa_rotate(q: Rows, q_out: Rows, H, k: Rows, k_out: Rows, Hkv, positions, rows, d, rope, rope_len, rot,
-              interleaved, backward, stream=None) -> None:
+def fa_rotate(q, q_out, H, k, k_out, Hkv, positions, rows, d, rope, rope_len, rot, interleaved, backward,
+              stream=None) -> None:
+    """Row tensors as fa_fwd_packed."""
     _check(lib.fa_rotate(q, q_out, H, k, k_out, Hkv, _ptr(positions), rows, d, _ptr(rope), rope_len, rot,
                          int(bool(interleaved)), int(bool(backward)), _stream(stream)), "fa_rotate")
 
@@ -792,22 +795,38 @@ def packed_plan(cu_seqlens, rows: int, causal: bool = True, out: PackedPlan | No
     return out
 
 
-def _packed_rows(t, name, rows, heads, d, device) -> Rows:
-    """The row tensor t [rows, heads, d]."""
-    n, row, head = _rows(t, name, heads, d, device, rows)
-    return Rows(t.data_ptr(), row, head)
+def _row_block(rows, d, device, *tensors):
+    """The row tensors (tensor, name, heads) as consecutive fa_rows: their memory, to be kept until the
+    call has returned, and its address."""
+    index = device.index
+    block = array.array("q")
+    for t, name, heads in tensors:
+        if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == (rows, heads, d)
+                and t.get_device() == index):
+            row, head, one = t.stride()
+            if one == 1:
+                block.extend((t.data_ptr(), row, head))
+                continue
+        _, row, head = _rows(t, name, heads, d, device, rows)  # raises, but for empty tensors
+        block.extend((t.data_ptr(), row, head))
+    return block, block.buffer_info()[0]
+
+
+_ROWS = ctypes.sizeof(Rows)
 
 
 def _packed_heads(q, k, plan):
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    if not isinstance(plan, PackedPlan):
+        raise ValueError("plan must be a PackedPlan (packed_plan)")
+    dev = _current_device(q, "q")
+    if q.dim() != 3:
         raise ValueError("expected q [rows, H, d]")
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k [rows, Hkv, d]")
-    if not isinstance(plan, PackedPlan):
-        raise ValueError("plan must be a PackedPlan (packed_plan)")
-    if plan.plan.device != _current_device(q, "q"):
-        raise ValueError(f"plan is on {plan.plan.device}, expected {q.device}")
-    return plan.rows, q.shape[1], k.shape[1], q.shape[2]
+    if plan.plan.get_device() != dev.index:
+        raise ValueError(f"plan is on {plan.plan.device}, expected {dev}")
+    _, H, d = q.shape
+    return dev, plan.rows, H, k.shape[1], d
 
 
 def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=None, stream=None):
@@ -815,67 +834,78 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
     [rows, H, d], k and v [rows, Hkv, d] (H a multiple of Hkv; row and head strides
     that are multiples of 8) -> (o [rows, H, d], lse [rows, H]).  out: where o is
     written, strides as q.  Padding rows of the results are not written."""
-    rows, H, Hkv, d = _packed_heads(q, k, plan)
-    dev = q.device
-    shapes = ((rows, H), torch.float32), ((rows, H, d), torch.bfloat16)
+    dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
+    lse, = _empty(stream, dev, ((rows, H), torch.float32))
     if out is None:
-        lse, out = _empty(stream, dev, *shapes)
-    else:
-        lse, = _empty(stream, dev, shapes[0])
-    fa_fwd_packed(plan.plan, plan.sequences, rows, _packed_rows(q, "q", rows, H, d, dev),
-                  _packed_rows(k, "k", rows, Hkv, d, dev), _packed_rows(v, "v", rows, Hkv, d, dev),
-                  _packed_rows(out, "out", rows, H, d, dev), lse, H, Hkv, d,
+        out, = _empty(stream, dev, ((rows, H, d), torch.bfloat16))
+    keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (out, "out", H))
+    fa_fwd_packed(plan.plan, plan.sequences, rows, at, at + _ROWS, at + 2 * _ROWS, at + 3 * _ROWS, lse, H, Hkv, d,
                   default_scale(d) if scale is None else scale, stream)
     return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _packed_workspace_bytes(sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
+    return max(fa_bwd_packed_workspace_bytes(sequences, rows, H, Hkv, d), 1)
 
 
 def packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float | None = None, out=None,
                     workspace=None, stream=None):
     """Gradients (dq, dk, dv) of packed_forward, shaped as q, k and v; dk and dv are
     summed over the query heads that share a key head.  out: (dq, dk, dv) to write
-    to, strides as q (parts of a fused projection's gradient, say).  Padding rows of the results are
-    not written."""
-    rows, H, Hkv, d = _packed_heads(q, k, plan)
-    dev = q.device
+    to, strides as q (parts of a fused projection's gradient, say).  Padding rows of
+    the results are not written."""
+    dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
     if out is None:
-        out = _empty(stream, dev, *[((rows, h, d), torch.bfloat16) for h in (H, Hkv, Hkv)])
+        shared = (rows, Hkv, d), torch.bfloat16
+        out = _empty(stream, dev, ((rows, H, d), torch.bfloat16), shared, shared)
     dq, dk, dv = out
     if workspace is None:
-        n = fa_bwd_packed_workspace_bytes(plan.sequences, rows, H, Hkv, d)
-        workspace, = _empty(stream, dev, (max(n, 1), torch.uint8))
+        workspace, = _empty(stream, dev, (_packed_workspace_bytes(plan.sequences, rows, H, Hkv, d), torch.uint8))
     _check_tensor(lse, "lse", torch.float32, (rows, H), dev)
-    of_q = [_packed_rows(t, name, rows, H, d, dev) for t, name in ((q, "q"), (o, "o"), (dout, "dout"), (dq, "dq"))]
-    of_k = [_packed_rows(t, name, rows, Hkv, d, dev) for t, name in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv"))]
-    fa_bwd_packed(plan.plan, plan.sequences, rows, of_q[0], of_k[0], of_k[1], of_q[1], lse, of_q[2], of_q[3], of_k[2],
-                  of_k[3], H, Hkv, d, default_scale(d) if scale is None else scale, workspace, stream)
+    keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (o, "o", H), (dout, "dout", H),
+                          (dq, "dq", H), (dk, "dk", Hkv), (dv, "dv", Hkv))
+    q, k, v, o, dout, gq, gk, gv = range(at, at + 8 * _ROWS, _ROWS)
+    fa_bwd_packed(plan.plan, plan.sequences, rows, q, k, v, o, lse, dout, gq, gk, gv, H, Hkv, d,
+                  default_scale(d) if scale is None else scale, workspace, stream)
     return dq, dk, dv
 
 
 def rotate(q, k, positions, rope, interleaved: bool = False, backward: bool = False, out=None, stream=None):
     """q [rows, H, d] and k [rows, Hkv, d] (either may be None) rotated by their rows'
-    positions, int32 [rows] (a plan's `positions`, or any), with the table `rope` [length, rot]
-    (see rope_table): (q', k').  backward: the transpose, which takes the gradients
-    of q' and k' to those of q and k.  out: (q', k') to write to; each may be q or k
-    itself.  Rows of negative position are not written."""
+    positions, int32 [rows] (a plan's `positions`, or any), with the table `rope`
+    [length, rot] (see rope_table): (q', k').  backward: the transpose, which takes
+    the gradients of q' and k' to those of q and k.  out: (q', k') to write to; each
+    may be q or k itself.  Rows of negative position are not written."""
     some = k if q is None else q
-    if not isinstance(some, torch.Tensor) or some.dim() != 3:
-        raise ValueError("expected q [rows, H, d] or k [rows, Hkv, d]")
     dev = _current_device(some, "k" if q is None else "q")
+    if some.dim() != 3:
+        raise ValueError("expected q [rows, H, d] and k [rows, Hkv, d]")
     rows, _, d = some.shape
+    H = 0 if q is None else q.shape[1]
+    if k is None:
+        Hkv = 0
+    else:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("expected k [rows, Hkv, d]")
+        Hkv = k.shape[1]
     _check_tensor(positions, "positions", torch.int32, (rows,), dev)
     if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
         raise ValueError("rope must be [length, rot]")
     rope_len, rot = rope.shape
     _check_tensor(rope, "rope", torch.float32, (rope_len, rot), dev)
-    heads = [0 if x is None else x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 3 else None for x in (q, k)]
     if out is None:
-        new = iter(_empty(stream, dev, *[((rows, h, d), torch.bfloat16) for x, h in zip((q, k), heads) if x is not None]))
-        out = tuple(None if x is None else next(new) for x in (q, k))
-    args = []
-    for x, y, h, name in zip((q, k), out, heads, "qk"):
-        if (x is None) != (y is None):
-            raise ValueError(f"{name} and its place in out must both be given")
-        args += [None, None, 0] if x is None or h == 0 else [
-            _packed_rows(x, name, rows, h, d, dev), _packed_rows(y, f"out ({name})", rows, h, d, dev), h]
-    fa_rotate(*args, positions, rows, d, rope, rope_len, rot, interleaved, backward, stream)
-    return out
+        q2 = None if q is None else _empty(stream, dev, ((rows, H, d), torch.bfloat16))[0]
+        k2 = None if k is None else _empty(stream, dev, ((rows, Hkv, d), torch.bfloat16))[0]
+    else:
+        q2, k2 = out
+        if (q is None) != (q2 is None) or (k is None) != (k2 is None):
+            raise ValueError("out must hold a tensor for each of q and k that is given, and None otherwise")
+    given = () if q is None else ((q, "q", H), (q2, "out (q)", H))
+    if k is not None:
+        given += (k, "k", Hkv), (k2, "out (k)", Hkv)
+    keep, at = _row_block(rows, d, dev, *given)
+    of_k = at if q is None else at + 2 * _ROWS  # (not read where Hkv is 0, nor q's where H is)
+    fa_rotate(at, at + _ROWS, H, of_k, of_k + _ROWS, Hkv, positions, rows, d, rope, rope_len, rot, interleaved,
+              backward, stream)
+    return q2, k2
