@@ -981,13 +981,38 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+namespace {
+
+// How many parts the backward cuts each item (key tile of a key head) into:
+// enough for four items to an SM, so that a causal batch of few items, which differ
+// by their place, fills the SMs evenly, but two query tiles each at least, by the
+// mean length.  At d = 64 no part may be without a query tile (its kernel's
+// ring), so there are as many as heads in a group at most.  The parts' dK and dV are joined by the
+// kernel after the main one.  XXX us, against YYY unsplit.
+int packed_parts(int sequences, int rows, int H, int Hkv, int d) {
+  const int sms = sm_count();
+  const long long items = packed_tiles(rows, sequences, kBlockN) * Hkv;
+  const long long tiles = (static_cast<long long>(rows) / sequences + kBlockM - 1) / kBlockM;
+  const long long by_sms = 4LL * (sms > 0 ? sms : 152) / items;  // (without a device: a size for GB300)
+  const long long by_work = (tiles + 1) / 2 * (H / Hkv) / 2;
+  const long long most = d == 64 && H / Hkv < 8 ? H / Hkv : 8;
+  long long n = by_sms < by_work ? by_sms : by_work;
+  if (n > most) n = most;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+}  // namespace
+
 size_t fa_bwd_packed_workspace_bytes(int sequences, int rows, int H, int Hkv, int d) {
   bool empty = false;
   // (any aligned address stands for the plan)
   if (check_packed(reinterpret_cast<const void*>(kWsAlign), sequences, rows, H, Hkv, d, 1.0f, &empty) != FA_OK || empty)
     return 0;
   const size_t n = static_cast<size_t>(rows) * H;
-  return n > 0x7fffffffu ? 0 : 2 * round_up(n * sizeof(float)) + round_up(n * d * sizeof(float));
+  if (n > 0x7fffffffu) return 0;
+  const int parts = packed_parts(sequences, rows, H, Hkv, d);
+  return kWsAlign + 2 * round_up(n * sizeof(float)) + round_up(n * d * sizeof(float)) +
+         (parts > 1 ? round_up(static_cast<size_t>(parts) * 2 * Hkv * rows * d * sizeof(float)) : 0);
 }
 
 int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k, const fa_rows* v,
@@ -1007,7 +1032,7 @@ int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   if (!workspace || workspace_bytes < fa_bwd_packed_workspace_bytes(sequences, rows, H, Hkv, d) ||
       (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0)
     return FA_ERR_WORKSPACE;
-  char* w = static_cast<char*>(workspace);
+  char* w = static_cast<char*>(workspace) + kWsAlign;  // behind the counter
   float* dsum = reinterpret_cast<float*>(w);
   float* lse_heads = reinterpret_cast<float*>(w + round_up(n * sizeof(float)));
   float* dq_acc = reinterpret_cast<float*>(w + 2 * round_up(n * sizeof(float)));
@@ -1040,6 +1065,10 @@ int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   p.plan = plan;
   p.sequences = sequences;
   p.div_kv = FastDiv(static_cast<uint32_t>(Hkv));
+  p.split_parts = packed_parts(sequences, rows, H, Hkv, d);
+  p.div_parts = FastDiv(static_cast<uint32_t>(p.split_parts));
+  p.counter = static_cast<unsigned int*>(workspace);
+  p.tile_part = dq_acc + round_up(n * d * sizeof(float)) / sizeof(float);
 
   PackedBwdParams r = {};
   r.plan = plan;
@@ -1061,6 +1090,17 @@ int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   r.dq_head = head_stride(*dq, H);
   r.scale = scale;
   r.div_h = FastDiv(static_cast<uint32_t>(H));
+  r.counter = p.counter;
+  r.parts = p.split_parts;
+  r.Hkv = Hkv;
+  r.part = p.tile_part;
+  r.dk = static_cast<__nv_bfloat16*>(dk->data);
+  r.dv = static_cast<__nv_bfloat16*>(dv->data);
+  r.dk_row = p.dk_row;
+  r.dk_head = p.dk_head;
+  r.dv_row = p.dv_row;
+  r.dv_head = p.dv_head;
+  r.div_kv = p.div_kv;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_packed_pre(r, d, s) != cudaSuccess) return FA_ERR_CUDA;
   if (timing_record(1, true, s) != cudaSuccess) return FA_ERR_CUDA;

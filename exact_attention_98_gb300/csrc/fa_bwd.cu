@@ -282,7 +282,9 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   PackedItem item{0, p.N, 0, 0, p.causal != 0};
   if constexpr (kPacked) {
     grid_dependency_wait();
-    if (!packed_item(p, blk, item)) return;
+    const int i = packed_block(p, blk, part);
+    if (i >= packed_items(p)) return;
+    item = packed_item_at(p, i);
   }
   const int row0 = kPacked ? item.start : 0;  // of the sequence
   const int len = kPacked ? item.len : p.N;
@@ -295,7 +297,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
   const int i_last = kWindow ? min(n_qtiles - 1, (k0 + kBlockN - 2 + p.window) / kBlockM) : n_qtiles - 1;
   int n_iter = (kGrouped ? p.group : 1) * (i_last - i_first + 1);
   int it0 = 0;  // the part's first
-  if constexpr (kWindow) {
+  if constexpr (kGrouped) {
     if (part >= 0) {
       const int q = p.div_parts.div(n_iter), r = n_iter - q * p.split_parts;
       it0 = q * part + min(part, r);
@@ -966,7 +968,10 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
           }
         }
         if constexpr (kPacked) {
-          if (rows && row_valid) {
+          if (part >= 0) {
+            if (row_valid)
+              packed_part_row(packed_part(p, part, wg == 0, bh, row0 + kpos, D) + h * 64, r, n_iter > 0);
+          } else if (rows && row_valid) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(wg == 0 ? p.dv : p.dk) +
                                  (row0 + kpos) * (wg == 0 ? p.dv_row : p.dk_row) +
                                  bh * (wg == 0 ? p.dv_head : p.dk_head) + h * 64;
@@ -1059,6 +1064,7 @@ cudaError_t launch_bwd_d(const BwdParams& p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   long long blocks = static_cast<long long>(p.n_kblk) * p.BH;
   if (kWindow) blocks = p.split_from + (blocks - p.split_from) * p.split_parts;
+  if (kPacked) blocks *= p.split_parts;
   err = launch_dependent(kernel, dim3(static_cast<unsigned int>(blocks)), dim3(C::kThreads),
                          C::kSmemBytes, stream, p);
   if (err != cudaSuccess) return err;

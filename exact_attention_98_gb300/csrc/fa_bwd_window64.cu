@@ -93,10 +93,16 @@ struct WinCfg {
   // to clear rows of have landed
   static constexpr int kBarTrimKV = kBarKVFree + 1;
   static constexpr int kBarTrim = kBarTrimKV + 2;
-  static constexpr int kNumBars = kPacked ? kBarTrim + kStages : kBarKVFree + 1;
+  // packed: the ring of items that the producer hands to the other warps
+  static constexpr int kRing = 4;
+  static constexpr int kBarRingFull = kBarTrim + kStages;
+  static constexpr int kBarRingEmpty = kBarRingFull + kRing;
+  static constexpr int kRingReaders = kComputeWarps + 4 + 3;  // compute, drain, KV, MMA, trim
+  static constexpr int kNumBars = kPacked ? kBarRingEmpty + kRing : kBarKVFree + 1;
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kAbortOff = kTmemSlotOff + 4;
-  static constexpr int kSmemBytes = kAbortOff + 4 + 1024;
+  static constexpr int kRingOff = (kAbortOff + 4 + 15) / 16 * 16;
+  static constexpr int kSmemBytes = (kPacked ? kRingOff + kRing * 48 : kAbortOff + 4) + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;
@@ -127,19 +133,22 @@ enum : unsigned int {
   kSiteAccFree = 0x21D,
   kSiteKVFree = 0x21E,
   kSiteTrim = 0x21F,
+  kSiteRingFull = 0x220,
+  kSiteRingEmpty = 0x221,
 };
 
-// Block `blk` of the list of items: a key tile of a key head (from split_from
-// on a part of its query tiles) and its query tiles i_first..i_last, head by head.
+// Block `blk` of the list of items: a key tile of a key head (or a part of its
+// query tiles) and its query tiles i_first..i_last, head by head.
 template <bool kPacked>
-struct KeyItem {
-  int bh, kt, k0;  // key head, key tile, its first key
-  int start, len;  // packed: rows of the sequence
-  bool causal;
+struct alignas(16) KeyItem {
+  int bh, k0;      // key head, first key
+  int diag;        // the query tile that the diagonal crosses (packed, not causal: -1)
   int part;        // of a split item, else -1
   int i_first, i_last;
   int n_iter;      // query tiles (all heads')
   int i, head;     // the first: tile and query head
+  int start, len;  // packed: rows of the sequence
+  int unused;
 
   __device__ __forceinline__ void next() {
     if (++i > i_last) {
@@ -156,34 +165,30 @@ struct KeyItem {
 template <bool kPacked>
 __device__ __forceinline__ KeyItem<kPacked> key_item(const BwdParams& p, int blk) {
   KeyItem<kPacked> t;
-  t.part = -1;
   if constexpr (kPacked) {
-    const PackedItem item = packed_item_at(p, blk);
+    const PackedItem item = packed_item_at(p, packed_block(p, blk, t.part));
     t.start = item.start;
     t.len = item.len;
-    t.causal = item.causal;
     t.bh = item.kv;
-    t.kt = item.kt;
-    t.k0 = t.kt * kBlockN;
-    t.i_first = t.causal ? t.kt : 0;
+    t.k0 = item.kt * kBlockN;
+    t.diag = item.causal ? item.kt : -1;
+    t.i_first = item.causal ? item.kt : 0;
     t.i_last = (t.len + kBlockM - 1) / kBlockM - 1;
-    t.n_iter = p.group * (t.i_last - t.i_first + 1);
-    t.head = t.bh * p.group;
-    t.i = t.i_first;
-    return t;
+  } else {
+    t.part = -1;
+    int item = blk;
+    if (blk >= p.split_from) {
+      const int i = p.div_parts.div(blk - p.split_from);
+      item = p.split_from + i;
+      t.part = blk - p.split_from - i * p.split_parts;
+    }
+    t.bh = p.div_kblk.div(item);
+    t.diag = item - t.bh * p.n_kblk;
+    t.k0 = t.diag * kBlockN;
+    t.i_first = t.diag;
+    // (window <= N <= 2^30, so the sum is an int)
+    t.i_last = min((p.N + kBlockM - 1) / kBlockM - 1, (t.k0 + kBlockN - 2 + p.window) / kBlockM);
   }
-  int item = blk;
-  if (blk >= p.split_from) {
-    const int i = p.div_parts.div(blk - p.split_from);
-    item = p.split_from + i;
-    t.part = blk - p.split_from - i * p.split_parts;
-  }
-  t.bh = p.div_kblk.div(item);
-  t.kt = item - t.bh * p.n_kblk;
-  t.k0 = t.kt * kBlockN;
-  t.i_first = t.kt;
-  // (window <= N <= 2^30, so the sum is an int)
-  t.i_last = min((p.N + kBlockM - 1) / kBlockM - 1, (t.k0 + kBlockN - 2 + p.window) / kBlockM);
   const int per = t.i_last - t.i_first + 1;
   t.n_iter = p.group * per;
   int start = 0;
@@ -204,17 +209,21 @@ __device__ __forceinline__ KeyItem<kPacked> key_item(const BwdParams& p, int blk
 
 // The next block from `blk` on, in steps of `stride`, that has query tiles (a
 // part of a split item may have none); false if there is none.
-template <bool kPacked>
-__device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stride, int total, KeyItem<kPacked>& t) {
+__device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stride, int total, KeyItem<false>& t) {
   for (; blk < total; blk += stride) {
-    t = key_item<kPacked>(p, blk);
+    t = key_item<false>(p, blk);
     if (t.n_iter > 0) return true;
   }
   return false;
 }
 
 // kPacked: items come from a plan of packed sequences; the tiles' rows are
-// a sequence's, the masks the diagonal (if causal) and the sequence's end.
+// a sequence's, the masks the diagonal (if causal) and the sequence's end.  Items
+// differ in their work by far, so a CTA takes its next one when it gets to it,
+// from a counter: the producer, which is first to need it, takes it, looks it up in
+// the plan and hands it to the other warps through a ring (dealt out in turn, as
+// for windows, the CTAs' sums differ by 28% for XXX; looked up by every warp, the
+// code grew from 74 to 97 KB, and the kernel from 211 us to 225).
 template <bool kPacked>
 __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     fa_bwd_window64_kernel(const __grid_constant__ BwdParams p) {
@@ -233,11 +242,29 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
   int total = 0;
   if constexpr (kPacked) {
     grid_dependency_wait();  // the plan is earlier work of the stream
-    total = packed_items(p);
+    total = packed_items(p) * p.split_parts;
   } else {
     total = p.split_from + (p.n_kblk * p.BH - p.split_from) * p.split_parts;
   }
   const int stride = static_cast<int>(gridDim.x);
+  KeyItem* ring = reinterpret_cast<KeyItem*>(smem + C::kRingOff);
+  static_assert(sizeof(KeyItem) == 48, "ring entries");
+  int taken = 0;  // packed: entries of the ring that this warp has read (the producer: written)
+  // A warp's next item that has query tiles, `blk` being the next block to look at;
+  // packed: the ring's next, which has some unless it is the end.
+  auto advance = [&](int& blk, KeyItem& t) {
+    if constexpr (kPacked) {
+      const int slot = taken % C::kRing;
+      if (!mbar_wait_short_warp(bar(C::kBarRingFull + slot), (taken / C::kRing) & 1, ctl, kSiteRingFull)) return false;
+      t = ring[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kBarRingEmpty + slot));
+      ++taken;
+      return t.n_iter > 0;
+    } else {
+      return next_item(p, blk, stride, total, t);
+    }
+  };
 
   // One arrival for the warp's lanes, each of which has made its own fence: lanes
   // that all arrive take turns at the barrier's word, and shared memory is what
@@ -284,13 +311,20 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     mbar_init(bar(C::kBarKVFree), 2);
     if constexpr (kPacked)
       for (int b = 0; b < 2 + C::kStages; ++b) mbar_init(bar(C::kBarTrimKV + b), 1);
+    if constexpr (kPacked)
+      for (int b = 0; b < C::kRing; ++b) {
+        mbar_init(bar(C::kBarRingFull + b), 1);
+        mbar_init(bar(C::kBarRingEmpty + b), C::kRingReaders);
+      }
     fence_mbar_init();
     grid_dependency_wait();
-    KeyItem t;
-    int blk = blockIdx.x;
-    if (next_item(p, blk, stride, total, t)) {
-      load_kv(0, t);
-      load_tile(0, t);
+    if constexpr (!kPacked) {
+      KeyItem t;
+      int blk = blockIdx.x;
+      if (advance(blk, t)) {
+        load_kv(0, t);
+        load_tile(0, t);
+      }
     }
   }
   if (warp == C::kMmaWarp) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -314,8 +348,30 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
       };
       int blk = blockIdx.x;
       KeyItem t;
-      for (bool more = next_item(p, blk, stride, total, t); ok && more;) {
+      // packed: block blk's item, to the ring; false behind the last (its entry
+      // has no query tiles)
+      auto hand_out = [&] {
+        const int slot = taken % C::kRing;
+        if (taken >= C::kRing && !wait(C::kBarRingEmpty + slot, (taken / C::kRing - 1) & 1, kSiteRingEmpty)) return false;
+        ++taken;
+        t.n_iter = 0;
+        if (blk < total) t = key_item<kPacked>(p, blk);
+        if (lane == 0) {
+          ring[slot] = t;
+          mbar_arrive(bar(C::kBarRingFull + slot));
+        }
+        return blk < total;
+      };
+      unsigned int following = 0;
+      auto first = [&] {
+        if constexpr (kPacked) return hand_out();
+        else return advance(blk, t);
+      };
+      for (bool more = first(); ok && more;) {
         for (int it = 0; it < t.n_iter; ++it) {
+          // packed: the next item is taken as late as its copies can still be in time,
+          // three tiles ahead
+          if (kPacked && lane == 0 && it == max(0, t.n_iter - C::kStages)) following = atomicAdd(p.counter, 1u);
           const int s = n % C::kStages;
           // fp32 rows -LSE_q log2 e and -D_q; rows past N get -inf (P = 0 there)
           // and D = 0.  Read before the wait for the stage.
@@ -329,7 +385,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
             nd[r4] = (q < t.rows(p)) ? -p.dsum[head_row + q] : 0.0f;
           }
           if (n >= C::kStages && !wait(C::kBarStEmpty + s, (n / C::kStages - 1) & 1, kSiteStEmpty)) break;
-          if (lane == 0 && n > 0) load_tile(s, t);  // (the very first is on its way)
+          if (lane == 0 && (kPacked || n > 0)) load_tile(s, t);  // (windows: the very first is on its way)
           float* row_l = reinterpret_cast<float*>(smem + C::kRowsOff + 2 * s * C::kRowBytes);
 #pragma unroll
           for (int r4 = 0; r4 < 4; ++r4) {
@@ -341,8 +397,13 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
           ++n;
           t.next();
         }
-        blk += stride;
-        more = ok && next_item(p, blk, stride, total, t);
+        if constexpr (kPacked) {
+          blk = stride + static_cast<int>(__shfl_sync(0xffffffffu, following, 0));
+          more = ok && hand_out();
+        } else {
+          blk += stride;
+          more = ok && advance(blk, t);
+        }
       }
       // Let every copy this CTA started land before shared memory is released
       // (only on the give-up path, where a barrier may lack the loader's own
@@ -351,24 +412,35 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         for (int k = max(0, n - C::kStages); k < n; ++k)
           mbar_wait_drain(bar(C::kBarStFull + k % C::kStages), (k / C::kStages) & 1);
       }
-    } else if (warp == C::kKVWarp && lane == 0) {
+    } else if (warp == C::kKVWarp && (kPacked || lane == 0)) {
       // ----------------------------------------------------------- K and V
       bool ok = true;
       int blk = blockIdx.x;
       KeyItem t;
-      bool more = next_item(p, blk, stride, total, t);  // (its copies are on their way)
-      int m = 1;
-      while (more) {
-        blk += stride;
-        more = next_item(p, blk, stride, total, t);
-        if (!more) break;
-        // the buffers are free once dV and dK of the item before the last have
-        // left them
-        if (m > 1 && !(ok = mbar_wait_short(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
-        load_kv(m++, t);
+      if constexpr (kPacked) {
+        int m = 0;
+        for (; advance(blk, t); ++m) {
+          // (as below)
+          if (m > 1 && !(ok = mbar_wait_short_warp(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
+          if (lane == 0) load_kv(m, t);
+        }
+        if (!ok && lane == 0)
+          for (int k = max(0, m - 2); k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
+      } else {
+        bool more = advance(blk, t);  // (its copies are on their way)
+        int m = 1;
+        while (more) {
+          blk += stride;
+          more = advance(blk, t);
+          if (!more) break;
+          // the buffers are free once dV and dK of the item before the last have
+          // left them
+          if (m > 1 && !(ok = mbar_wait_short(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
+          load_kv(m++, t);
+        }
+        if (!ok)
+          for (int k = m - 2; k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
       }
-      if (!ok)
-        for (int k = m - 2; k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
     } else if (kPacked && warp == C::kTrimWarp) {
       // ----------------------------------------------------------- trim
       // Rows past the sequence's end are another's, or padding, whatever they
@@ -394,7 +466,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         bool ok = true;
         int blk = blockIdx.x;
         KeyItem t;
-        for (; ok && next_item(p, blk, stride, total, t); blk += stride, ++m) {
+        for (; ok && advance(blk, t); ++m) {
           if (t.k0 + kBlockN > t.len) {
             if (!(ok = wait(C::kBarTrimKV + (m & 1)))) break;
             clear(C::kKOff + (m & 1) * C::kTileBytes, t.len - t.k0);
@@ -445,12 +517,13 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
       // the first item's first S^T and dP^T alone.
       int m = 0, blk = blockIdx.x;
       KeyItem t;
-      bool more = next_item(p, blk, stride, total, t);
-      int left = 0, next_left = more ? t.n_iter : 0;  // tiles of the item from this step's on; of the next item
+      int left = 0;                                    // tiles of the item from this step's on
+      int next_left = !kPacked && advance(blk, t) ? t.n_iter : 0;  // of the next item (packed: looked up in time)
       bool first = false;                             // this step's tile is its item's first
       bool ok = true;
       for (int n = -1;; ++n) {
         const bool last = left <= 1;  // (of the item, or step -1)
+        if (kPacked && last) next_left = advance(blk, t) ? t.n_iter : 0;
         const bool next = !last || next_left > 0;
         if (n < 0 && !next) break;
         const int s = n % C::kStages;
@@ -496,8 +569,10 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         --left;
         if (last) {
           left = next_left;
-          blk += stride;
-          next_left = next_item(p, blk, stride, total, t) ? t.n_iter : 0;
+          if constexpr (!kPacked) {
+            blk += stride;
+            next_left = advance(blk, t) ? t.n_iter : 0;
+          }
         }
       }
       if (!ok) {
@@ -519,7 +594,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     bool ok = true;
     int blk = blockIdx.x;
     KeyItem t;
-    for (; ok && next_item(p, blk, stride, total, t); blk += stride) {
+    for (; ok && advance(blk, t); blk += stride) {
       for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
         ok = mbar_wait_short(bar(C::kBarDQFull), n & 1, ctl, kSiteDQFull);
         ok = __all_sync(0xffffffffu, ok);
@@ -591,8 +666,14 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     int n = 0, m = 0;
     bool ok = true;
     KeyItem t_next;
-    if (static_cast<int>(blockIdx.x) < total) t_next = key_item<kPacked>(p, blockIdx.x);
-    for (int blk = blockIdx.x; ok && blk < total; blk += stride) {
+    // (windows: items without query tiles, too)
+    auto look = [&](int blk) {
+      if constexpr (kPacked) return advance(blk, t_next);
+      if (blk < total) t_next = key_item<kPacked>(p, blk);
+      return blk < total;
+    };
+    bool more = look(blockIdx.x);
+    for (int blk = blockIdx.x; ok && more; blk += stride) {
       KeyItem t = t_next;
       const bool row_valid = t.k0 + kr < t.rows(p);
       const bool last_tile = t.k0 + kBlockN > t.rows(p);  // some key rows are past the last
@@ -600,8 +681,8 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         const int s = n % C::kStages;
         // the diagonal tile, those whose last rows are past some key's window,
         // and all of a key tile with rows past N
-        const bool edge = kPacked ? (t.causal && t.i == t.kt) || last_tile
-                                  : t.i == t.kt || (t.i - t.kt) * kBlockM + kBlockM - 1 >= p.window || last_tile;
+        const bool edge = kPacked ? t.i == t.diag || last_tile
+                                  : t.i == t.diag || (t.i - t.diag) * kBlockM + kBlockM - 1 >= p.window || last_tile;
         ok = mbar_wait_short(bar(C::kBarSFull), n & 1, ctl, kSiteSFull);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
@@ -636,8 +717,8 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
           }
         if (edge) {
           // the key sees the query columns [lo, lo + window) of the tile
-          // (packed: [lo, ...) if causal, all otherwise)
-          const int lo = kPacked && !t.causal ? 0 : (t.kt - t.i) * kBlockM + kr - wg * 64;
+          // (packed: [lo, ...), all where nothing is masked but the sequence's end)
+          const int lo = kPacked && t.i != t.diag ? 0 : (t.diag - t.i) * kBlockM + kr - wg * 64;
           const int hi = kPacked ? 64 : lo + p.window;
           auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
 #pragma unroll
@@ -701,7 +782,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(bar(C::kBarDSFull));
       }
-      if (blk + stride < total) t_next = key_item<kPacked>(p, blk + stride);
+      more = look(blk + stride);
 
       // The item's dV (warpgroup 0) and dK (warpgroup 1, times the softmax scale,
       // which dS left out): a thread holds its key row.
@@ -709,11 +790,11 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
       // of a part's (zeros if it has no query tile), and the first tokens', which
       // also get the queries whose windows have left them.
       float* raw = nullptr;
-      if (kPacked)
-        raw = nullptr;
-      else if (t.part >= 0)
+      if constexpr (kPacked) {
+        if (t.part >= 0 && row_valid) raw = packed_part(p, t.part, wg == 0, t.bh, t.start + t.k0 + kr, D);
+      } else if (t.part >= 0)
         raw = p.tile_part + ((static_cast<size_t>(blk - p.split_from) * 2 + (wg == 0 ? 1 : 0)) * kBlockN + kr) * D;
-      else if (p.sink_main != nullptr && t.kt == 0 && kr < p.sinks)
+      else if (p.sink_main != nullptr && t.k0 == 0 && kr < p.sinks)
         raw = p.sink_main + ((static_cast<size_t>(t.bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D;
       if (ok && t.n_iter > 0) {
         ok = mbar_wait_short(bar(C::kBarMmaDone), m & 1, ctl, kSiteMmaDone);
@@ -821,7 +902,7 @@ cudaError_t launch_bwd_window64(const BwdParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_bwd_packed64(const BwdParams& p, cudaStream_t stream) {
-  return launch<true>(p, p.n_kblk * p.BH, stream);
+  return launch<true>(p, p.n_kblk * p.BH * p.split_parts, stream);
 }
 
 }  // namespace fa

@@ -152,6 +152,8 @@ struct BwdParams {
   int sequences;
   long long dk_row, dk_head, dv_row, dv_head;  // strides in elements
   FastDiv div_kv;  // by BH
+  // (split_parts, div_parts, tile_part: every item is split, see packed_part)
+  unsigned int* counter;  // blocks that CTAs have taken (d = 64), zeroed before
 };
 
 // What the sliding-window backward does beside its main kernel (fa_window.cu):
@@ -354,6 +356,15 @@ struct PackedBwdParams {
   long long dq_row, dq_head;
   float scale;
   FastDiv div_h;      // by H
+  // parts > 1: dK and dV from the main kernel's parts (packed_part)
+  unsigned int* counter;  // zeroed
+  int parts;
+  int Hkv;
+  const float* part;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  long long dk_row, dk_head, dv_row, dv_head;
+  FastDiv div_kv;     // by Hkv
 };
 cudaError_t launch_packed_pre(const PackedBwdParams& p, int d, cudaStream_t stream);
 cudaError_t launch_packed_post(const PackedBwdParams& p, int d, cudaStream_t stream);

@@ -139,13 +139,13 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
     // a lane's own tiles where there are few, all lanes together on a long sequence's
     const int place = at + sum - n;
     if (n > 0 && n <= 8)
-      for (int t = 0; t < n; ++t) list[place + t] = make_int4(start, len, first + t, place);
+      for (int t = 0; t < n; ++t) list[place + t] = make_int4(start, len, first + t, 0);
     for (unsigned int left = __ballot_sync(0xffffffffu, n > 8); left != 0; left &= left - 1) {
       const int src = __ffs(left) - 1;
       const int s = __shfl_sync(0xffffffffu, start, src), ln = __shfl_sync(0xffffffffu, len, src);
       const int f = __shfl_sync(0xffffffffu, first, src), m = __shfl_sync(0xffffffffu, n, src);
       const int pl = __shfl_sync(0xffffffffu, place, src);
-      for (int t = lane; t < m; t += 32) list[pl + t] = make_int4(s, ln, f + t, pl);
+      for (int t = lane; t < m; t += 32) list[pl + t] = make_int4(s, ln, f + t, 0);
     }
     at += __shfl_sync(0xffffffffu, sum, 31);
   }
@@ -154,13 +154,15 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
 // Before the backward's main kernel: D = rowsum(dO * O) and LSE by heads, where the
 // main kernel reads a head's rows one after another, and the zeroed dQ
 // accumulator.  16 bytes of a row to a lane.  Rows of no sequence are left out.
-// After it: dQ = scale * accumulator -> bf16.  Both are bound by HBM.
+// After it: dQ = scale * accumulator -> bf16, and dK and dV from their parts, where the
+// main kernel's items are split, in order.  Both are bound by HBM.
 constexpr int kRowThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) fa_packed_pre_kernel(const __grid_constant__ PackedBwdParams p) {
   constexpr int kLanes = D / 8;
   grid_dependency_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0u;
   const PackedHead& head = *static_cast<const PackedHead*>(p.plan);
   if (!packed_fits(head, p.rows, p.sequences)) return;  // (the main kernel records it)
   const int col = static_cast<int>(threadIdx.x) % kLanes * 8;
@@ -233,6 +235,30 @@ __global__ void __launch_bounds__(kRowThreads) fa_packed_post_kernel(const __gri
         *reinterpret_cast<uint4*>(to[u]) =
             make_uint4(pack_bf16x2(a[u].x * p.scale, a[u].y * p.scale), pack_bf16x2(a[u].z * p.scale, a[u].w * p.scale),
                        pack_bf16x2(b[u].x * p.scale, b[u].y * p.scale), pack_bf16x2(b[u].z * p.scale, b[u].w * p.scale));
+  }
+  if (p.parts < 2) return;
+  const long long m = 2LL * (head.end - head.begin) * p.Hkv;
+  const size_t stride = 2 * static_cast<size_t>(p.Hkv) * p.rows * D;  // of a part
+  for (long long i = blockIdx.x * static_cast<long long>(kRows) + threadIdx.x / kLanes; i < m;
+       i += static_cast<long long>(gridDim.x) * kRows) {
+    const int dv = static_cast<int>(i & 1);
+    const uint32_t th = static_cast<uint32_t>(i >> 1), t = p.div_kv.div(th);
+    const long long row = head.begin + static_cast<long long>(t);
+    const int h = static_cast<int>(th - t * p.div_kv.d);
+    const float* from = p.part + ((static_cast<size_t>(dv) * p.Hkv + h) * p.rows + row) * D + col;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+    for (int k = 0; k < p.parts; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(from + k * stride);
+      const float4 y = *reinterpret_cast<const float4*>(from + k * stride + 4);
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    }
+    const float mul = dv ? 1.0f : p.scale;
+    __nv_bfloat16* to = dv ? p.dv + row * p.dv_row + h * p.dv_head : p.dk + row * p.dk_row + h * p.dk_head;
+    *reinterpret_cast<uint4*>(to + col) =
+        make_uint4(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul),
+                   pack_bf16x2(b.x * mul, b.y * mul), pack_bf16x2(b.z * mul, b.w * mul));
   }
 }
 

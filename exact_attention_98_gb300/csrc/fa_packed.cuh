@@ -4,11 +4,10 @@
 // cu[b+1]-1.  A plan is what the kernels need to know about them, made once from
 // cu by one kernel (fa_packed.cu) and used by every call on rows of the same
 // batch: a head, each row's position, and three lists of tiles.  A list's entry is
-//   {first row of the sequence, its length, the tile's index in it, w}
+//   {first row of the sequence, its length, the tile's index in it, 0}
 //   tiles      128-row tiles, those that see the most keys first
 //   blocks     256-row blocks in the same order
-//   seq_tiles  128-row tiles, sequence by sequence, those of most tiles first;
-//              w is the index in this list of the sequence's first
+//   seq_tiles  128-row tiles, sequence by sequence, those of most tiles first
 #pragma once
 
 #include "fa_device.cuh"
@@ -65,10 +64,15 @@ __device__ __forceinline__ bool packed_fits(const PackedHead& h, int rows, int s
   return h.magic == kPackedMagic && h.rows == rows && h.sequences == sequences;
 }
 
-// Work item of the backward: a key tile of a key head.  Item i belongs to the
-// sequence of entry i / Hkv of seq_tiles; within a sequence the heads come one
-// after another, the key tiles of each in order (causal: those of most work first), so
-// that CTAs that run at the same time add to the same rows of dQ.
+// Work item of the backward: a key tile of a key head, or (split_parts > 1) one
+// of as many parts of its query tiles.  The heads (and parts) of an entry of a
+// list follow one another.  The list is seq_tiles, so that CTAs that run at the
+// same time walk the same query tiles, whose Q, dO and dQ then pass through L2
+// once for all of them: with the heaviest key tiles of all sequences first, 131072
+// rows of 24 sequences (H = 16, Hkv = 4, d = 128, causal) took 8286 us instead of
+// 6170.  A causal batch of few tiles takes the heaviest first all the same: there
+// the last CTAs' idle time weighs more (16384 rows of 11 sequences: 325 us, not 338).
+constexpr int kFewTiles = 152;
 struct PackedItem {
   int start, len;  // rows of the sequence
   int kt;          // key tile
@@ -76,7 +80,7 @@ struct PackedItem {
   bool causal;
 };
 
-// Items of a backward call: 0 when the plan is not one for its rows (recorded).
+// Items of a backward call, without their parts: 0 when the plan is not one for its rows (recorded).
 __device__ __forceinline__ int packed_items(const BwdParams& p) {
   const PackedHead& h = *static_cast<const PackedHead*>(p.plan);
   if (!packed_fits(h, p.N, p.sequences)) {
@@ -89,20 +93,43 @@ __device__ __forceinline__ int packed_items(const BwdParams& p) {
 // Item i (< packed_items) of a backward call.
 __device__ __forceinline__ PackedItem packed_item_at(const BwdParams& p, int i) {
   const uint8_t* plan = static_cast<const uint8_t*>(p.plan);
-  const int4 e = reinterpret_cast<const int4*>(plan + packed_layout(p.N, p.sequences).seq_tiles)[p.div_kv.div(i)];
+  const PackedHead& h = *reinterpret_cast<const PackedHead*>(plan);
+  const PackedLayout l = packed_layout(p.N, p.sequences);
+  // in `tiles` the last tile of a sequence costs most; its first key tile does
+  const bool heaviest = h.causal != 0 && h.n_tiles <= kFewTiles;
+  const int entry = p.div_kv.div(i);
+  const int4 e = reinterpret_cast<const int4*>(plan + (heaviest ? l.tiles : l.seq_tiles))[entry];
   PackedItem it;
   it.start = e.x;
   it.len = e.y;
-  const int tiles = (e.y + kBlockN - 1) / kBlockN, at = i - e.w * p.BH;
-  it.kv = at / tiles;
-  it.kt = at - it.kv * tiles;
-  it.causal = reinterpret_cast<const PackedHead*>(plan)->causal != 0;
+  it.kv = i - entry * p.BH;
+  it.kt = heaviest ? (e.y - 1) / kBlockN - e.z : e.z;
+  it.causal = h.causal != 0;
   return it;
 }
-__device__ __forceinline__ bool packed_item(const BwdParams& p, int i, PackedItem& it) {
-  if (i >= packed_items(p)) return false;
-  it = packed_item_at(p, i);
-  return true;
+
+// The item of block blk, and its part (-1: not split).
+__device__ __forceinline__ int packed_block(const BwdParams& p, int blk, int& part) {
+  part = -1;
+  if (p.split_parts == 1) return blk;
+  const int i = p.div_parts.div(blk);
+  part = blk - i * p.split_parts;
+  return i;
+}
+
+// fp32 dK or dV (unscaled) of a part: [part][dK, dV][key heads][rows][d].
+__device__ __forceinline__ float* packed_part(const BwdParams& p, int part, bool dv, int kv, int row, int d) {
+  return p.tile_part + (((static_cast<size_t>(part) * 2 + (dv ? 1 : 0)) * p.BH + kv) * p.N + row) * d;
+}
+// 64 columns of such a row; `some`: the part has query tiles, else they are zeros.
+__device__ __forceinline__ void packed_part_row(float* to, const uint32_t (&r)[2][32], bool some) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t* x = &r[c >> 3][(c & 7) * 4];
+    reinterpret_cast<float4*>(to)[c] =
+        some ? make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3]))
+             : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 }
 
 }  // namespace fa

@@ -386,8 +386,10 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
  *   o, lse     : in,  the forward's outputs
  *   dout, dq   : in, out: row tensors of H heads; dk, dv: out, of Hkv heads
  *   workspace  : fa_bwd_packed_workspace_bytes() bytes, 256-byte aligned, contents
- *                on entry irrelevant: fp32 D and LSE by heads, and the dQ
- *                accumulator.  0 for empty or unsupported shapes.
+ *                on entry irrelevant: fp32 D and LSE by heads, the dQ
+ *                accumulator and, where key tiles are split over SMs (by
+ *                the current device's SM count), the parts of dK and dV.  0 for
+ *                empty or unsupported shapes.
  * What rows of the other sequences and padding rows hold does not matter; a
  * sequence's own rows have to be finite, all of them.  rows * H up to 2^31 - 1
  * (FA_ERR_UNSUPPORTED).
