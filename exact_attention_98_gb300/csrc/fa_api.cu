@@ -983,21 +983,29 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
 
 namespace {
 
-// How many parts the backward cuts each item (key tile of a key head) into:
-// enough for four items to an SM, so that a causal batch of few items, which differ
-// by their place, fills the SMs evenly, but two query tiles each at least, by the
-// mean length.  At d = 64 no part may be without a query tile (its kernel's
-// ring), so there are as many as heads in a group at most.  The parts' dK and dV are joined by the
-// kernel after the main one.  XXX us, against YYY unsplit.
+// How many parts the backward cuts each item (key tile of a key head) into; the
+// parts' dK and dV are joined by the kernel after the main one, which costs
+// an item's part about four query tiles.  By the mean length of a sequence (lengths
+// are not known here), causal: as many parts as leave no SM idle, of two query
+// tiles each; as fill the SMs twice, since items differ by their place, of eight;
+// two where items are long and no more than two to an SM.  At d = 64 no part may be
+// without a query tile (its kernel's ring): as many as a group's heads at most.
+// d = 128, causal, in all, one part against the rule's: 1024 rows, H = 16, Hkv = 2,
+// 153 us -> 42 (8 parts); 12000 rows, H = 8, Hkv = 1, 1605 -> 578 (3); 4096
+// rows, H = 16, Hkv = 4, 302 -> 179 (2); 16001 rows, H = 8, Hkv = 2, 1118 ->
+// 1048 (2).  Beyond: 8 sequences of 1024 rows, H = 16, Hkv = 4, 149 us, with 2 parts 175.
 int packed_parts(int sequences, int rows, int H, int Hkv, int d) {
-  const int sms = sm_count();
+  const int sms = sm_count() > 0 ? sm_count() : 152;  // (without a device: a size for GB300)
+  const int group = H / Hkv;
   const long long items = packed_tiles(rows, sequences, kBlockN) * Hkv;
   const long long tiles = (static_cast<long long>(rows) / sequences + kBlockM - 1) / kBlockM;
-  const long long by_sms = 4LL * (sms > 0 ? sms : 152) / items;  // (without a device: a size for GB300)
-  const long long by_work = (tiles + 1) / 2 * (H / Hkv) / 2;
-  const long long most = d == 64 && H / Hkv < 8 ? H / Hkv : 8;
-  long long n = by_sms < by_work ? by_sms : by_work;
-  if (n > most) n = most;
+  const long long mean = (tiles + 1) * group / 2;  // query tiles of an item
+  auto least = [](long long a, long long b) { return a < b ? a : b; };
+  long long n = least(sms / items, mean / 2);
+  const long long twice = least(2 * sms / items, mean / 8);
+  if (twice > n) n = twice;
+  if (n < 2 && items <= 2 * sms && tiles * group >= 128) n = 2;
+  n = least(n, d == 64 && group < 8 ? group : 8);
   return n < 1 ? 1 : static_cast<int>(n);
 }
 

@@ -817,7 +817,9 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) r[0][e] = r[1][e] = 0u;
       }
-      if (raw != nullptr) {
+      if (kPacked && raw != nullptr) {
+        packed_part_row(raw, r, true);
+      } else if (raw != nullptr) {
         float4* dst = reinterpret_cast<float4*>(raw);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {

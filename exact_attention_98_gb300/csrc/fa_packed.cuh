@@ -124,11 +124,12 @@ __device__ __forceinline__ float* packed_part(const BwdParams& p, int part, bool
 // 64 columns of such a row; `some`: the part has query tiles, else they are zeros.
 __device__ __forceinline__ void packed_part_row(float* to, const uint32_t (&r)[2][32], bool some) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const uint32_t* x = &r[c >> 3][(c & 7) * 4];
-    reinterpret_cast<float4*>(to)[c] =
-        some ? make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3]))
-             : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t* x = &r[c >> 2][(c & 3) * 8];
+    if (some)
+      st_global_v8(to + 8 * c, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+    else
+      st_global_v8(to + 8 * c, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u);
   }
 }
 

@@ -112,8 +112,8 @@ cudaError_t launch(RotateParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_rotate(RotateParams p, int d, cudaStream_t stream) {
-  if (d == 128) return launch<128, 4>(p, stream);
-  if (d == 64) return launch<64, 4>(p, stream);
+  if (d == 128) return launch<128, 3>(p, stream);
+  if (d == 64) return launch<64, 3>(p, stream);
   return cudaErrorInvalidValue;
 }
 
