@@ -140,15 +140,15 @@ enum : unsigned int {
 // Block `blk` of the list of items: a key tile of a key head (or a part of its
 // query tiles) and its query tiles i_first..i_last, head by head.
 template <bool kPacked>
-struct alignas(16) KeyItem {
+struct alignas(kPacked ? 16 : 4) KeyItem {
   int bh, k0;      // key head, first key
-  int diag;        // the query tile that the diagonal crosses (packed, not causal: -1)
+  int diag;        // packed: the query tile that the diagonal crosses (-1: not causal)
   int part;        // of a split item, else -1
   int i_first, i_last;
   int n_iter;      // query tiles (all heads')
   int i, head;     // the first: tile and query head
   int start, len;  // packed: rows of the sequence
-  int unused;
+  int kt;          // key tile
 
   __device__ __forceinline__ void next() {
     if (++i > i_last) {
@@ -170,6 +170,7 @@ __device__ __forceinline__ KeyItem<kPacked> key_item(const BwdParams& p, int blk
     t.start = item.start;
     t.len = item.len;
     t.bh = item.kv;
+    t.kt = item.kt;
     t.k0 = item.kt * kBlockN;
     t.diag = item.causal ? item.kt : -1;
     t.i_first = item.causal ? item.kt : 0;
@@ -183,9 +184,9 @@ __device__ __forceinline__ KeyItem<kPacked> key_item(const BwdParams& p, int blk
       t.part = blk - p.split_from - i * p.split_parts;
     }
     t.bh = p.div_kblk.div(item);
-    t.diag = item - t.bh * p.n_kblk;
-    t.k0 = t.diag * kBlockN;
-    t.i_first = t.diag;
+    t.kt = item - t.bh * p.n_kblk;
+    t.k0 = t.kt * kBlockN;
+    t.i_first = t.kt;
     // (window <= N <= 2^30, so the sum is an int)
     t.i_last = min((p.N + kBlockM - 1) / kBlockM - 1, (t.k0 + kBlockN - 2 + p.window) / kBlockM);
   }
@@ -666,14 +667,14 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     int n = 0, m = 0;
     bool ok = true;
     KeyItem t_next;
+    bool more = false;  // packed: t_next is an item
     // (windows: items without query tiles, too)
     auto look = [&](int blk) {
-      if constexpr (kPacked) return advance(blk, t_next);
-      if (blk < total) t_next = key_item<kPacked>(p, blk);
-      return blk < total;
+      if constexpr (kPacked) more = advance(blk, t_next);
+      else if (blk < total) t_next = key_item<kPacked>(p, blk);
     };
-    bool more = look(blockIdx.x);
-    for (int blk = blockIdx.x; ok && more; blk += stride) {
+    look(blockIdx.x);
+    for (int blk = blockIdx.x; ok && (kPacked ? more : blk < total); blk += stride) {
       KeyItem t = t_next;
       const bool row_valid = t.k0 + kr < t.rows(p);
       const bool last_tile = t.k0 + kBlockN > t.rows(p);  // some key rows are past the last
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         // the diagonal tile, those whose last rows are past some key's window,
         // and all of a key tile with rows past N
         const bool edge = kPacked ? t.i == t.diag || last_tile
-                                  : t.i == t.diag || (t.i - t.diag) * kBlockM + kBlockM - 1 >= p.window || last_tile;
+                                  : t.i == t.kt || (t.i - t.kt) * kBlockM + kBlockM - 1 >= p.window || last_tile;
         ok = mbar_wait_short(bar(C::kBarSFull), n & 1, ctl, kSiteSFull);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         if (edge) {
           // the key sees the query columns [lo, lo + window) of the tile
           // (packed: [lo, ...), all where nothing is masked but the sequence's end)
-          const int lo = kPacked && t.i != t.diag ? 0 : (t.diag - t.i) * kBlockM + kr - wg * 64;
+          const int lo = kPacked && t.i != t.diag ? 0 : (t.kt - t.i) * kBlockM + kr - wg * 64;
           const int hi = kPacked ? 64 : lo + p.window;
           auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
 #pragma unroll
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(bar(C::kBarDSFull));
       }
-      more = look(blk + stride);
+      look(blk + stride);
 
       // The item's dV (warpgroup 0) and dK (warpgroup 1, times the softmax scale,
       // which dS left out): a thread holds its key row.
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         if (t.part >= 0 && row_valid) raw = packed_part(p, t.part, wg == 0, t.bh, t.start + t.k0 + kr, D);
       } else if (t.part >= 0)
         raw = p.tile_part + ((static_cast<size_t>(blk - p.split_from) * 2 + (wg == 0 ? 1 : 0)) * kBlockN + kr) * D;
-      else if (p.sink_main != nullptr && t.k0 == 0 && kr < p.sinks)
+      else if (p.sink_main != nullptr && t.kt == 0 && kr < p.sinks)
         raw = p.sink_main + ((static_cast<size_t>(t.bh) * 2 + (wg == 0 ? 1 : 0)) * p.sink_rows + kr) * D;
       if (ok && t.n_iter > 0) {
         ok = mbar_wait_short(bar(C::kBarMmaDone), m & 1, ctl, kSiteMmaDone);

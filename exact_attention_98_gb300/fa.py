@@ -658,12 +658,28 @@ def paged_pages(num_pages: int, heads: int, page_size: int, d: int, format: str 
     return torch.zeros((num_pages, heads, 2, page_size, d), dtype=torch.bfloat16, device=device)
 
 
-def rope_table(length: int, rot: int, base: float = 10000.0, device="cuda"):
+def rope_table(length: int, rot: int, base: float = 10000.0, device="cuda", scale: float = 1.0, trained: int = 0,
+               turns: tuple[float, float] = (1.0, 32.0), magnitude: float = 1.0):
     """fp32 [length, rot]: cos, then sin of position * base^(-2 i / rot), the
-    angles taken in 64 bits."""
+    angles taken in 64 bits.  For contexts longer than those trained on:
+    scale: every angle is divided by it (positions interpolated);
+    trained: the length trained on, if that is to depend on the pair: one that
+    turns at least turns[1] times over it keeps its angle, one that turns at
+    most turns[0] times has it divided by `scale`, between them the two are mixed
+    evenly by the number of turns;
+    magnitude: a factor on cos and sin (of rotated Q and K both: the scores' by its
+    square)."""
+    low, high = turns
+    if scale <= 0 or trained < 0 or not 0 <= low < high:
+        raise ValueError("scale must be positive, trained not negative, turns two rising numbers from 0 on")
     rate = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if trained:
+        kept = ((trained * rate / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        rate = rate * (kept + (1 - kept) / scale)
+    elif scale != 1:
+        rate = rate / scale
     angle = torch.arange(length, dtype=torch.float64)[:, None] * rate
-    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+    return (torch.cat([angle.cos(), angle.sin()], 1) * magnitude).float().to(device)
 
 
 def paged_append(k, v, pages, page_table, seq_lens, cu_new, q=None, rope=None, interleaved: bool = False,
@@ -845,7 +861,7 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
 
 
 @functools.lru_cache(maxsize=256)
-def _packed_workspace_bytes(sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
+def _packed_workspace_bytes(device: int, sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
     return max(fa_bwd_packed_workspace_bytes(sequences, rows, H, Hkv, d), 1)
 
 
@@ -861,7 +877,7 @@ def packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float | None
         out = _empty(stream, dev, ((rows, H, d), torch.bfloat16), shared, shared)
     dq, dk, dv = out
     if workspace is None:
-        workspace, = _empty(stream, dev, (_packed_workspace_bytes(plan.sequences, rows, H, Hkv, d), torch.uint8))
+        workspace, = _empty(stream, dev, (_packed_workspace_bytes(dev.index, plan.sequences, rows, H, Hkv, d), torch.uint8))
     _check_tensor(lse, "lse", torch.float32, (rows, H), dev)
     keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (o, "o", H), (dout, "dout", H),
                           (dq, "dq", H), (dk, "dk", Hkv), (dv, "dv", Hkv))

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from packed import batch, check_backward, check_forward, f64, plain_backward, plain_forward, rows
+from packed import batch, check_backward, check_forward, f64, plain_backward, plain_forward, rows, within
 from test_packed import CASES, run
 
 NAN = float("nan")
@@ -34,6 +34,78 @@ def test_backward(lengths, H, Hkv, causal, d):
 @pytest.mark.parametrize("H,Hkv", [(48, 16), (48, 24)])
 def test_more_items_than_sms(H, Hkv, d):
     check([300, 520, 77, 1, 900, 256], H, Hkv, d, True, seed=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths,H,Hkv,causal", [
+    ([2000], 1, 1, True),           # parts without a query tile (d = 128)
+    ([1030], 3, 1, True),           # parts that begin within a head
+    ([1500, 3, 700], 8, 1, True),
+    ([700, 1, 640], 16, 2, True),
+    ([900], 8, 1, False),
+    ([130] * 5, 8, 1, True),
+])
+def test_split_items(lengths, H, Hkv, causal, d):
+    """Few items: each is split, its parts joined afterwards."""
+    from exact_attention_98_gb300 import fa
+
+    n = sum(lengths)
+    whole = 256 + 2 * ((n * H * 4 + 255) // 256 * 256) + (n * H * d * 4 + 255) // 256 * 256
+    parts = (fa.fa_bwd_packed_workspace_bytes(len(lengths), n, H, Hkv, d) - whole) // (2 * Hkv * n * d * 4)
+    assert parts > 1 or (d == 64 and H == Hkv)
+    check(lengths, H, Hkv, d, causal, seed=n)
+    check(lengths, H, Hkv, d, causal, before=70, after=200, seed=n + 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_sequences(d):
+    check([1 + 7 * (i % 5) for i in range(700)], 2, 1, d, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_offsets_past_32_bits(d):
+    """The sequences are the last rows of tensors of more than 2^31 elements."""
+    from exact_attention_98_gb300 import fa
+
+    H, Hkv, lengths = 256, 2, [300, 77]
+    n = 2 ** 31 // (H * d) + 1000
+    cu, n = batch(lengths, n - sum(lengths), 5)
+    end = slice(cu[0], n)
+    q, k, v, do = (torch.empty(n, h, d, dtype=torch.bfloat16, device="cuda") for h in (H, Hkv, Hkv, H))
+    for i, t in enumerate((q, k, v, do)):
+        t[end] = rows(n - cu[0], t.shape[1], d, i, "dense")
+    plan = fa.packed_plan(torch.tensor(cu, dtype=torch.int32, device="cuda"), n)
+    table = fa.rope_table(300, d)
+    turned, _ = fa.rotate(q, None, plan.positions, table)
+    want = fa.rotate(q[end].clone(), None, plan.positions[end].clone(), table)[0]
+    live = slice(cu[0], cu[-1])
+    assert torch.equal(turned[live], want[: cu[-1] - cu[0]])
+    del turned, want
+    o, lse = fa.packed_forward(q, k, v, plan)
+    grads = fa.packed_backward(q, k, v, o, lse, do, plan)
+    assert fa.fa_last_device_status() == fa.FA_OK
+    cu = [x - cu[0] for x in cu]
+    heads = [0, 1, 127, 128, 255]  # (the bounds of every head would take minutes)
+    small = [t[end] for t in (q, k, v, o, lse, do, *grads)]
+    q, k, v, o, lse, do, dq, dk, dv = small
+    for h in heads:
+        one = [t[:, h: h + 1] for t in (q, o, do, dq)]
+        kv = [t[:, h // 128: h // 128 + 1] for t in (k, v)]
+        check_forward(one[1], lse[:, h: h + 1], one[0], *kv, cu, fa.default_scale(d), True)
+        for b in range(2):
+            s = slice(cu[b], cu[b + 1])
+            g, err = plain_backward(f64(one[0][s, 0]), f64(kv[0][s, 0]), f64(kv[1][s, 0]), f64(one[1][s, 0]),
+                                    f64(lse[s, h]), f64(one[2][s, 0]), fa.default_scale(d), True)
+            within(f64(one[3][s, 0]), g[0], err[0], ("dq", h))
+    # dK and dV as those of a batch of the last rows alone (whose items are split otherwise)
+    m = cu[-1]
+    alone = fa.packed_plan(torch.tensor(cu, dtype=torch.int32, device="cuda"), m)
+    again = fa.packed_backward(q[:m], k[:m], v[:m], o[:m], lse[:m].contiguous(), do[:m], alone)
+    for a, b in zip((dk, dv), again[1:]):
+        assert np.abs(f64(a[:m]) - f64(b)).max() <= 2.0 ** -7 * np.abs(f64(b)).max()
 
 
 @pytest.mark.gpu
