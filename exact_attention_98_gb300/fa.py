@@ -814,18 +814,25 @@ def packed_plan(cu_seqlens, rows: int, causal: bool = True, out: PackedPlan | No
 def _row_block(rows, d, device, *tensors):
     """The row tensors (tensor, name, heads) as consecutive fa_rows: their memory, to be kept until the
     call has returned, and its address."""
-    index = device.index
-    block = array.array("q")
+    index, fields = device.index, []
     for t, name, heads in tensors:
         if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == (rows, heads, d)
                 and t.get_device() == index):
             row, head, one = t.stride()
             if one == 1:
-                block.extend((t.data_ptr(), row, head))
+                fields += (t.data_ptr(), row, head)
                 continue
         _, row, head = _rows(t, name, heads, d, device, rows)  # raises, but for empty tensors
-        block.extend((t.data_ptr(), row, head))
+        fields += (t.data_ptr(), row, head)
+    block = array.array("q", fields)
     return block, block.buffer_info()[0]
+
+
+def _row_empty(stream, device, shape):
+    """An uninitialised row tensor whose memory belongs to the stream that uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return _empty(stream, device, (shape, torch.bfloat16))[0]
 
 
 _ROWS = ctypes.sizeof(Rows)
@@ -853,7 +860,7 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
     dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
     lse, = _empty(stream, dev, ((rows, H), torch.float32))
     if out is None:
-        out, = _empty(stream, dev, ((rows, H, d), torch.bfloat16))
+        out = _row_empty(stream, dev, (rows, H, d))
     keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (out, "out", H))
     fa_fwd_packed(plan.plan, plan.sequences, rows, at, at + _ROWS, at + 2 * _ROWS, at + 3 * _ROWS, lse, H, Hkv, d,
                   default_scale(d) if scale is None else scale, stream)
@@ -873,9 +880,10 @@ def packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float | None
     the results are not written."""
     dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
     if out is None:
-        shared = (rows, Hkv, d), torch.bfloat16
-        out = _empty(stream, dev, ((rows, H, d), torch.bfloat16), shared, shared)
-    dq, dk, dv = out
+        dq = _row_empty(stream, dev, (rows, H, d))
+        dk, dv = _row_empty(stream, dev, (rows, Hkv, d)), _row_empty(stream, dev, (rows, Hkv, d))
+    else:
+        dq, dk, dv = out
     if workspace is None:
         workspace, = _empty(stream, dev, (_packed_workspace_bytes(dev.index, plan.sequences, rows, H, Hkv, d), torch.uint8))
     _check_tensor(lse, "lse", torch.float32, (rows, H), dev)
@@ -911,8 +919,8 @@ def rotate(q, k, positions, rope, interleaved: bool = False, backward: bool = Fa
     rope_len, rot = rope.shape
     _check_tensor(rope, "rope", torch.float32, (rope_len, rot), dev)
     if out is None:
-        q2 = None if q is None else _empty(stream, dev, ((rows, H, d), torch.bfloat16))[0]
-        k2 = None if k is None else _empty(stream, dev, ((rows, Hkv, d), torch.bfloat16))[0]
+        q2 = None if q is None else _row_empty(stream, dev, (rows, H, d))
+        k2 = None if k is None else _row_empty(stream, dev, (rows, Hkv, d))
     else:
         q2, k2 = out
         if (q is None) != (q2 is None) or (k is None) != (k2 is None):
