@@ -821,17 +821,22 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (!(seen & (1u << e))) r[ch][e] = __float_as_uint(-INFINITY);
           }
+        } else if (PACKED && edge) {
+          const int lim = iv[1];
+          auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            const uint32_t seen = below(lim - ch * 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen & (1u << e))) r[ch][e] = __float_as_uint(-INFINITY);
+          }
         } else if (edge) {
           // the row keeps its first `lim` columns: keys below N and, causal,
           // not after the query
-          int lim;
-          if constexpr (PACKED) {
-            lim = iv[1];
-          } else {
-            const int kbase = jabs * kBlockN;
-            lim = p.N - kbase;
-            if (p.causal) lim = min(lim, iv[3] * kBlockN + row - kbase + 1);
-          }
+          const int kbase = jabs * kBlockN;
+          int lim = p.N - kbase;
+          if (p.causal) lim = min(lim, iv[3] * kBlockN + row - kbase + 1);
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
