@@ -1,5 +1,5 @@
-// Backward of the sliding window with shared key heads at d = 64 (d = 128 runs
-// fa_bwd.cu's body): the key-stationary products of fa_bwd.cu (S^T = K Q_i^T,
+// Backward of the sliding window and of packed sequences, both with shared key
+// heads, at d = 64 (d = 128 runs fa_bwd.cu's body): the key-stationary products of fa_bwd.cu (S^T = K Q_i^T,
 // dP^T = V dO_i^T, dV += P^T dO_i, dK += dS^T Q_i, dQ_i = dS K, all tcgen05 into
 // tensor memory, same columns and operand layouts), over the query tiles whose
 // windows reach the key tile, of each query head of the group in turn: dV and dK
@@ -140,7 +140,7 @@ enum : unsigned int {
 // Block `blk` of the list of items: a key tile of a key head (or a part of its
 // query tiles) and its query tiles i_first..i_last, head by head.
 template <bool kPacked>
-struct alignas(kPacked ? 16 : 4) KeyItem {
+struct alignas(16) KeyItem {
   int bh, k0;      // key head, first key
   int diag;        // packed: the query tile that the diagonal crosses (-1: not causal)
   int part;        // of a split item, else -1
@@ -148,7 +148,7 @@ struct alignas(kPacked ? 16 : 4) KeyItem {
   int n_iter;      // query tiles (all heads')
   int i, head;     // the first: tile and query head
   int start, len;  // packed: rows of the sequence
-  int kt;          // key tile
+  int kt;          // key tile (windows)
 
   __device__ __forceinline__ void next() {
     if (++i > i_last) {
@@ -170,7 +170,6 @@ __device__ __forceinline__ KeyItem<kPacked> key_item(const BwdParams& p, int blk
     t.start = item.start;
     t.len = item.len;
     t.bh = item.kv;
-    t.kt = item.kt;
     t.k0 = item.kt * kBlockN;
     t.diag = item.causal ? item.kt : -1;
     t.i_first = item.causal ? item.kt : 0;
@@ -222,9 +221,12 @@ __device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stri
 // a sequence's, the masks the diagonal (if causal) and the sequence's end.  Items
 // differ in their work by far, so a CTA takes its next one when it gets to it,
 // from a counter: the producer, which is first to need it, takes it, looks it up in
-// the plan and hands it to the other warps through a ring (dealt out in turn, as
-// for windows, the CTAs' sums differ by 28% for XXX; looked up by every warp, the
-// code grew from 74 to 97 KB, and the kernel from 211 us to 225).
+// the plan and hands it to the other warps through a ring.  16384 rows of 13
+// sequences, H = Hkv = 16: dealt out in turn, as for windows, 211 us, since the
+// CTAs' sums differ by 28%; off the counter but looked up by every warp 225 (97 KB
+// of code instead of 74); through the ring 202; taken when a CTA is three tiles from its
+// item's end, not an item ahead, 176.  It is 0.76 PFLOP/s of visible pairs; the
+// chain of a tile bounds it as below, the tensor pipe is active for 35% of the time.
 template <bool kPacked>
 __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     fa_bwd_window64_kernel(const __grid_constant__ BwdParams p) {
@@ -667,14 +669,14 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     int n = 0, m = 0;
     bool ok = true;
     KeyItem t_next;
-    bool more = false;  // packed: t_next is an item
     // (windows: items without query tiles, too)
     auto look = [&](int blk) {
-      if constexpr (kPacked) more = advance(blk, t_next);
-      else if (blk < total) t_next = key_item<kPacked>(p, blk);
+      if constexpr (kPacked) return advance(blk, t_next);
+      if (blk < total) t_next = key_item<kPacked>(p, blk);
+      return blk < total;
     };
-    look(blockIdx.x);
-    for (int blk = blockIdx.x; ok && (kPacked ? more : blk < total); blk += stride) {
+    bool more = look(blockIdx.x);
+    for (int blk = blockIdx.x; ok && more; blk += stride) {
       KeyItem t = t_next;
       const bool row_valid = t.k0 + kr < t.rows(p);
       const bool last_tile = t.k0 + kBlockN > t.rows(p);  // some key rows are past the last
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         if (edge) {
           // the key sees the query columns [lo, lo + window) of the tile
           // (packed: [lo, ...), all where nothing is masked but the sequence's end)
-          const int lo = kPacked && t.i != t.diag ? 0 : (t.kt - t.i) * kBlockM + kr - wg * 64;
+          const int lo = !kPacked ? (t.kt - t.i) * kBlockM + kr - wg * 64 : t.i == t.diag ? kr - wg * 64 : 0;
           const int hi = kPacked ? 64 : lo + p.window;
           auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
 #pragma unroll
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(bar(C::kBarDSFull));
       }
-      look(blk + stride);
+      more = look(blk + stride);
 
       // The item's dV (warpgroup 0) and dK (warpgroup 1, times the softmax scale,
       // which dS left out): a thread holds its key row.

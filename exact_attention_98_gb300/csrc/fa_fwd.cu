@@ -258,6 +258,14 @@ __device__ __forceinline__ WinItem win_item(const FwdParams& p, int w) {
 // Packed work item: two 128-row query tiles of one sequence that walk its key
 // tiles, all or up to the diagonal.  As for windows they are one query tile of two
 // heads of a group where the group is even, otherwise two neighbouring tiles of one head.
+//
+// What bounds it: as the plain forward for long sequences (36001 rows of 9, the
+// longest 32768, H = 16, Hkv = 4, d = 128: 2.6 ms, 1.69 PFLOP/s); for short ones an
+// item's change, about 1.5 key tiles' time, mostly the epilogue, in which both
+// softmax warpgroups leave the tensor core idle (24001 rows of 24 sequences, H =
+// 32, Hkv = 8: 229 us, 1.01 PFLOP/s, 83% of the walked pairs visible).  No gain:
+// items handed out by a warp of their own through a ring (245 us: spills in the
+// softmax), half of an O tile stored directly beside the staged half (235).
 struct PackItem {
   int head0, head1;  // query heads of the two tiles
   int row0, row1;    // their first rows within the sequence

@@ -5,11 +5,11 @@
 // CTA's share of the work then differs by 3% at most from an exact order's).  A
 // warp takes one bucket of one list: its first walk over the sequences counts the tiles of
 // higher buckets, which gives the bucket's place without a word between warps,
-// its second writes the bucket's tiles, in the order of the sequences, so the plan's bits do
-// not vary.  Two further walks' worth of blocks write the rows' positions.
+// its second writes the bucket's tiles, in the order of the sequences, so the plan's
+// bits do not vary.  Further blocks write the rows' positions.
 //
 // Latency bounds it (cu is read from cache by every warp): 3 sequences of 300 rows
-// and 24 of 24001 take about the time of a launch; it is made once for a batch.
+// and 24 of 24001 take 3 to 4 us; it is made once for a batch.
 #include "fa_packed.cuh"
 
 namespace fa {
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_packed_plan_kernel(const __gr
 // main kernel reads a head's rows one after another, and the zeroed dQ
 // accumulator.  16 bytes of a row to a lane.  Rows of no sequence are left out.
 // After it: dQ = scale * accumulator -> bf16, and dK and dV from their parts, where the
-// main kernel's items are split, in order.  Both are bound by HBM.
+// main kernel's items are split, in order.  Both are bound by HBM: 16384 rows, H = 16,
+// d = 128: 38 us for 268 MB (7.1 TB/s) and 26.5 for 201 MB (part of them still in L2).
 constexpr int kRowThreads = 256;
 
 template <int D>

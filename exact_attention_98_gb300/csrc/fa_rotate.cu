@@ -8,7 +8,9 @@
 // HBM bounds it: every element is read and written once, a few operations each.  A
 // thread takes 16 elements (8 pairs: two 16-byte loads) of kHeads heads of one row,
 // all loads before the first use, and the pairs' cos and sin once for these
-// heads.
+// heads.  16384 rows, H = 32, Hkv = 8, d = 128: 51 us, 6.6 TB/s.  Three heads to a
+// thread are 64 registers; 1, 2, 4 and 8 heads took 65, 62, 58 and 62 us against 58,
+// 4999 rows of 20 heads 17, 17, 17 and 17 against 15 (timed one by one).
 #include "fa_packed.cuh"
 
 namespace fa {
