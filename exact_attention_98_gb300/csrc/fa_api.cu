@@ -125,14 +125,15 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int N, int BH, int d,
 
 // Rows of packed sequences (fa_rows), bf16, viewed as (d, rows, heads): box as
 // encode_tile_map.  A single row's or head's stride does not matter.
-bool encode_rows_map(CUtensorMap* map, const fa_rows& t, int rows, int heads, int d) {
+bool encode_rows_map(CUtensorMap* map, const fa_rows& t, int rows, int heads, int d,
+                     unsigned int box_rows = kBlockM) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(heads)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rows > 1 ? t.row : d) * 2,
                                  static_cast<cuuint64_t>(heads > 1 ? t.head : d) * 2};
-  const cuuint32_t box[3] = {64, kBlockM, 1};
+  const cuuint32_t box[3] = {64, box_rows, 1};
   const cuuint32_t elem_strides[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.data, dims, strides, box, elem_strides,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -952,7 +953,7 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
     return FA_ERR_INVALID_ARG;
   FwdParams p = {};
   if (!encode_rows_map(&p.tm_q, *q, rows, H, d) || !encode_rows_map(&p.tm_k, *k, rows, Hkv, d) ||
-      !encode_rows_map(&p.tm_v, *v, rows, Hkv, d) || !encode_rows_map(&p.tm_o, *o, rows, H, d))
+      !encode_rows_map(&p.tm_v, *v, rows, Hkv, d) || !encode_rows_map(&p.tm_o, *o, rows, H, d, 32))
     return FA_ERR_CUDA;
   p.o = o->data;
   p.o_row = row_stride(*o, rows);
@@ -969,6 +970,8 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   p.num_splits = 1;
   const int group = H / Hkv;
   p.win_tiles = group % 2 == 0 ? 1 : 2;
+  const PackedLayout l = packed_layout(rows, sequences);
+  p.list = reinterpret_cast<const int4*>(static_cast<const char*>(plan) + (p.win_tiles == 1 ? l.tiles : l.blocks));
   const int units = p.win_tiles == 1 ? H / 2 : H;
   // an upper bound: the kernel reads how many there are (its grid is no larger than this)
   p.n_items = static_cast<int>(packed_tiles(rows, sequences, p.win_tiles * kBlockM) * units);
@@ -1071,6 +1074,9 @@ int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   p.log2e = 1.4426950408889634f;
   p.group = H / Hkv;
   p.plan = plan;
+  const PackedLayout l = packed_layout(rows, sequences);
+  p.tiles = reinterpret_cast<const int4*>(static_cast<const char*>(plan) + l.tiles);
+  p.seq_tiles = reinterpret_cast<const int4*>(static_cast<const char*>(plan) + l.seq_tiles);
   p.sequences = sequences;
   p.div_kv = FastDiv(static_cast<uint32_t>(Hkv));
   p.split_parts = packed_parts(sequences, rows, H, Hkv, d);

@@ -263,9 +263,13 @@ __device__ __forceinline__ WinItem win_item(const FwdParams& p, int w) {
 // longest 32768, H = 16, Hkv = 4, d = 128: 2.6 ms, 1.69 PFLOP/s); for short ones an
 // item's change, about 1.5 key tiles' time, mostly the epilogue, in which both
 // softmax warpgroups leave the tensor core idle (24001 rows of 24 sequences, H =
-// 32, Hkv = 8: 229 us, 1.01 PFLOP/s, 83% of the walked pairs visible).  No gain:
-// items handed out by a warp of their own through a ring (245 us: spills in the
-// softmax), half of an O tile stored directly beside the staged half (235).
+// 32, Hkv = 8: 223 us, 1.04 PFLOP/s, 83% of the walked pairs visible).  Of its about
+// 5000 cycles (by clock) the wait for the last product takes 1100, reading, scaling
+// and packing O 1000, its staged halves 1400, the next item's look-up 700, the first
+// wait for S 500.  From 229 us no gain (us): items handed out by a warp of their own
+// through a ring 245 (spills in the softmax), their entries prefetched into L1 232, half
+// of an O tile stored directly beside the staged half 235, a warp's rows turned over in
+// shared memory and stored directly 233.
 struct PackItem {
   int head0, head1;  // query heads of the two tiles
   int row0, row1;    // their first rows within the sequence
@@ -285,11 +289,9 @@ struct PackItem {
 };
 
 __device__ __forceinline__ PackItem pack_item(const FwdParams& p, int w) {
-  const PackedLayout l = packed_layout(p.N, p.sequences);
-  const uint8_t* plan = static_cast<const uint8_t*>(p.plan);
-  const bool causal = reinterpret_cast<const PackedHead*>(plan)->causal != 0;
+  const bool causal = static_cast<const PackedHead*>(p.plan)->causal != 0;
   const int entry = p.div_bh.div(w), unit = w - entry * static_cast<int>(p.div_bh.d);
-  const int4 e = reinterpret_cast<const int4*>(plan + (p.win_tiles == 1 ? l.tiles : l.blocks))[entry];
+  const int4 e = p.list[entry];
   PackItem it;
   it.start = e.x;
   it.len = e.y;
@@ -750,7 +752,8 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
         iv[2] = itm.skip;
         iv[3] = itm.q_row(t) / kBlockN;
       } else if constexpr (PACKED) {
-        // columns that a row keeps of the last tile, less those its own place adds
+        // the columns that the row keeps of the last tile; for the epilogue, the
+        // query tile's head and first row, and how many it has
         const bool causal = static_cast<const PackedHead*>(p.plan)->causal != 0;
         iv[0] = itm.nkv(t);
         iv[1] = causal ? row + 1 : itm.len - (itm.nkv(t) - 1) * kBlockN;
@@ -980,25 +983,26 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
       }
       // The staged epilogue synchronises the warpgroup's four warps: they
       // enter it, or leave the item loop, together.
-      if constexpr (C::kStageO) ok = named_bar_and(1 + t, kBlockM, ok);
+      if constexpr (C::kStageO && !PACKED) ok = named_bar_and(1 + t, kBlockM, ok);
       {
         if (ok) {
           tc_fence_after();
           const auto item = item_of(wi);
           const int bh = item.q_head(t);
           const int qrow0 = PAIR ? item.q_row(0) + tile_row0 : item.q_row(t);
-          const int qpos = qrow0 + row;
           const int part = item.part;
+          const int qpos = qrow0 + row;
           bool in_range = qpos < p.N;
-          bool staged = C::kStageO && part < 0;
           size_t lse_at = static_cast<size_t>(bh) * p.N + qpos;
           __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + lse_at * D;
           bool o32 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+          // PACKED: each warp its 32 rows; those behind the sequence's end are not
+          // its own, so a bulk store is for whole warps only
+          bool staged = C::kStageO && part < 0;
           if constexpr (PACKED) {
-            // the rows behind a sequence's end are not its own: a bulk store for
-            // whole tiles only
-            in_range = item.row(t) + row < item.len;
-            staged = item.row(t) + kBlockM <= item.len;
+            const int rows = item.len - item.row(t);  // of the query tile
+            in_range = row < rows;
+            staged = quarter * 32 + 32 <= rows;
             lse_at = static_cast<size_t>(qpos) * p.H + bh;
             orow = static_cast<__nv_bfloat16*>(p.o) + qpos * p.o_row + bh * p.o_head;
             o32 = o32 && p.o_row % 16 == 0 && p.o_head % 16 == 0;
@@ -1031,11 +1035,21 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
                                              __uint_as_float(r[ch][2 * e + 1]) * inv_l);
             uint8_t* stage = smem + C::kStageOff + t * C::kStageBytes + row * 128;
             const uint32_t stage_s = sbase + C::kStageOff + t * C::kStageBytes;
+            // PACKED: a warp stages and stores its rows by itself (boxes of 32 rows):
+            // without the warpgroup's barriers an item's change takes 350 cycles less
+            // of about 5000.
+            auto wait_read = [&] {
+              if (PACKED ? lane == 0 : row == 0) bulk_wait_read<0>();
+            };
+            auto sync = [&] {
+              if constexpr (PACKED) __syncwarp();
+              else named_bar_sync(1 + t, kBlockM);
+            };
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
               // the buffer's previous bulk store has read it
-              if (row == 0) bulk_wait_read<0>();
-              named_bar_sync(1 + t, kBlockM);
+              wait_read();
+              sync();
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const int wi = h * 32 + c * 4;
@@ -1043,8 +1057,13 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
                     make_uint4(w[wi], w[wi + 1], w[wi + 2], w[wi + 3]);
               }
               fence_proxy_async_smem();
-              named_bar_sync(1 + t, kBlockM);
-              if (row == 0) {
+              sync();
+              if constexpr (PACKED) {
+                if (lane == 0) {
+                  tma_store_3d(&p.tm_o, stage_s + quarter * 32 * 128, h * 64, qrow0 + quarter * 32, bh);
+                  bulk_commit();
+                }
+              } else if (row == 0) {
                 tma_store_3d(&p.tm_o, stage_s, h * 64, qrow0, bh);
                 bulk_commit();
               }
@@ -1112,7 +1131,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
     // The CTA may end once the last bulk stores of O have read shared
     // memory; the grid's completion covers their writes.
     if constexpr (C::kStageO) {
-      if (row == 0) bulk_wait_read<0>();
+      if (PACKED ? lane == 0 : row == 0) bulk_wait_read<0>();
     }
   }
 

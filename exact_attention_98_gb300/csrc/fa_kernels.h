@@ -82,11 +82,12 @@ struct FwdParams {
   int win_tiles;
   FastDiv div_group;
   // Packed sequences (plan != null; bf16, no split): the rows of all sequences
-  // follow one another, N is their number, and tm_q, tm_k, tm_v and tm_o have one
-  // slice per head.  A work item is entry i / units of the plan's list: two
+  // follow one another, N is their number, and tm_q, tm_k, tm_v and tm_o (box {64,
+  // 32, 1}) have one slice per head.  A work item is entry i / units of the plan's list: two
   // query tiles of one head (win_tiles = 2: blocks), or one of two heads (tiles);
   // div_bh's divisor is units.
   const void* plan;
+  const int4* list;          // in it
   int sequences;
   int H;                     // of lse [N, H]
   long long o_row, o_head;   // strides of o in elements
@@ -149,6 +150,8 @@ struct BwdParams {
   // rows of all sequences, BH the key heads, and `group` query heads share one;
   // lse and dsum are [query heads, N] as elsewhere.
   const void* plan;
+  const int4* tiles;      // in it
+  const int4* seq_tiles;
   int sequences;
   long long dk_row, dk_head, dv_row, dv_head;  // strides in elements
   FastDiv div_kv;  // by BH

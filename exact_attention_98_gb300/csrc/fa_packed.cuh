@@ -92,13 +92,11 @@ __device__ __forceinline__ int packed_items(const BwdParams& p) {
 
 // Item i (< packed_items) of a backward call.
 __device__ __forceinline__ PackedItem packed_item_at(const BwdParams& p, int i) {
-  const uint8_t* plan = static_cast<const uint8_t*>(p.plan);
-  const PackedHead& h = *reinterpret_cast<const PackedHead*>(plan);
-  const PackedLayout l = packed_layout(p.N, p.sequences);
+  const PackedHead& h = *static_cast<const PackedHead*>(p.plan);
   // in `tiles` the last tile of a sequence costs most; its first key tile does
   const bool heaviest = h.causal != 0 && h.n_tiles <= kFewTiles;
   const int entry = p.div_kv.div(i);
-  const int4 e = reinterpret_cast<const int4*>(plan + (heaviest ? l.tiles : l.seq_tiles))[entry];
+  const int4 e = (heaviest ? p.tiles : p.seq_tiles)[entry];
   PackedItem it;
   it.start = e.x;
   it.len = e.y;
