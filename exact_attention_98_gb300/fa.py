@@ -813,9 +813,12 @@ def packed_plan(cu_seqlens, rows: int, causal: bool = True, out: PackedPlan | No
 
 def _row_block(rows, d, device, *tensors):
     """The row tensors (tensor, name, heads) as consecutive fa_rows: their memory, to be kept until the
-    call has returned, and its address."""
+    call has returned, and its address.  Name None: one that has just been made (_row_empty)."""
     index, fields = device.index, []
     for t, name, heads in tensors:
+        if name is None:
+            fields += (t.data_ptr(), heads * d, d)
+            continue
         if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == (rows, heads, d)
                 and t.get_device() == index):
             row, head, one = t.stride()
@@ -859,11 +862,13 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
     written, strides as q.  Padding rows of the results are not written."""
     dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
     lse, = _empty(stream, dev, ((rows, H), torch.float32))
+    name = "out"
     if out is None:
-        out = _row_empty(stream, dev, (rows, H, d))
-    keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (out, "out", H))
-    fa_fwd_packed(plan.plan, plan.sequences, rows, at, at + _ROWS, at + 2 * _ROWS, at + 3 * _ROWS, lse, H, Hkv, d,
-                  default_scale(d) if scale is None else scale, stream)
+        out, name = _row_empty(stream, dev, (rows, H, d)), None
+    keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (out, name, H))
+    _check(lib.fa_fwd_packed(plan.plan.data_ptr(), plan.sequences, rows, at, at + _ROWS, at + 2 * _ROWS, at + 3 * _ROWS,
+                             lse.data_ptr(), H, Hkv, d, default_scale(d) if scale is None else float(scale),
+                             _stream(stream)), "fa_fwd_packed")
     return out, lse
 
 
@@ -879,8 +884,9 @@ def packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float | None
     to, strides as q (parts of a fused projection's gradient, say).  Padding rows of
     the results are not written."""
     dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
+    names = "dq", "dk", "dv"
     if out is None:
-        dq = _row_empty(stream, dev, (rows, H, d))
+        dq, names = _row_empty(stream, dev, (rows, H, d)), (None, None, None)
         dk, dv = _row_empty(stream, dev, (rows, Hkv, d)), _row_empty(stream, dev, (rows, Hkv, d))
     else:
         dq, dk, dv = out
@@ -888,10 +894,12 @@ def packed_backward(q, k, v, o, lse, dout, plan: PackedPlan, scale: float | None
         workspace, = _empty(stream, dev, (_packed_workspace_bytes(dev.index, plan.sequences, rows, H, Hkv, d), torch.uint8))
     _check_tensor(lse, "lse", torch.float32, (rows, H), dev)
     keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (o, "o", H), (dout, "dout", H),
-                          (dq, "dq", H), (dk, "dk", Hkv), (dv, "dv", Hkv))
+                          (dq, names[0], H), (dk, names[1], Hkv), (dv, names[2], Hkv))
     q, k, v, o, dout, gq, gk, gv = range(at, at + 8 * _ROWS, _ROWS)
-    fa_bwd_packed(plan.plan, plan.sequences, rows, q, k, v, o, lse, dout, gq, gk, gv, H, Hkv, d,
-                  default_scale(d) if scale is None else scale, workspace, stream)
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    _check(lib.fa_bwd_packed(plan.plan.data_ptr(), plan.sequences, rows, q, k, v, o, lse.data_ptr(), dout, gq, gk, gv,
+                             H, Hkv, d, default_scale(d) if scale is None else float(scale), ws_ptr, ws_bytes,
+                             _stream(stream)), "fa_bwd_packed")
     return dq, dk, dv
 
 
@@ -918,18 +926,20 @@ def rotate(q, k, positions, rope, interleaved: bool = False, backward: bool = Fa
         raise ValueError("rope must be [length, rot]")
     rope_len, rot = rope.shape
     _check_tensor(rope, "rope", torch.float32, (rope_len, rot), dev)
+    names = "out (q)", "out (k)"
     if out is None:
         q2 = None if q is None else _row_empty(stream, dev, (rows, H, d))
         k2 = None if k is None else _row_empty(stream, dev, (rows, Hkv, d))
+        names = None, None
     else:
         q2, k2 = out
         if (q is None) != (q2 is None) or (k is None) != (k2 is None):
             raise ValueError("out must hold a tensor for each of q and k that is given, and None otherwise")
-    given = () if q is None else ((q, "q", H), (q2, "out (q)", H))
+    given = () if q is None else ((q, "q", H), (q2, names[0], H))
     if k is not None:
-        given += (k, "k", Hkv), (k2, "out (k)", Hkv)
+        given += (k, "k", Hkv), (k2, names[1], Hkv)
     keep, at = _row_block(rows, d, dev, *given)
     of_k = at if q is None else at + 2 * _ROWS  # (not read where Hkv is 0, nor q's where H is)
-    fa_rotate(at, at + _ROWS, H, of_k, of_k + _ROWS, Hkv, positions, rows, d, rope, rope_len, rot, interleaved,
-              backward, stream)
+    _check(lib.fa_rotate(at, at + _ROWS, H, of_k, of_k + _ROWS, Hkv, positions.data_ptr(), rows, d, rope.data_ptr(),
+                         rope_len, rot, 1 if interleaved else 0, 1 if backward else 0, _stream(stream)), "fa_rotate")
     return q2, k2
