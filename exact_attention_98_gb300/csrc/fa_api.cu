@@ -1052,7 +1052,7 @@ int fa_bwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   if (!encode_rows_map(&p.tm_q, *q, rows, H, d) || !encode_rows_map(&p.tm_k, *k, rows, Hkv, d) ||
       !encode_rows_map(&p.tm_v, *v, rows, Hkv, d) || !encode_rows_map(&p.tm_do, *dout, rows, H, d) ||
       !encode_rows_map(&p.tm_dk, *dk, rows, Hkv, d) || !encode_rows_map(&p.tm_dv, *dv, rows, Hkv, d) ||
-      !encode_dq_map(&p.tm_dq, dq_acc, rows, H, d))
+      (d == 64 && !encode_dq_map(&p.tm_dq, dq_acc, rows, H, d)))  // (d = 128 adds dQ from registers)
     return FA_ERR_CUDA;
   p.lse = lse_heads;
   p.dsum = dsum;

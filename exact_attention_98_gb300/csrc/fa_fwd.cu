@@ -263,13 +263,14 @@ __device__ __forceinline__ WinItem win_item(const FwdParams& p, int w) {
 // longest 32768, H = 16, Hkv = 4, d = 128: 2.6 ms, 1.69 PFLOP/s); for short ones an
 // item's change, about 1.5 key tiles' time, mostly the epilogue, in which both
 // softmax warpgroups leave the tensor core idle (24001 rows of 24 sequences, H =
-// 32, Hkv = 8: 223 us, 1.04 PFLOP/s, 83% of the walked pairs visible).  Of its about
+// 32, Hkv = 8: 220 us, 1.05 PFLOP/s, 83% of the walked pairs visible).  Of its about
 // 5000 cycles (by clock) the wait for the last product takes 1100, reading, scaling
 // and packing O 1000, its staged halves 1400, the next item's look-up 700, the first
 // wait for S 500.  From 229 us no gain (us): items handed out by a warp of their own
 // through a ring 245 (spills in the softmax), their entries prefetched into L1 232, half
 // of an O tile stored directly beside the staged half 235, a warp's rows turned over in
-// shared memory and stored directly 233.
+// shared memory and stored directly 233; from 222, the next item looked up while the
+// last product runs 232 (and 2% on long sequences), this one's place 224.
 struct PackItem {
   int head0, head1;  // query heads of the two tiles
   int row0, row1;    // their first rows within the sequence
@@ -1008,7 +1009,8 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
             o32 = o32 && p.o_row % 16 == 0 && p.o_head % 16 == 0;
           }
           float inv_l = 1.0f / l;
-          float lse_row = m_used * p.ln2 + logf(l);
+          float lse_row = 0.0f;
+          if constexpr (!PACKED) lse_row = m_used * p.ln2 + logf(l);
           if constexpr (FP8) {  // P carried a factor 64, V the head's scale
             const float va = __uint_as_float(p.fp8_amax[p.BH + bh]);
             inv_l *= va > 0.0f ? va * (1.0f / 448.0f) : 1.0f;
@@ -1063,13 +1065,16 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
                   tma_store_3d(&p.tm_o, stage_s + quarter * 32 * 128, h * 64, qrow0 + quarter * 32, bh);
                   bulk_commit();
                 }
+                // (all rows are in range; the logarithm while the first half is read)
+                if (h == 0) p.lse[lse_at] = m_used * p.ln2 + logf(l);
               } else if (row == 0) {
                 tma_store_3d(&p.tm_o, stage_s, h * 64, qrow0, bh);
                 bulk_commit();
               }
             }
-            if (in_range) p.lse[lse_at] = lse_row;
+            if (!PACKED && in_range) p.lse[lse_at] = lse_row;
           } else if (part < 0) {
+            if constexpr (PACKED) lse_row = m_used * p.ln2 + logf(l);
             // The whole O row in one batch of loads (pair mode: 32 columns at
             // a time, registers are short there), then 32-byte stores where O
             // allows them (a row is 2d bytes, so every row keeps O's alignment).
