@@ -987,16 +987,18 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
 namespace {
 
 // How many parts the backward cuts each item (key tile of a key head) into; the
-// parts' dK and dV are joined by the kernel after the main one, which costs
-// an item's part about four query tiles.  By the mean length of a sequence (lengths
-// are not known here), causal: as many parts as leave no SM idle, of two query
-// tiles each; as fill the SMs twice, since items differ by their place, of eight;
-// two where items are long and no more than two to an SM.  At d = 64 no part may be
-// without a query tile (its kernel's ring): as many as a group's heads at most.
-// d = 128, causal, in all, one part against the rule's: 1024 rows, H = 16, Hkv = 2,
-// 153 us -> 42 (8 parts); 12000 rows, H = 8, Hkv = 1, 1605 -> 578 (3); 4096
-// rows, H = 16, Hkv = 4, 302 -> 179 (2); 16001 rows, H = 8, Hkv = 2, 1118 ->
-// 1048 (2).  Beyond: 8 sequences of 1024 rows, H = 16, Hkv = 4, 149 us, with 2 parts 175.
+// parts' dK and dV are joined by the kernel after the main one, which costs a part
+// about as much as four query tiles.  By the mean length of a sequence (lengths are
+// not known here), causal: as many parts as leave no SM idle, of two query tiles
+// each; as fill the SMs twice, since items differ by their place, of eight; two where
+// items are long and no more than two to an SM.  At d = 64 no part may be without a
+// query tile (its kernel's ring): as many as a group's heads at most.
+// Measured at d = 128, causal, in all, one part against the rule's:
+//   1024 rows, H = 16, Hkv = 2     153 us -> 42 (8 parts)
+//   12000 rows, H = 8, Hkv = 1    1605 us -> 578 (3)
+//   4096 rows, H = 16, Hkv = 4     302 us -> 179 (2)
+//   16001 rows, H = 8, Hkv = 2    1118 us -> 1048 (2)
+// and beyond it, 8 sequences of 1024 rows, H = 16, Hkv = 4: 149 us, with 2 parts 175.
 int packed_parts(int sequences, int rows, int H, int Hkv, int d) {
   const int sms = sm_count() > 0 ? sm_count() : 152;  // (without a device: a size for GB300)
   const int group = H / Hkv;

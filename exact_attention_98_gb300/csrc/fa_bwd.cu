@@ -277,8 +277,7 @@ __device__ __forceinline__ void bwd_body(const BwdParams& p) {
       blk = p.split_from + i;
     }
   }
-  // Packed: the heads of a sequence in turn, the key tiles of each.  The plan is
-  // earlier work of the stream.
+  // Packed: an entry of the plan's list (earlier work of the stream) for a head.
   PackedItem item{0, p.N, 0, 0, p.causal != 0};
   if constexpr (kPacked) {
     grid_dependency_wait();

@@ -1,9 +1,9 @@
 // Backward of the sliding window and of packed sequences, both with shared key
-// heads, at d = 64 (d = 128 runs fa_bwd.cu's body): the key-stationary products of fa_bwd.cu (S^T = K Q_i^T,
-// dP^T = V dO_i^T, dV += P^T dO_i, dK += dS^T Q_i, dQ_i = dS K, all tcgen05 into
-// tensor memory, same columns and operand layouts), over the query tiles whose
-// windows reach the key tile, of each query head of the group in turn: dV and dK
-// of a shared key head accumulate in tensor memory over the whole group.
+// heads, at d = 64 (d = 128 runs fa_bwd.cu's body): the key-stationary products of
+// fa_bwd.cu (S^T = K Q_i^T, dP^T = V dO_i^T, dV += P^T dO_i, dK += dS^T Q_i, dQ_i =
+// dS K, all tcgen05 into tensor memory, same columns and operand layouts), over the
+// query tiles that see the key tile, of each query head of the group in turn: dV and
+// dK of a shared key head accumulate in tensor memory over the whole group.
 //
 // An item is a key tile of a key head.  A short window leaves it few query
 // tiles (window / 128 + 1 per head) of little work each at d = 64, so what a CTA
@@ -427,7 +427,9 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
           if (m > 1 && !(ok = mbar_wait_short_warp(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
           if (lane == 0) load_kv(m, t);
         }
-        if (!ok && lane == 0)
+        // every copy has landed before shared memory is released (waits on the
+        // give-up path only: a wait for the ring may have ended the loop, too)
+        if (lane == 0)
           for (int k = max(0, m - 2); k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
       } else {
         bool more = advance(blk, t);  // (its copies are on their way)

@@ -68,10 +68,11 @@ __device__ __forceinline__ bool packed_fits(const PackedHead& h, int rows, int s
 // of as many parts of its query tiles.  The heads (and parts) of an entry of a
 // list follow one another.  The list is seq_tiles, so that CTAs that run at the
 // same time walk the same query tiles, whose Q, dO and dQ then pass through L2
-// once for all of them: with the heaviest key tiles of all sequences first, 131072
-// rows of 24 sequences (H = 16, Hkv = 4, d = 128, causal) took 8286 us instead of
-// 6170.  A causal batch of few tiles takes the heaviest first all the same: there
-// the last CTAs' idle time weighs more (16384 rows of 11 sequences: 325 us, not 338).
+// once for all of them: 131072 rows of 24 sequences (H = 16, Hkv = 4, d = 128, causal)
+// take 5926 us, with the heaviest key tiles of all sequences first 8286.  A causal
+// batch of few tiles takes the heaviest first all the same: there the last CTAs' idle
+// time weighs more (16384 rows of 11 sequences: 325 us instead of 338, both with a
+// sequence's heads in turn).
 constexpr int kFewTiles = 152;
 struct PackedItem {
   int start, len;  // rows of the sequence
@@ -80,7 +81,8 @@ struct PackedItem {
   bool causal;
 };
 
-// Items of a backward call, without their parts: 0 when the plan is not one for its rows (recorded).
+// Items of a backward call, without their parts: 0 when the plan is not one for its
+// rows (recorded).
 __device__ __forceinline__ int packed_items(const BwdParams& p) {
   const PackedHead& h = *static_cast<const PackedHead*>(p.plan);
   if (!packed_fits(h, p.N, p.sequences)) {
