@@ -943,14 +943,50 @@ int fa_packed_plan(const int* cu_seqlens, int sequences, int rows, int causal, v
   return launch_packed_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+namespace {
+
+// Key ranges that the forward may cut an item into (1: none) in a call of too few items
+// for the SMs; the kernel takes as many as the lengths ask for.  Whole call on the GPU, with
+// and without (us; one causal sequence, d = 128): 1500 rows, H 1: 23 and 28; 2048 rows, H 2:
+// 25 and 35; 8192, H 2: 52 and 106; 16384, H 1: 79 and 195.  fp32 parts and the join cost
+// 5 to 10, so that from half the SMs in items on only long sequences gain (H 3, d = 128:
+// 8192 rows, 99 items: 82 and 108; 4 x 2048, 108 items, not causal: 49 and 37), and under
+// 1408 rows a sequence little or nothing does (3 x 1300, H 3, not causal: 35 and 29).
+int packed_ranges(int sequences, int rows, int H, int Hkv) {
+  const int sms = sm_count() > 0 ? sm_count() : 152;  // (without a device: a size for GB300)
+  const bool pairs = H / Hkv % 2 == 0;
+  const long long entries = packed_tiles(rows, sequences, pairs ? kBlockM : 2 * kBlockM);
+  const long long items = entries * (pairs ? H / 2 : H);
+  const int mean = rows / sequences / kBlockN;  // key tiles of a sequence
+  if (mean < 11 || items > (mean < 32 ? sms / 2 : sms * 2 / 3)) return 1;
+  return static_cast<int>(std::min<long long>(kMaxPackParts, 2 * sms / items + 1));
+}
+
+}  // namespace
+
+size_t fa_fwd_packed_workspace_bytes(int sequences, int rows, int H, int Hkv, int d) {
+  bool empty = false;
+  // (any aligned address stands for the plan)
+  if (check_packed(reinterpret_cast<const void*>(kWsAlign), sequences, rows, H, Hkv, d, 1.0f, &empty) != FA_OK || empty)
+    return 0;
+  const int ranges = packed_ranges(sequences, rows, H, Hkv);
+  if (ranges < 2) return 0;
+  const size_t n = static_cast<size_t>(ranges) * rows * H;
+  return kWsAlign + round_up(n * d * sizeof(float)) + round_up(n * sizeof(float));
+}
+
 int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k, const fa_rows* v,
-                  const fa_rows* o, float* lse, int H, int Hkv, int d, float scale, void* stream) {
+                  const fa_rows* o, float* lse, int H, int Hkv, int d, float scale, void* workspace,
+                  size_t workspace_bytes, void* stream) {
   bool empty = false;
   const int rc = check_packed(plan, sequences, rows, H, Hkv, d, scale, &empty);
   if (rc != FA_OK || empty) return rc;
   if (!rows_ok(q, rows, H, d) || !rows_ok(k, rows, Hkv, d) || !rows_ok(v, rows, Hkv, d) || !rows_ok(o, rows, H, d) ||
       !lse || !aligned4(lse))
     return FA_ERR_INVALID_ARG;
+  const size_t need = fa_fwd_packed_workspace_bytes(sequences, rows, H, Hkv, d);
+  if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0))
+    return FA_ERR_WORKSPACE;
   FwdParams p = {};
   if (!encode_rows_map(&p.tm_q, *q, rows, H, d) || !encode_rows_map(&p.tm_k, *k, rows, Hkv, d) ||
       !encode_rows_map(&p.tm_v, *v, rows, Hkv, d) || !encode_rows_map(&p.tm_o, *o, rows, H, d, 32))
@@ -968,18 +1004,25 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
   p.c = scale * 1.4426950408889634f;
   p.ln2 = 0.6931471805599453f;
   p.num_splits = 1;
+  if (workspace && need > 0) {
+    p.num_splits = packed_ranges(sequences, rows, H, Hkv);
+    p.part_count = static_cast<int*>(workspace);
+    p.o_part = static_cast<float*>(workspace) + kWsAlign / sizeof(float);
+    p.lse_part = p.o_part + round_up(static_cast<size_t>(p.num_splits) * rows * H * d * sizeof(float)) / sizeof(float);
+  }
   const int group = H / Hkv;
   p.win_tiles = group % 2 == 0 ? 1 : 2;
   const PackedLayout l = packed_layout(rows, sequences);
   p.list = reinterpret_cast<const int4*>(static_cast<const char*>(plan) + (p.win_tiles == 1 ? l.tiles : l.blocks));
   const int units = p.win_tiles == 1 ? H / 2 : H;
   // an upper bound: the kernel reads how many there are (its grid is no larger than this)
-  p.n_items = static_cast<int>(packed_tiles(rows, sequences, p.win_tiles * kBlockM) * units);
+  p.n_items = static_cast<int>(packed_tiles(rows, sequences, p.win_tiles * kBlockM) * units) * p.num_splits;
   p.div_bh = FastDiv(static_cast<uint32_t>(units));
   p.div_group = FastDiv(static_cast<uint32_t>(group));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err = timing_record(0, true, s);
   if (err == cudaSuccess) err = launch_fwd(p, d, s);
+  if (err == cudaSuccess && p.num_splits > 1) err = launch_packed_merge(p, d, s);
   if (err == cudaSuccess) err = timing_record(0, false, s);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -109,7 +109,8 @@ struct FwdCfg {
   static constexpr int kNumBars = kBarTrim + (PACKED ? kSlots : 0);
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kAbortOff = kTmemSlotOff + 4;
-  static constexpr int kSmemUsed = kAbortOff + 4;
+  static constexpr int kPartsOff = kAbortOff + 4;  // PartTable
+  static constexpr int kSmemUsed = kPartsOff + (PACKED ? (3 + kMaxPackParts) * 4 : 0);
   static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for 1024-byte alignment
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
@@ -313,6 +314,83 @@ __device__ __forceinline__ PackItem pack_item(const FwdParams& p, int w) {
   return it;
 }
 
+// The same cut by keys, for calls of few items: range s of an item is its key tiles
+// [s C, (s + 1) C), its own item where there are such.  All items' first ranges come
+// first, then their second ones, ...: the items of range s are those of more than
+// s C key tiles, which the list begins with.  (Its order is exact to 3%: from 64
+// key tiles on, a range may have an item without keys, which is passed over.)
+// Every range found by striding over all items and ranges, the empty ones too, leaves
+// CTAs without one and others with two: 35 us instead of 29 (4096 rows, H 2, d = 128).
+struct PartTable {
+  int tiles;                    // C
+  int parts;                    // ranges of the longest item
+  int first[kMaxPackParts + 1];  // items before range s
+};
+struct PackPart : PackItem {
+  int kb;    // the first key tile
+  int part;  // s
+  int parts0, parts1;  // ranges that each query tile sees keys of
+  __device__ __forceinline__ int parts(int t) const { return t ? parts1 : parts0; }
+  __device__ __forceinline__ int key_row(int j) const { return PackItem::key_row(kb + j); }
+  __device__ __forceinline__ bool ragged(int j) const { return PackItem::ragged(kb + j); }
+};
+
+__device__ __forceinline__ PackPart pack_part(const FwdParams& p, int w, const PartTable& tab) {
+  int s = 0;
+  while (s + 1 < tab.parts && w >= tab.first[s + 1]) ++s;
+  PackPart it;
+  static_cast<PackItem&>(it) = pack_item(p, w - tab.first[s]);
+  it.part = s;
+  it.kb = s * tab.tiles;
+  it.parts0 = (it.nkv0 + tab.tiles - 1) / tab.tiles;
+  it.parts1 = (it.nkv1 + tab.tiles - 1) / tab.tiles;
+  it.nkv0 = max(0, min(it.nkv0 - it.kb, tab.tiles));
+  it.nkv1 = max(0, min(it.nkv1 - it.kb, tab.tiles));
+  it.nmax = max(it.nkv0, it.nkv1);
+  return it;
+}
+
+// The cut of a call, the same in every CTA; one warp.  cost: room for the entries'
+// key tiles.  Of 32 lengths of a range, the one of the least time, in key tiles: a range
+// costs two more than it has; with more ranges than CTAs, a CTA's share and half a range.
+__device__ __forceinline__ void part_table(const FwdParams& p, int entries, int* cost, PartTable& tab) {
+  const int lane = lane_id(), units = static_cast<int>(p.div_bh.d);
+  const int ctas = static_cast<int>(gridDim.x);
+  entries = min(entries, kMaxPackPartEntries);  // (as the host has seen to)
+  int longest = 0, sum = 0;
+  for (int e = lane; e < entries; e += 32) {
+    const int n = pack_item(p, e * units).nmax;
+    cost[e] = n;
+    longest = max(longest, n);
+    sum += n;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  __syncwarp();
+  int c = max(max(2, (longest + p.num_splits - 1) / p.num_splits), (longest * (lane + 1) + 31) / 32);
+  int total = 0;
+  for (int e = 0; e < entries; ++e) total += (cost[e] + c - 1) / c;
+  total *= units;
+  const int time = total <= ctas ? c + 2 : max(c + 2, (sum * units + 2 * total) / ctas + c / 2);
+  const unsigned int best = __reduce_min_sync(0xffffffffu, static_cast<unsigned int>(time) * 32 + 31 - lane);
+  c = __shfl_sync(0xffffffffu, c, 31 - static_cast<int>(best & 31u));
+  const int parts = max(1, (longest + c - 1) / c);
+  int n = 0;  // lane s: the items of range s
+  for (int e = 0; e < entries; ++e)
+    if (cost[e] > lane * c) n = (e + 1) * units;
+  int before = 0;
+  for (int s = 0; s < parts; ++s) {
+    if (lane == 0) tab.first[s] = before;
+    before += __shfl_sync(0xffffffffu, n, s);
+  }
+  if (lane == 0) {
+    tab.tiles = c;
+    tab.parts = parts;
+    tab.first[parts] = before;
+    if (blockIdx.x == 0) *p.part_count = parts;
+  }
+}
+
 // Work items of a packed call: 0 when the plan is not one for its rows
 // (recorded).
 __device__ __forceinline__ int pack_items(const FwdParams& p) {
@@ -339,8 +417,10 @@ __device__ __forceinline__ int fwd_item_index(int r) {
 // at positions 0 .. POLY-1 are evaluated by the polynomial on the FMA pipe
 // (exp2_poly2 for a pair, exp2_poly for a lone one), the rest by MUFU ex2.
 // WINDOW: sliding window with first tokens and shared key heads (win_item).
-// PACKED: packed sequences and shared key heads (pack_item).
-template <int D, int POLY, bool FP8, bool PAIR = false, bool WINDOW = false, bool PACKED = false>
+// PACKED: packed sequences and shared key heads (pack_item).  PARTS: its items cut by
+// keys (pack_part).
+template <int D, int POLY, bool FP8, bool PAIR = false, bool WINDOW = false, bool PACKED = false,
+          bool PARTS = false>
 __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using C = FwdCfg<D, FP8, PAIR, PACKED>;
@@ -358,9 +438,11 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
   const int n_ktiles = (p.N + kBlockN - 1) / kBlockN;
   // pair mode: this CTA's rank in the pair (0 issues the MMAs)
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  PartTable& part_tab = *reinterpret_cast<PartTable*>(smem + C::kPartsOff);
   auto item_of = [&](int wi) {
     if constexpr (PAIR) return pair_item(p, wi, n_ktiles);
     else if constexpr (WINDOW) return win_item(p, wi);
+    else if constexpr (PARTS) return pack_part(p, wi, part_tab);
     else if constexpr (PACKED) return pack_item(p, wi);
     else return fwd_item(p, wi, n_ktiles);
   };
@@ -399,6 +481,14 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
   grid_dependency_wait();
   int n_packed = 0;
   if constexpr (PACKED) n_packed = pack_items(p);
+  if constexpr (PARTS) {
+    // (the entries' costs in the ring, before its first copy)
+    if (warp == 0)
+      part_table(p, p.div_bh.div(n_packed), reinterpret_cast<int*>(smem + C::kRingOff), part_tab);
+    fence_proxy_async_smem();
+    __syncthreads();
+    n_packed = part_tab.first[part_tab.parts];
+  }
   auto n_items = [&] { return PACKED ? n_packed : p.n_items; };
 
   if (warp >= 8) {
@@ -535,12 +625,12 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
       for (int round = 0;; ++round) {
         const int wi = fwd_item_index(round);
         if (wi >= n_items()) break;
-        const PackItem item = pack_item(p, wi);
-        if (item.ragged(item.nmax - 1)) {
+        const auto item = item_of(wi);
+        if ((!PARTS || item.nmax > 0) && item.ragged(item.nmax - 1)) {
           const int slot = (base + 2 * item.nmax - 1) % C::kSlots;
           if (!mbar_wait_warp(bar(C::kBarTrim + slot), (parity >> slot) & 1u, ctl, kSiteTrim)) break;
           parity ^= 1u << slot;
-          const int row0 = item.len - (item.nmax - 1) * kBlockN;
+          const int row0 = item.start + item.len - item.key_row(item.nmax - 1);
           for (int h = 0; h < D / 64; ++h)
             for (int i = row0 * 8 + lane; i < kBlockN * 8; i += 32)
               *reinterpret_cast<uint4*>(smem + C::kRingOff + slot * C::kTileBytes + h * C::kHalfBytes + i * 16) =
@@ -758,12 +848,21 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
         const bool causal = static_cast<const PackedHead*>(p.plan)->causal != 0;
         iv[0] = itm.nkv(t);
         iv[1] = causal ? row + 1 : itm.len - (itm.nkv(t) - 1) * kBlockN;
+        if constexpr (PARTS) {  // only the part with the diagonal or the end masks
+          const int end = itm.kb + itm.nkv(t);
+          if (causal ? end * kBlockN <= itm.row(t) : end * kBlockN <= itm.len) iv[1] = kBlockN;
+          else if (!causal) iv[1] = itm.len - (end - 1) * kBlockN;
+        }
       } else {
         iv[0] = itm.nkv0;
         iv[1] = itm.nkv1;
         iv[2] = itm.kb;
         iv[3] = (itm.q0 + tile_row0) / kBlockN;
       }
+      if constexpr (PARTS)  // the ranges without keys for the row have no weight in the join
+        if (itm.part == 0 && itm.row(t) + row < itm.len)
+          for (int s = itm.parts(t); s < part_tab.parts; ++s)
+            p.lse_part[(static_cast<size_t>(s) * p.N + itm.q_row(t) + row) * p.H + itm.q_head(t)] = -INFINITY;
       if (iv[WINDOW || PACKED ? 0 : t] == 0) {
         if constexpr (WINDOW || PACKED) continue;
         // Split mode: an empty key range still leaves its partial result
@@ -1003,7 +1102,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
           if constexpr (PACKED) {
             const int rows = item.len - item.row(t);  // of the query tile
             in_range = row < rows;
-            staged = quarter * 32 + 32 <= rows;
+            staged = !PARTS && quarter * 32 + 32 <= rows;
             lse_at = static_cast<size_t>(qpos) * p.H + bh;
             orow = static_cast<__nv_bfloat16*>(p.o) + qpos * p.o_row + bh * p.o_head;
             o32 = o32 && p.o_row % 16 == 0 && p.o_head % 16 == 0;
@@ -1016,7 +1115,26 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
             inv_l *= va > 0.0f ? va * (1.0f / 448.0f) : 1.0f;
             lse_row -= 6.0f * p.ln2;
           }
-          if (staged) {
+          if constexpr (PARTS) {
+            // this part's O (normalised over it) and LSE in fp32, for the join
+            const size_t at = (static_cast<size_t>(part) * p.N + qpos) * p.H + bh;
+            float* to = p.o_part + at * D;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              uint32_t r[32];
+              tmem_ld32(t_o + ch * 32, r);
+              tmem_ld_wait(r);
+              if (in_range) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv_l);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                  st_global_v8(to + ch * 32 + e, r[e], r[e + 1], r[e + 2], r[e + 3], r[e + 4], r[e + 5], r[e + 6],
+                               r[e + 7]);
+              }
+            }
+            if (in_range) p.lse_part[at] = m_used * p.ln2 + logf(l);
+          } else if (staged) {
             // The whole O row in one batch of loads, normalised and packed;
             // then per 64 columns: staged in this warpgroup's buffer (a 128B-
             // swizzle box: row r at r * 128 bytes, 16-byte chunk c at
@@ -1152,10 +1270,10 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8, PAIR, PACKED>::kThreads, 1)
   }
 }
 
-template <int D, int POLY, bool FP8 = false, bool WINDOW = false, bool PACKED = false>
+template <int D, int POLY, bool FP8 = false, bool WINDOW = false, bool PACKED = false, bool PARTS = false>
 cudaError_t launch_fwd_dp(const FwdParams& p, cudaStream_t stream) {
   using C = FwdCfg<D, FP8, false, PACKED>;
-  constexpr auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW, PACKED>;
+  constexpr auto kernel = fa_fwd_kernel<D, POLY, FP8, false, WINDOW, PACKED, PARTS>;
   cudaError_t err = configure_kernel<kernel>(C::kSmemBytes, C::kLaunchRegs);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM (the kernel holds all of tensor memory),
@@ -1221,6 +1339,10 @@ cudaError_t launch_fwd_d(const FwdParams& p, cudaStream_t stream) {
 
 cudaError_t launch_fwd(const FwdParams& p, int d, cudaStream_t stream) {
   if (p.pair) return (d == 128 && !p.fp8) ? launch_fwd_pair(p, stream) : cudaErrorInvalidValue;
+  if (p.plan && p.num_splits > 1)
+    return d == 128  ? launch_fwd_dp<128, 0, false, false, true, true>(p, stream)
+           : d == 64 ? launch_fwd_dp<64, 0, false, false, true, true>(p, stream)
+                     : cudaErrorInvalidValue;
   if (p.plan)
     return d == 128  ? launch_fwd_dp<128, 0, false, false, true>(p, stream)
            : d == 64 ? launch_fwd_dp<64, 0, false, false, true>(p, stream)

@@ -31,6 +31,10 @@ constexpr int kBlockN = 128;
 // tau = 8; on N(0,1) inputs tau = 2 rescales about 0.7% of row-tiles.
 constexpr float kRescaleThreshold = 2.0f;
 
+// Packed forward cut by keys: ranges of an item, and entries of the plan's list, at most.
+constexpr int kMaxPackParts = 16;
+constexpr int kMaxPackPartEntries = 512;
+
 struct FwdParams {
   CUtensorMap tm_q;  // bf16 [BH, N, d], box {64, 128, 1}, 128B swizzle
   CUtensorMap tm_k;
@@ -91,6 +95,10 @@ struct FwdParams {
   int sequences;
   int H;                     // of lse [N, H]
   long long o_row, o_head;   // strides of o in elements
+  // num_splits > 1: items are cut into up to as many key ranges, whose O (normalised)
+  // and LSE go to o_part [ranges, N, H, d], lse_part [ranges, N, H]; how many, to
+  // part_count
+  int* part_count;
 };
 
 // Default share of the forward's exponentials evaluated by the polynomial on
@@ -340,6 +348,8 @@ struct PackedPlanParams {
   unsigned int* status;
 };
 cudaError_t launch_packed_plan(PackedPlanParams p, cudaStream_t stream);
+// O and LSE of a packed forward from its parts.
+cudaError_t launch_packed_merge(const FwdParams& p, int d, cudaStream_t stream);
 
 // What the packed backward does beside its main kernel (fa_packed.cu): before it D,
 // LSE by heads and the zeroed dQ accumulator, after it dQ as bf16.

@@ -263,6 +263,64 @@ __global__ void __launch_bounds__(kRowThreads) fa_packed_post_kernel(const __gri
   }
 }
 
+// The forward's parts joined: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.
+// Parts without a key have LSE_s = -inf and are not read.  In fp32, rounded once, at the end.
+// Bound by latency: the parts, at most some 60 MB, come from L2.
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) fa_packed_merge_kernel(const __grid_constant__ FwdParams p) {
+  constexpr int kLanes = D / 8, kRows = kRowThreads / kLanes;
+  grid_dependency_wait();
+  const PackedHead& head = *static_cast<const PackedHead*>(p.plan);
+  if (!packed_fits(head, p.N, p.sequences)) return;
+  const int parts = *p.part_count;
+  const int col = static_cast<int>(threadIdx.x) % kLanes * 8;
+  const long long n = static_cast<long long>(head.end - head.begin) * p.H;
+  const size_t stride = static_cast<size_t>(p.N) * p.H;  // of a part
+  for (long long i = blockIdx.x * static_cast<long long>(kRows) + threadIdx.x / kLanes; i < n;
+       i += static_cast<long long>(gridDim.x) * kRows) {
+    const size_t at = static_cast<size_t>(head.begin) * p.H + i;  // row * H + head
+    // four ranges at a time: their loads together
+    float m = -INFINITY;
+    for (int s0 = 0; s0 < parts; s0 += 4) {
+      float ls[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) ls[u] = s0 + u < parts ? p.lse_part[(s0 + u) * stride + at] : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) m = fmaxf(m, ls[u]);
+    }
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f;
+    for (int s0 = 0; s0 < parts; s0 += 4) {
+      float w[4];
+      float4 x[4], y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float ls = s0 + u < parts ? p.lse_part[(s0 + u) * stride + at] : -INFINITY;
+        w[u] = 0.0f;
+        x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ls != -INFINITY) {
+          w[u] = expf(ls - m);
+          const float4* from = reinterpret_cast<const float4*>(p.o_part + ((s0 + u) * stride + at) * D + col);
+          x[u] = from[0];
+          y[u] = from[1];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        sum += w[u];
+        acc[0] += w[u] * x[u].x; acc[1] += w[u] * x[u].y; acc[2] += w[u] * x[u].z; acc[3] += w[u] * x[u].w;
+        acc[4] += w[u] * y[u].x; acc[5] += w[u] * y[u].y; acc[6] += w[u] * y[u].z; acc[7] += w[u] * y[u].w;
+      }
+    }
+    const float inv = 1.0f / sum;
+    const long long row = head.begin + i / p.H;
+    const int h = static_cast<int>(i % p.H);
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + row * p.o_row + h * p.o_head + col;
+    *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                                               pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (col == 0) p.lse[at] = m + logf(sum);
+  }
+}
+
 // Blocks for n rows of a head: as many as are resident at once, at most.
 dim3 row_grid(long long n, int per_block) {
   const long long blocks = (n + per_block - 1) / per_block, cap = 8LL * (sm_count() > 0 ? sm_count() : 1);
@@ -281,6 +339,13 @@ cudaError_t launch_packed_pre(const PackedBwdParams& p, int d, cudaStream_t stre
 cudaError_t launch_packed_post(const PackedBwdParams& p, int d, cudaStream_t stream) {
   const cudaError_t err = launch_dependent(d == 128 ? fa_packed_post_kernel<128> : fa_packed_post_kernel<64>,
                                            row_grid(static_cast<long long>(p.rows) * p.H, 4 * kRowThreads / (d / 8)),
+                                           dim3(kRowThreads), 0, stream, p);
+  return err != cudaSuccess ? err : launched(1);
+}
+
+cudaError_t launch_packed_merge(const FwdParams& p, int d, cudaStream_t stream) {
+  const cudaError_t err = launch_dependent(d == 128 ? fa_packed_merge_kernel<128> : fa_packed_merge_kernel<64>,
+                                           row_grid(static_cast<long long>(p.N) * p.H, kRowThreads / (d / 8)),
                                            dim3(kRowThreads), 0, stream, p);
   return err != cudaSuccess ? err : launched(1);
 }

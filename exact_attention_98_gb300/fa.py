@@ -133,7 +133,9 @@ def _load() -> ctypes.CDLL:
     lib.fa_packed_plan_bytes.restype = sz
     lib.fa_packed_plan.argtypes = [vp, i, i, i, vp, sz, vp]
     lib.fa_packed_plan.restype = i
-    lib.fa_fwd_packed.argtypes = [vp, i, i, rows, rows, rows, rows, vp, i, i, i, f, vp]
+    lib.fa_fwd_packed_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.fa_fwd_packed_workspace_bytes.restype = sz
+    lib.fa_fwd_packed.argtypes = [vp, i, i, rows, rows, rows, rows, vp, i, i, i, f, vp, sz, vp]
     lib.fa_fwd_packed.restype = i
     lib.fa_bwd_packed_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.fa_bwd_packed_workspace_bytes.restype = sz
@@ -479,10 +481,15 @@ def fa_packed_plan(cu_seqlens, sequences, rows, causal, plan, stream=None) -> No
                               _stream(stream)), "fa_packed_plan")
 
 
-def fa_fwd_packed(plan, sequences, rows, q, k, v, o, lse, H, Hkv, d, scale, stream=None) -> None:
+def fa_fwd_packed_workspace_bytes(sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib.fa_fwd_packed_workspace_bytes(sequences, rows, H, Hkv, d))
+
+
+def fa_fwd_packed(plan, sequences, rows, q, k, v, o, lse, H, Hkv, d, scale, workspace=None, stream=None) -> None:
     """q, k, v, o: an fa_rows each, as byref(Rows(...)) or its address (None: null)."""
-    _check(lib.fa_fwd_packed(_ptr(plan), sequences, rows, q, k, v, o, _ptr(lse), H, Hkv, d, float(scale),
-                             _stream(stream)), "fa_fwd_packed")
+    ws_ptr, ws_bytes = _workspace(workspace, plan.device)
+    _check(lib.fa_fwd_packed(_ptr(plan), sequences, rows, q, k, v, o, _ptr(lse), H, Hkv, d, float(scale), ws_ptr,
+                             ws_bytes, _stream(stream)), "fa_fwd_packed")
 
 
 def fa_bwd_packed_workspace_bytes(sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
@@ -855,20 +862,31 @@ def _packed_heads(q, k, plan):
     return dev, plan.rows, H, k.shape[1], d
 
 
-def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=None, stream=None):
+@functools.lru_cache(maxsize=256)
+def _packed_split_bytes(device: int, sequences: int, rows: int, H: int, Hkv: int, d: int) -> int:
+    return fa_fwd_packed_workspace_bytes(sequences, rows, H, Hkv, d)
+
+
+def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=None, workspace=None, stream=None):
     """Attention within each packed sequence of `plan` (see packed_plan): q
     [rows, H, d], k and v [rows, Hkv, d] (H a multiple of Hkv; row and head strides
     that are multiples of 8) -> (o [rows, H, d], lse [rows, H]).  out: where o is
-    written, strides as q.  Padding rows of the results are not written."""
+    written, strides as q.  workspace: of fa_fwd_packed_workspace_bytes() bytes (None:
+    allocated where the call uses one).  Padding rows of the results are not written."""
     dev, rows, H, Hkv, d = _packed_heads(q, k, plan)
     lse, = _empty(stream, dev, ((rows, H), torch.float32))
     name = "out"
     if out is None:
         out, name = _row_empty(stream, dev, (rows, H, d)), None
+    if workspace is None:
+        n = _packed_split_bytes(dev.index, plan.sequences, rows, H, Hkv, d)
+        if n:
+            workspace, = _empty(stream, dev, (n, torch.uint8))
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
     keep, at = _row_block(rows, d, dev, (q, "q", H), (k, "k", Hkv), (v, "v", Hkv), (out, name, H))
     _check(lib.fa_fwd_packed(plan.plan.data_ptr(), plan.sequences, rows, at, at + _ROWS, at + 2 * _ROWS, at + 3 * _ROWS,
-                             lse.data_ptr(), H, Hkv, d, default_scale(d) if scale is None else float(scale),
-                             _stream(stream)), "fa_fwd_packed")
+                             lse.data_ptr(), H, Hkv, d, default_scale(d) if scale is None else float(scale), ws_ptr,
+                             ws_bytes, _stream(stream)), "fa_fwd_packed")
     return out, lse
 
 

@@ -371,13 +371,21 @@ int fa_packed_plan(const int* cu_seqlens, int sequences, int rows, int causal, v
  *                     multiple of Hkv
  *   lse             : out, fp32 [rows, H]
  *   d               : 64 or 128
+ *   workspace       : optional (NULL, 0 = none): with fa_fwd_packed_workspace_bytes()
+ *                     bytes on the current device, 256-byte aligned, contents on entry
+ *                     irrelevant, a call with too few work items for the SMs (a
+ *                     long prompt of few heads) cuts them into key ranges,
+ *                     joined by a second kernel as fa_fwd_splitkv's.  0 bytes where
+ *                     that does not apply.  Calls in flight at once need one each.
+ *                     FA_ERR_WORKSPACE for a short or misaligned one.
  * K and V have to be finite in the rows of a sequence that hold a row's later keys
  * (a masked pair's weight is an exact 0, and 0 times an infinity or a NaN is not);
  * what other sequences and padding rows hold does not matter.
  */
+size_t fa_fwd_packed_workspace_bytes(int sequences, int rows, int H, int Hkv, int d);
 int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, const fa_rows* k,
                   const fa_rows* v, const fa_rows* o, float* lse, int H, int Hkv, int d, float scale,
-                  void* stream);
+                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Backward of fa_fwd_packed, as fa_bwd: gradients of sum(O * dO); dk and dv
@@ -596,8 +604,8 @@ int fa_timing_last_ms(int kernel, float* ms);
  * fa_bwd_deterministic three; fa_fwd_fp8 three (two preparation kernels and
  * the forward; four with the merge, as fa_fwd); fa_fwd_splitkv two;
  * fa_fwd_2cta one; fa_bwd_2cta three; fa_fwd_window one; fa_bwd_window three;
- * fa_paged_append and fa_paged_read one; fa_packed_plan, fa_fwd_packed and
- * fa_rotate one, fa_bwd_packed three;
+ * fa_paged_append and fa_paged_read one; fa_packed_plan and fa_rotate one,
+ * fa_fwd_packed one, or two when it cuts items into key ranges, fa_bwd_packed three;
  * fa_fwd_paged two (the forward, then the join of segments that several CTAs
  * shared).
  */

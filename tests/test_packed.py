@@ -55,6 +55,121 @@ def test_forward_more_items_than_sms(d):
     run([300, 520, 77, 1, 900, 256], 48, 24, d, True, seed=2)
 
 
+# Few items: cut into key ranges and joined.  The bounds hold for that too: a range's LSE, of
+# up to 9, is off by its rounding, 2^-21, and weights by exponentials' few ulps, so a
+# joined O by less than the 2 * 2^-20 sum p |v| that scores' errors are given.
+SPLIT = [
+    ([1408], 1, 1, True),
+    ([2000], 4, 2, True),             # an even group: one tile of two heads
+    ([1537], 3, 1, True),                # an odd one: two tiles of one head, the last without a second
+    ([3300, 1, 0, 2400], 2, 2, True),
+    ([1281, 1700, 1300], 2, 1, True),
+    ([4225], 1, 1, True),
+    ([100, 4000], 4, 2, True),
+    ([100, 4000], 6, 3, False),    # one item too many
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths,H,Hkv,split", SPLIT)
+def test_forward_split(lengths, H, Hkv, split, d, causal):
+    from exact_attention_98_gb300 import fa
+
+    assert (fa.fa_fwd_packed_workspace_bytes(len(lengths), sum(lengths), H, Hkv, d) > 0) == split
+    run(lengths, H, Hkv, d, causal, layout="fused" if H % 2 else "heads", seed=d + H)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,H,Hkv", [([8200, 8350], 1, 1), ([9000], 2, 1), ([16000, 30], 1, 1), ([1500] * 5, 2, 2)])
+def test_forward_split_as_without(lengths, H, Hkv, causal):
+    """Longer sequences, with the workspace and without: both round P (2^-8 of sum p v, v > 0, so of O) and O
+    once, and nothing else beyond fp32, so they differ by 2 * 2^-8 (1 + 1) |O|, and a little."""
+    from ctypes import byref
+
+    from exact_attention_98_gb300 import fa
+
+    cu, n = batch(lengths, 1, 2)
+    d = 128
+    q, k, v = rows(n, H, d, 1, "dense"), rows(n, Hkv, d, 2, "dense"), rows(n, Hkv, d, 3, "dense")
+    v = v.abs() + torch.linspace(0, 1, n, device="cuda").to(torch.bfloat16)[:, None, None]
+    plan = fa.packed_plan(torch.tensor(cu, dtype=torch.int32, device="cuda"), n, causal)
+    need = fa.fa_fwd_packed_workspace_bytes(len(lengths), n, H, Hkv, d)
+    assert need > 0
+    got = []
+    # (what the workspace holds on entry does not matter)
+    for ws in (None, torch.full((need,), 255, dtype=torch.uint8, device="cuda")):
+        o = torch.full((n, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((n, H), 7.0, device="cuda")
+        r = [byref(fa.Rows(t.data_ptr(), t.stride(0), t.stride(1))) for t in (q, k, v, o)]
+        fa.fa_fwd_packed(plan.plan, len(lengths), n, *r, lse, H, Hkv, d, fa.default_scale(d), ws)
+        assert fa.fa_last_device_status() == fa.FA_OK, hex(fa.fa_last_device_site())
+        got.append((o.double(), lse.double()))
+    (o0, l0), (o1, l1) = got
+    for t in (o0, l0, o1, l1):
+        assert (t[:1] == 7).all() and (t[cu[-1]:] == 7).all()
+    r = slice(1, cu[-1])
+    assert ((o0 - o1).abs()[r] <= 2.0 ** -8 * 4.1 * o0.abs()[r]).all()
+    # scores alike in both; sums and logarithms in fp32
+    assert ((l0 - l1).abs()[r] <= 2.0 ** -18 * (1 + l0.abs()[r])).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_forward_split_other_rows_do_not_matter(d, causal):
+    from exact_attention_98_gb300 import fa
+
+    cu, n = batch([1500, 1300, 1700], 3, 200)
+    q, k, v = rows(n, 2, d, 5), rows(n, 2, d, 6), rows(n, 2, d, 7)
+    for t, bad in ((q, NAN), (k, float("inf")), (v, NAN)):
+        for a, b in ((0, 3), (cu[1], cu[2]), (cu[-1], n)):
+            t[a:b] = bad
+    plan = fa.packed_plan(torch.tensor(cu, dtype=torch.int32, device="cuda"), n, causal)
+    assert fa.fa_fwd_packed_workspace_bytes(3, n, 2, 2, d) > 0
+    wide = torch.full((n, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.packed_forward(q, k, v, plan, out=wide[:, 1:3])
+    assert fa.fa_last_device_status() == fa.FA_OK
+    check_forward(o, lse, q, k, v, cu, fa.default_scale(d), causal, skip=(1,))
+    assert (wide[:, 0] == 7).all() and (wide[:, 3] == 7).all()
+    assert (wide[:3] == 7).all() and (wide[cu[-1]:] == 7).all()
+
+
+@pytest.mark.gpu
+def test_forward_split_plans():
+    """A plan remade in a captured graph, of one sequence, of many and of none; bits do not vary;
+    memory that is no plan."""
+    from exact_attention_98_gb300 import fa
+
+    n, d = 3000, 128
+    cu = torch.tensor([0, 0, n], dtype=torch.int32, device="cuda")
+    q, k, v = (rows(n, 2, d, s) for s in range(3))
+    plan = fa.packed_plan(cu, n)
+    assert fa.fa_fwd_packed_workspace_bytes(2, n, 2, 2, d) > 0
+    out = torch.empty(n, 2, d, dtype=torch.bfloat16, device="cuda")
+    first = fa.packed_forward(q, k, v, plan)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.packed_plan(cu, n, out=plan)
+        _, lse = fa.packed_forward(q, k, v, plan, out=out)
+    for offsets in ([0, 0, n], [0, 130, 140], [7, 7, 7], [1, 1500, n - 1]):
+        cu.copy_(torch.tensor(offsets, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fa.fa_last_device_status() == fa.FA_OK
+        check_forward(out, lse, q, k, v, offsets, fa.default_scale(d), True)
+        assert (out[: offsets[0]] == 7).all() and (out[offsets[-1]:] == 7).all()
+        if offsets == [0, 0, n]:
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    out.fill_(7.0)
+    fa.packed_forward(q, k, v, fa.PackedPlan(torch.zeros_like(plan.plan), n, 2, True), out=out)
+    assert fa.fa_last_device_status() == fa.FA_ERR_INVALID_ARG
+    assert (out == 7).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("layout", ["dense", "heads"])
 def test_forward_layouts(layout):

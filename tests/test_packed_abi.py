@@ -31,9 +31,9 @@ def plan(fa, cu=A, n=3, rows=100, causal=1, plan=A, nbytes=BIG):
     return fa.lib.fa_packed_plan(P(cu), n, rows, causal, P(plan), nbytes, None)
 
 
-def forward(fa, plan=A, n=3, rows=100, lse=A, H=4, Hkv=2, d=128, scale=0.1, **t):
+def forward(fa, plan=A, n=3, rows=100, lse=A, H=4, Hkv=2, d=128, scale=0.1, ws=0, nbytes=0, **t):
     r = [t.get(x, block(fa)) for x in ("q", "k", "v", "o")]
-    return fa.lib.fa_fwd_packed(P(plan), n, rows, *r, P(lse), H, Hkv, d, scale, None)
+    return fa.lib.fa_fwd_packed(P(plan), n, rows, *r, P(lse), H, Hkv, d, scale, P(ws), nbytes, None)
 
 
 def backward(fa, plan=A, n=3, rows=100, lse=A, H=4, Hkv=2, d=128, scale=0.1, ws=A, nbytes=BIG, **t):
@@ -119,6 +119,19 @@ def test_rows_are_checked(fa, rows):
         assert backward(fa, **{x: t}) == fa.FA_ERR_INVALID_ARG, x
     for x in ("q", "q_out"):
         assert rotate(fa, **{x: t}) == fa.FA_ERR_INVALID_ARG, x
+
+
+def test_forward_workspace(fa):
+    """Optional, where there are few items of long sequences; a short or misaligned one is refused."""
+    need = fa.fa_fwd_packed_workspace_bytes(1, 4096, 4, 2, 128)
+    assert need >= 2 * 4096 * 4 * (128 * 4 + 4)
+    kw = dict(n=1, rows=4096, H=4, Hkv=2)
+    for bad in (dict(nbytes=need - 1), dict(nbytes=BIG, ws=A + 64)):
+        assert forward(fa, **{**kw, "ws": A, **bad}) == fa.FA_ERR_WORKSPACE, bad
+    for a in ((0, 4096, 4, 2, 128), (1, 0, 4, 2, 128), (1, 4096, 0, 2, 128), (1, 4096, 4, 3, 128), (1, 4096, 4, 2, 96),
+              (-1, 4096, 4, 2, 128), (1, 1, 1, 1, 64), (100, 4096, 4, 2, 128), (1, 4096, 64, 8, 128),
+              (1, 2 ** 30, 1, 1, 64)):
+        assert fa.fa_fwd_packed_workspace_bytes(*a) == 0, a
 
 
 def test_backward_workspace(fa):
