@@ -37,6 +37,7 @@
 #include "fa_device.cuh"
 #include "fa_kernels.h"
 #include "fa_packed.cuh"
+#include "fa_walk.h"
 
 namespace fa {
 namespace {
@@ -254,20 +255,24 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
   static_assert(sizeof(KeyItem) == 48, "ring entries");
   int taken = 0;  // packed: entries of the ring that this warp has read (the producer: written)
   // A warp's next item that has query tiles, `blk` being the next block to look at;
-  // packed: the ring's next, which has some unless it is the end.
+  // packed: the ring's next, which has some unless it is the end.  A wait for the ring
+  // may give up, for each warp by itself.
   auto advance = [&](int& blk, KeyItem& t) {
     if constexpr (kPacked) {
       const int slot = taken % C::kRing;
-      if (!mbar_wait_short_warp(bar(C::kBarRingFull + slot), (taken / C::kRing) & 1, ctl, kSiteRingFull)) return false;
+      if (!mbar_wait_short_warp(bar(C::kBarRingFull + slot), (taken / C::kRing) & 1, ctl, kSiteRingFull))
+        return Next::kGaveUp;
       t = ring[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::kBarRingEmpty + slot));
       ++taken;
-      return t.n_iter > 0;
+      return t.n_iter > 0 ? Next::kItem : Next::kEnd;
     } else {
-      return next_item(p, blk, stride, total, t);
+      return next_item(p, blk, stride, total, t) ? Next::kItem : Next::kEnd;
     }
   };
+  // the same for roles whose warps do not meet, and leave at either
+  auto another = [&](int& blk, KeyItem& t) { return advance(blk, t) == Next::kItem; };
 
   // One arrival for the warp's lanes, each of which has made its own fence: lanes
   // that all arrive take turns at the barrier's word, and shared memory is what
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     if constexpr (!kPacked) {
       KeyItem t;
       int blk = blockIdx.x;
-      if (advance(blk, t)) {
+      if (another(blk, t)) {
         load_kv(0, t);
         load_tile(0, t);
       }
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
       unsigned int following = 0;
       auto first = [&] {
         if constexpr (kPacked) return hand_out();
-        else return advance(blk, t);
+        else return another(blk, t);
       };
       for (bool more = first(); ok && more;) {
         for (int it = 0; it < t.n_iter; ++it) {
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
           more = ok && hand_out();
         } else {
           blk += stride;
-          more = ok && advance(blk, t);
+          more = ok && another(blk, t);
         }
       }
       // Let every copy this CTA started land before shared memory is released
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
       KeyItem t;
       if constexpr (kPacked) {
         int m = 0;
-        for (; advance(blk, t); ++m) {
+        for (; another(blk, t); ++m) {
           // (as below)
           if (m > 1 && !(ok = mbar_wait_short_warp(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
           if (lane == 0) load_kv(m, t);
@@ -432,11 +437,11 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         if (lane == 0)
           for (int k = max(0, m - 2); k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
       } else {
-        bool more = advance(blk, t);  // (its copies are on their way)
+        bool more = another(blk, t);  // (its copies are on their way)
         int m = 1;
         while (more) {
           blk += stride;
-          more = advance(blk, t);
+          more = another(blk, t);
           if (!more) break;
           // the buffers are free once dV and dK of the item before the last have
           // left them
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         bool ok = true;
         int blk = blockIdx.x;
         KeyItem t;
-        for (; ok && advance(blk, t); ++m) {
+        for (; ok && another(blk, t); ++m) {
           if (t.k0 + kBlockN > t.len) {
             if (!(ok = wait(C::kBarTrimKV + (m & 1)))) break;
             clear(C::kKOff + (m & 1) * C::kTileBytes, t.len - t.k0);
@@ -523,12 +528,12 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
       int m = 0, blk = blockIdx.x;
       KeyItem t;
       int left = 0;                                    // tiles of the item from this step's on
-      int next_left = !kPacked && advance(blk, t) ? t.n_iter : 0;  // of the next item (packed: looked up in time)
+      int next_left = !kPacked && another(blk, t) ? t.n_iter : 0;  // of the next item (packed: looked up in time)
       bool first = false;                             // this step's tile is its item's first
       bool ok = true;
       for (int n = -1;; ++n) {
         const bool last = left <= 1;  // (of the item, or step -1)
-        if (kPacked && last) next_left = advance(blk, t) ? t.n_iter : 0;
+        if (kPacked && last) next_left = another(blk, t) ? t.n_iter : 0;
         const bool next = !last || next_left > 0;
         if (n < 0 && !next) break;
         const int s = n % C::kStages;
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
           left = next_left;
           if constexpr (!kPacked) {
             blk += stride;
-            next_left = advance(blk, t) ? t.n_iter : 0;
+            next_left = another(blk, t) ? t.n_iter : 0;
           }
         }
       }
@@ -595,61 +600,74 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     const int qr = quarter * 32 + lane;  // query row within the tile (d = 64)
     const bool leader = (warp == C::kDrainWarp0 && lane == 0);
     const uint32_t t_dq = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + C::kColDQ;
-    int n = 0, buf = 0;
-    bool ok = true;
+    int n = 0, buf = 0, left = 0;
     int blk = blockIdx.x;
     KeyItem t;
-    for (; ok && advance(blk, t); blk += stride) {
-      for (int it = 0; it < t.n_iter; ++it, ++n, t.next()) {
-        ok = mbar_wait_short(bar(C::kBarDQFull), n & 1, ctl, kSiteDQFull);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          // release drain warps already waiting at this tile's barriers below (the
-          // next tile's dQ never comes without this warp's kBarDQEmpty)
-          for (int c = 0; c < C::kDqChunks; ++c) named_bar_arrive(C::kDrainBarrier, kBlockM);
-          break;
-        }
-        tc_fence_after();
-        const int q0 = t.i * kBlockM;
-        uint32_t r[4][16];
+    uint32_t r[4][16];
+    // The fp32 dQ tile goes out in chunks of 16 columns (64-byte swizzled rows)
+    // through a ring of buffers; the TMA adds them into the accumulator.
+    auto stage = [&](const uint32_t (&x)[16]) {
+      uint8_t* row = smem + C::kDqOff + buf * C::kDqChunkBytes + qr * 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld16(t_dq + c * C::kDqCols, r[c]);
-        tmem_ld_wait16(r[0]);
-        reg_fence16(r[1]);
-        reg_fence16(r[2]);
-        reg_fence16(r[3]);
-        tc_fence_before();
-        warp_arrive(bar(C::kBarDQEmpty));
-        // packed: rows past the sequence's end add zeros to whatever follows it
-        if (kPacked && q0 + qr >= t.len) {
+      for (int c4 = 0; c4 < 4; ++c4)
+        *reinterpret_cast<uint4*>(row + ((c4 ^ ((qr >> 1) & 3)) << 4)) =
+            make_uint4(x[4 * c4], x[4 * c4 + 1], x[4 * c4 + 2], x[4 * c4 + 3]);
+      fence_proxy_async_smem();
+    };
+    auto look = [&] {
+      const Next next = advance(blk, t);
+      blk += stride;
+      if (next == Next::kItem) left = t.n_iter;
+      return next;
+    };
+    auto take = [&] {
+      bool ok = mbar_wait_short(bar(C::kBarDQFull), n & 1, ctl, kSiteDQFull);
+      if (!(ok = __all_sync(0xffffffffu, ok))) return false;
+      tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) tmem_ld16(t_dq + c * C::kDqCols, r[c]);
+      tmem_ld_wait16(r[0]);
+      reg_fence16(r[1]);
+      reg_fence16(r[2]);
+      reg_fence16(r[3]);
+      tc_fence_before();
+      warp_arrive(bar(C::kBarDQEmpty));
+      // packed: rows past the sequence's end add zeros to whatever follows it
+      if (kPacked && t.i * kBlockM + qr >= t.len) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) r[c][e] = 0u;
-        }
-        // The fp32 dQ tile goes out in chunks of 16 columns (64-byte swizzled rows)
-        // through a ring of buffers; the TMA adds them into the accumulator.
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int c = 0; c < C::kDqChunks; ++c) {
-          uint8_t* chunk = smem + C::kDqOff + buf * C::kDqChunkBytes;
-          uint8_t* row = chunk + qr * 64;
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4)
-            *reinterpret_cast<uint4*>(row + ((c4 ^ ((qr >> 1) & 3)) << 4)) =
-                make_uint4(r[c][4 * c4], r[c][4 * c4 + 1], r[c][4 * c4 + 2], r[c][4 * c4 + 3]);
-          fence_proxy_async_smem();
-          // The leader comes to it once the TMA has read all chunks but the last
-          // issued: the buffer written after the barrier is free.
-          named_bar_sync(C::kDrainBarrier, kBlockM);
-          if (leader) {
-            tma_reduce_add_3d(&p.tm_dq, smem_u32(chunk), c * C::kDqCols, t.row0() + q0, t.head);
-            bulk_commit();
-            bulk_wait_read<1>();
-          }
-          buf = buf == C::kDqBufs - 1 ? 0 : buf + 1;
-        }
+          for (int e = 0; e < 16; ++e) r[c][e] = 0u;
       }
-    }
+      stage(r[0]);
+      return true;
+    };
+    // The leader comes to a chunk's barrier once the TMA has read all chunks but the last
+    // issued: the buffer written after the barrier is free.  A tile's first is the
+    // warps' meeting.
+    auto meet = [&](bool ok) { return named_bar_and(C::kDrainBarrier, kBlockM, ok); };
+    auto give = [&] {
+#pragma unroll
+      for (int c = 0; c < C::kDqChunks; ++c) {
+        if (c > 0) {
+          stage(r[c]);
+          named_bar_sync(C::kDrainBarrier, kBlockM);
+        }
+        if (leader) {
+          tma_reduce_add_3d(&p.tm_dq, sbase + C::kDqOff + buf * C::kDqChunkBytes, c * C::kDqCols,
+                            t.row0() + t.i * kBlockM, t.head);
+          bulk_commit();
+          bulk_wait_read<1>();
+        }
+        buf = buf == C::kDqBufs - 1 ? 0 : buf + 1;
+      }
+    };
+    auto step = [&] {
+      ++n;
+      t.next();
+      return --left > 0;
+    };
+    walk_tiles(look, take, meet, give, step);
     if (leader) bulk_wait<0>();
   } else {
     regs_set<C::kComputeRegs, C::kLaunchRegs>();
@@ -675,10 +693,16 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     auto look = [&](int blk) {
       if constexpr (kPacked) return advance(blk, t_next);
       if (blk < total) t_next = key_item<kPacked>(p, blk);
-      return blk < total;
+      return blk < total ? Next::kItem : Next::kEnd;
     };
-    bool more = look(blockIdx.x);
-    for (int blk = blockIdx.x; ok && more; blk += stride) {
+    // The warpgroup goes on, or gives up, together: its warps meet in the epilogue, so
+    // that a warp which gives up, for a tile or for the ring, says so at the next
+    // meeting and leaves with the others behind it (fa_walk.h has the reasons).  The
+    // lookups of windows cannot fail.
+    auto meet = [&](bool v) { return named_bar_and(C::kEpiBarrier0 + wg, kBlockM, v); };
+    Next next = look(blockIdx.x);
+    if constexpr (kPacked) ok = meet(next != Next::kGaveUp);
+    for (int blk = blockIdx.x; ok && next == Next::kItem; blk += stride) {
       KeyItem t = t_next;
       const bool row_valid = t.k0 + kr < t.rows(p);
       const bool last_tile = t.k0 + kBlockN > t.rows(p);  // some key rows are past the last
@@ -787,7 +811,8 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(bar(C::kBarDSFull));
       }
-      more = look(blk + stride);
+      next = look(blk + stride);
+      if (kPacked && next == Next::kGaveUp) ok = false;
 
       // The item's dV (warpgroup 0) and dK (warpgroup 1, times the softmax scale,
       // which dS left out): a thread holds its key row.
@@ -805,8 +830,7 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
         ok = mbar_wait_short(bar(C::kBarMmaDone), m & 1, ctl, kSiteMmaDone);
         ok = __all_sync(0xffffffffu, ok);
       }
-      // the warpgroup goes on, or gives up, together: its warps meet below
-      if (!(ok = named_bar_and(C::kEpiBarrier0 + wg, kBlockM, ok))) break;
+      if (!(ok = meet(ok))) break;
       uint32_t r[2][32];
       if (t.n_iter > 0) {
         tc_fence_after();
