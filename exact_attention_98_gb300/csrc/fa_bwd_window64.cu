@@ -413,43 +413,40 @@ __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
           more = ok && another(blk, t);
         }
       }
-      // Let every copy this CTA started land before shared memory is released
-      // (only on the give-up path, where a barrier may lack the loader's own
-      // arrival or have no copy in flight: the waits are bounded).
-      if (lane == 0 && !ok) {
+      // Every copy this CTA started lands before shared memory is released, also where
+      // another role has given up: a barrier may then lack an arrival, so the waits are
+      // bounded.
+      if (lane == 0) {
         for (int k = max(0, n - C::kStages); k < n; ++k)
           mbar_wait_drain(bar(C::kBarStFull + k % C::kStages), (k / C::kStages) & 1);
       }
     } else if (warp == C::kKVWarp && (kPacked || lane == 0)) {
       // ----------------------------------------------------------- K and V
-      bool ok = true;
       int blk = blockIdx.x;
       KeyItem t;
       if constexpr (kPacked) {
         int m = 0;
         for (; another(blk, t); ++m) {
           // (as below)
-          if (m > 1 && !(ok = mbar_wait_short_warp(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
+          if (m > 1 && !mbar_wait_short_warp(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree)) break;
           if (lane == 0) load_kv(m, t);
         }
-        // every copy has landed before shared memory is released (waits on the
-        // give-up path only: a wait for the ring may have ended the loop, too)
+        // (as the producer's)
         if (lane == 0)
           for (int k = max(0, m - 2); k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
       } else {
         bool more = another(blk, t);  // (its copies are on their way)
-        int m = 1;
+        int m = more ? 1 : 0;
         while (more) {
           blk += stride;
           more = another(blk, t);
           if (!more) break;
           // the buffers are free once dV and dK of the item before the last have
           // left them
-          if (m > 1 && !(ok = mbar_wait_short(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree))) break;
+          if (m > 1 && !mbar_wait_short(bar(C::kBarKVFree), (m - 2) & 1, ctl, kSiteKVFree)) break;
           load_kv(m++, t);
         }
-        if (!ok)
-          for (int k = m - 2; k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
+        for (int k = max(0, m - 2); k < m; ++k) mbar_wait_drain(bar(C::kBarKV + (k & 1)), (k / 2) & 1);
       }
     } else if (kPacked && warp == C::kTrimWarp) {
       // ----------------------------------------------------------- trim
