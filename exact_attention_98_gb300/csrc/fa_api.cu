@@ -946,7 +946,10 @@ int fa_packed_plan(const int* cu_seqlens, int sequences, int rows, int causal, v
 namespace {
 
 // Key ranges that the forward may cut an item into (1: none) in a call of too few items
-// for the SMs; the kernel takes as many as the lengths ask for.  Whole call on the GPU, with
+// for the SMs; the kernel takes as many as the lengths ask for.  The lengths are on the
+// device: here their mean stands for them, empty sequences counted.  So a long sequence
+// beside many short or empty ones is not cut: 16384 rows, H 1, are, with 15 sequences of
+// 20 rows beside them they are not.  Whole call on the GPU, with
 // and without (us; one causal sequence, d = 128): 1500 rows, H 1: 23 and 28; 2048 rows, H 2:
 // 25 and 35; 8192, H 2: 52 and 106; 16384, H 1: 79 and 195.  fp32 parts and the join cost
 // 5 to 10, so that from half the SMs in items on only long sequences gain (H 3, d = 128:
@@ -1032,11 +1035,11 @@ namespace {
 // How many parts the backward cuts each item (key tile of a key head) into; the
 // parts' dK and dV are joined by the kernel after the main one, which costs a part
 // about as much as four query tiles.  By the mean length of a sequence (lengths are
-// not known here), causal: as many parts as leave no SM idle, of two query tiles
-// each; as fill the SMs twice, since items differ by their place, of eight; two where
+// not known here; empty ones count, and what few long ones among short ones would gain
+// is missed), causal: as many parts as leave no SM idle, of two query tiles each; as fill the SMs twice, since items differ by their place, of eight; two where
 // items are long and no more than two to an SM.  At d = 64 no part may be without a
 // query tile (its kernel's ring): as many as a group's heads at most.
-// Measured at d = 128, causal, in all, one part against the rule's:
+// Measured at d = 128, causal, one sequence, one part against the rule's:
 //   1024 rows, H = 16, Hkv = 2     153 us -> 42 (8 parts)
 //   12000 rows, H = 8, Hkv = 1    1605 us -> 578 (3)
 //   4096 rows, H = 16, Hkv = 4     302 us -> 179 (2)

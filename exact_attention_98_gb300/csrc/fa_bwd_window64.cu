@@ -28,8 +28,8 @@
 // of code were 92 us, 68 KB are 67.6 (B = 2, H = Hkv = 16, N = 4096, window 512).
 //
 // What bounds it (same sizes; 67.6 us, 0.6 PFLOP/s of the five products): the
-// chain of a tile, about 2900 cycles: exponentials (1100, the MUFU's rate), dV and
-// the next S^T behind them (900), commit and wake-up; dS and its way through shared
+// chain of a tile, about 2900 cycles: exponentials (1100; 512 at the MUFU's 32 a clock),
+// dV and the next S^T behind them (900), commit and wake-up; dS and its way through shared
 // memory fit beside.  An item's change costs another 3000.
 //
 // dS is formed from P as computed, not as rounded to bf16 for the dV product:
@@ -226,8 +226,9 @@ __device__ __forceinline__ bool next_item(const BwdParams& p, int& blk, int stri
 // sequences, H = Hkv = 16: dealt out in turn, as for windows, 211 us, since the
 // CTAs' sums differ by 28%; off the counter but looked up by every warp 225 (97 KB
 // of code instead of 74); through the ring 202; taken when a CTA is three tiles from its
-// item's end, not an item ahead, 176.  It is 0.76 PFLOP/s of visible pairs; the
-// chain of a tile bounds it as below, the tensor pipe is active for 35% of the time.
+// item's end, not an item ahead, 176, and 174 since the warps' walks of fa_walk.h.  It is
+// 0.77 PFLOP/s of visible pairs; the chain of a tile bounds it as above, the tensor
+// pipe is active for 37% of the time.
 template <bool kPacked>
 __global__ void __launch_bounds__(WinCfg<kPacked>::kThreads, 1)
     fa_bwd_window64_kernel(const __grid_constant__ BwdParams p) {

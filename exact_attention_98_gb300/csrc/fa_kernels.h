@@ -85,7 +85,7 @@ struct FwdParams {
   int sinks;
   int win_tiles;
   FastDiv div_group;
-  // Packed sequences (plan != null; bf16, no split): the rows of all sequences
+  // Packed sequences (plan != null; bf16): the rows of all sequences
   // follow one another, N is their number, and tm_q, tm_k, tm_v and tm_o (box {64,
   // 32, 1}) have one slice per head.  A work item is entry i / units of the plan's list: two
   // query tiles of one head (win_tiles = 2: blocks), or one of two heads (tiles);

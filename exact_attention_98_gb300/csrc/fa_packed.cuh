@@ -72,7 +72,9 @@ __device__ __forceinline__ bool packed_fits(const PackedHead& h, int rows, int s
 // take 5926 us, with the heaviest key tiles of all sequences first 8286.  A causal
 // batch of few tiles takes the heaviest first all the same: there the last CTAs' idle
 // time weighs more (16384 rows of 11 sequences: 325 us instead of 338, both with a
-// sequence's heads in turn).
+// sequence's heads in turn).  The limit counts tiles, not items (tiles times key heads),
+// and lies between two batches measured, both of 4 key heads: these 132 tiles and those
+// of 131072 rows, more than 1000.  Where it lies for 1 or 16 key heads is not known.
 constexpr int kFewTiles = 152;
 struct PackedItem {
   int start, len;  // rows of the sequence

@@ -376,7 +376,10 @@ int fa_packed_plan(const int* cu_seqlens, int sequences, int rows, int causal, v
  *                     irrelevant, a call with too few work items for the SMs (a
  *                     long prompt of few heads) cuts them into key ranges,
  *                     joined by a second kernel as fa_fwd_splitkv's.  0 bytes where
- *                     that does not apply.  Calls in flight at once need one each.
+ *                     that does not apply.  Whether it does is decided by the mean
+ *                     length, rows / sequences, empty sequences counted: a long
+ *                     sequence beside many short or empty ones is not cut.
+ *                     Calls in flight at once need one each.
  *                     FA_ERR_WORKSPACE for a short or misaligned one.
  * K and V have to be finite in the rows of a sequence that hold a row's later keys
  * (a masked pair's weight is an exact 0, and 0 times an infinity or a NaN is not);
@@ -395,8 +398,9 @@ int fa_fwd_packed(const void* plan, int sequences, int rows, const fa_rows* q, c
  *   dout, dq   : in, out: row tensors of H heads; dk, dv: out, of Hkv heads
  *   workspace  : fa_bwd_packed_workspace_bytes() bytes, 256-byte aligned, contents
  *                on entry irrelevant: fp32 D and LSE by heads, the dQ
- *                accumulator and, where key tiles are split over SMs (by
- *                the current device's SM count), the parts of dK and dV.  0 for
+ *                accumulator and, where key tiles are split over SMs (by the
+ *                current device's SM count and the mean length, empty
+ *                sequences counted), the parts of dK and dV.  0 for
  *                empty or unsupported shapes.
  * What rows of the other sequences and padding rows hold does not matter; a
  * sequence's own rows have to be finite, all of them.  rows * H up to 2^31 - 1
